@@ -21,6 +21,7 @@ SCALE_TENSOR, SCALE_ROW, SCALE_BLOCK128, SCALE_MX32 = range(4)
 OUT_BF16, OUT_F32 = range(2)
 MX_POW2_FLOOR, MX_OCP = range(2)
 RECIPE_TENSORWISE, RECIPE_ROWWISE_BF16_WGRAD = range(2)
+GATE_SOFTMAX, GATE_SOFTMAX_TOPK, GATE_SIGMOID = range(3)
 
 EXPORTS = [
     "fp8_probe", "fp8_status_string", "fp8_last_device_error", "fp8_format_max",
@@ -31,6 +32,8 @@ EXPORTS = [
     "fp8_scaled_mm", "fp8_scaled_mm_kpacked",
     "fp8_grouped_mm", "fp8_grouped_mm_kpacked", "fp8_wgrad_bf16", "fp8_grouped_wgrad_bf16", "fp8_linear_fwd", "fp8_linear_bwd",
     "fp8_linear_ws_bytes", "fp8_validate_offsets",
+    "fp8_add_norm_quant_row", "fp8_add_norm_bwd", "fp8_add_norm_bwd_ws_bytes",
+    "fp8_moe_route", "fp8_moe_route_ws_bytes", "fp8_moe_route_bwd", "fp8_moe_few", "fp8_moe_few_ws_bytes",
 ]
 
 
@@ -86,6 +89,14 @@ def load(path: str = LIB_PATH):
         "fp8_linear_bwd": (I, [P, P, P, I64, I64, I64, I, D, P, P, P, SZ, P]),
         "fp8_linear_ws_bytes": (SZ, [I64, I64, I64, I]),
         "fp8_validate_offsets": (I, [P, I32, I64]),
+        "fp8_add_norm_quant_row": (I, [P, P, P, P, I64, I64, I, D, I, D, P, P, P, P, P, P, P, P]),
+        "fp8_add_norm_bwd": (I, [P, P, P, P, P, P, I64, I64, I, P, P, P, P, SZ, P]),
+        "fp8_add_norm_bwd_ws_bytes": (SZ, [I64, I64, I]),
+        "fp8_moe_route": (I, [P, I, I64, I32, I32, I, P, P, P, P, P, P, SZ, P]),
+        "fp8_moe_route_ws_bytes": (SZ, [I64, I32, I32]),
+        "fp8_moe_route_bwd": (I, [P, I, I64, I32, I32, I, P, P, P, P, P]),
+        "fp8_moe_few": (I, [P, P, P, I64, I32, P, P, P, P, I, I32, I64, I64, I, P, P, SZ, P]),
+        "fp8_moe_few_ws_bytes": (SZ, [I64, I32, I64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -136,6 +147,48 @@ def _arg(fn, name, t, nbytes, esize=None):
         raise ValueError(f"{fn}: {name} must have {esize}-byte elements (got {t.dtype})")
     if t.numel() * t.element_size() < nbytes:
         raise ValueError(f"{fn}: {name} holds {t.numel() * t.element_size()} bytes, needs {nbytes}")
+
+
+def _args(fn, *operands):
+    """_arg for each (name, tensor, nbytes, dtype): contiguous, of exactly that dtype, at least
+    nbytes long and on one device, which is returned. A tensor may be None where nbytes is None."""
+    dev = None
+    for name, t, nbytes, dtype in operands:
+        if t is None:
+            if nbytes:
+                raise ValueError(f"{fn}: {name} is required")
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{fn}: {name} must be on the GPU")
+        if dev is None:
+            dev = t.get_device()
+        elif t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} is on another GPU than the operands before it")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{fn}: {name} must be {dtype} (got {t.dtype})")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+        if nbytes and t.nbytes < nbytes:
+            raise ValueError(f"{fn}: {name} holds {t.nbytes} bytes, needs {nbytes}")
+    return dev
+
+
+def _launch(fn, dev, stream, *args):
+    """Calls the library on the operands' device, which need not be the current one, and on
+    `stream` or that device's current stream."""
+    import torch
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev) if dev is not None else 0
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    call = getattr(_lib or load(), fn)
+    if dev is None or dev == torch._C._cuda_getDevice():
+        status = call(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, stream)
+    if status != OK:
+        raise Fp8Error(fn, status)
 
 
 def _offsets(fn, offsets, E):
@@ -439,6 +492,118 @@ def fp8_grouped_wgrad_bf16(gy, x, offsets, gw, stream=None):
     _arg(fn, "gw", gw, 2 * E * N * K, 2)
     _check(fn, load().fp8_grouped_wgrad_bf16(
         _ptr(gy), _ptr(x), _ptr(offsets), E, Mtot, N, K, _ptr(gw), _stream(stream)))
+
+
+# ---- residual norm, expert router, few-token expert layer --------------------------
+
+def fp8_add_norm_quant_row(x, res, gamma, beta, kind, norm_eps, fmt, eps, h, y, q, scale, inv_scale=None, mean=None,
+                           rstd=None, stream=None):
+    """h = bf16(x + res) [rows][cols] (res None: h = x), then y (bf16, or None) and q/scale/inv (rowwise
+    FP8 of y, or q None) as fp8_norm_quant_row of h. h: None, a tensor, x or res. mean (LAYER), rstd
+    [rows] fp32: the statistics fp8_add_norm_bwd takes."""
+    import torch
+    fn, bf, f32 = "fp8_add_norm_quant_row", torch.bfloat16, torch.float32
+    rows, cols = x.shape
+    n = 2 * rows * cols
+    q_rows = 0 if q is None else 4 * rows
+    dev = _args(fn, ("x", x, n, bf), ("res", res, res is not None and n, bf), ("gamma", gamma, 2 * cols, bf),
+                ("beta", beta, beta is not None and 2 * cols, bf), ("h", h, h is not None and n, bf),
+                ("y", y, y is not None and n, bf), ("q", q, q is not None and n // 2, torch.uint8),
+                ("scale", scale, q_rows or (scale is not None and 4 * rows), f32),
+                ("inv_scale", inv_scale, inv_scale is not None and 4 * rows, f32),
+                ("mean", mean, mean is not None and 4 * rows, f32), ("rstd", rstd, rstd is not None and 4 * rows, f32))
+    _launch(fn, dev, stream, _ptr(x), _ptr(res), _ptr(gamma), _ptr(beta), rows, cols, kind, norm_eps, fmt, eps, _ptr(h),
+            _ptr(y), _ptr(q), _ptr(scale), _ptr(inv_scale), _ptr(mean), _ptr(rstd))
+
+
+def fp8_add_norm_bwd_ws_bytes(rows: int, cols: int, kind: int) -> int:
+    return load().fp8_add_norm_bwd_ws_bytes(int(rows), int(cols), int(kind))
+
+
+def fp8_add_norm_bwd(dy, dh, h, gamma, mean, rstd, kind, dx, dgamma, dbeta, ws, stream=None):
+    """dy, h (and dh, or None) [rows][cols] -> dx [rows][cols], dgamma, dbeta [cols] (or None), all bf16."""
+    import torch
+    fn, bf, f32 = "fp8_add_norm_bwd", torch.bfloat16, torch.float32
+    rows, cols = dy.shape
+    n = 2 * rows * cols
+    dev = _args(fn, ("dy", dy, n, bf), ("dh", dh, dh is not None and n, bf), ("h", h, n, bf),
+                ("gamma", gamma, 2 * cols, bf), ("mean", mean, mean is not None and 4 * rows, f32),
+                ("rstd", rstd, 4 * rows, f32), ("dx", dx, n, bf),
+                ("dgamma", dgamma, dgamma is not None and 2 * cols, bf),
+                ("dbeta", dbeta, dbeta is not None and 2 * cols, bf), ("ws", ws, None, None))
+    _launch(fn, dev, stream, _ptr(dy), _ptr(dh), _ptr(h), _ptr(gamma), _ptr(mean), _ptr(rstd), rows, cols, kind,
+            _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), 0 if ws is None else ws.nbytes)
+
+
+def _logits_type(fn, logits):
+    import torch
+    if logits.dtype == torch.float32:
+        return OUT_F32
+    if logits.dtype == torch.bfloat16:
+        return OUT_BF16
+    raise ValueError(f"{fn}: logits must be bfloat16 or float32 (got {logits.dtype})")
+
+
+def fp8_moe_route_ws_bytes(T: int, E: int, k: int) -> int:
+    return load().fp8_moe_route_ws_bytes(int(T), int(E), int(k))
+
+
+def fp8_moe_route(logits, gate, ids, weights, offsets=None, order=None, slot=None, ws=None, stream=None):
+    """logits [T][E] bf16 or fp32 -> ids [T][k] int32, weights [T][k] fp32, and, all or none, offsets
+    [E + 1], order [T * k] and slot [T][k], int32."""
+    import torch
+    fn, i32 = "fp8_moe_route", torch.int32
+    T, E = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"{fn}: ids must be [T][k]")
+    k = ids.shape[1]
+    n = 4 * T * k
+    dev = _args(fn, ("logits", logits, None, None), ("ids", ids, n, i32), ("weights", weights, n, torch.float32),
+                ("offsets", offsets, offsets is not None and 4 * (E + 1), i32),
+                ("order", order, order is not None and n, i32), ("slot", slot, slot is not None and n, i32),
+                ("ws", ws, None, None))
+    _launch(fn, dev, stream, _ptr(logits), _logits_type(fn, logits), T, E, k, gate, _ptr(ids), _ptr(weights),
+            _ptr(offsets), _ptr(order), _ptr(slot), _ptr(ws), 0 if ws is None else ws.nbytes)
+
+
+def fp8_moe_route_bwd(logits, gate, ids, weights, dweights, dlogits, stream=None):
+    """dweights [T][k] fp32 and the forward's logits, ids, weights -> dlogits [T][E] (the logits' type)."""
+    import torch
+    fn, f32 = "fp8_moe_route_bwd", torch.float32
+    T, E = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"{fn}: ids must be [T][k]")
+    k = ids.shape[1]
+    n = 4 * T * k
+    dev = _args(fn, ("logits", logits, None, None), ("ids", ids, n, torch.int32), ("weights", weights, n, f32),
+                ("dweights", dweights, n, f32), ("dlogits", dlogits, logits.nbytes, logits.dtype))
+    _launch(fn, dev, stream, _ptr(logits), _logits_type(fn, logits), T, E, k, gate, _ptr(ids), _ptr(weights),
+            _ptr(dweights), _ptr(dlogits))
+
+
+def fp8_moe_few_ws_bytes(T: int, k: int, F: int) -> int:
+    return load().fp8_moe_few_ws_bytes(int(T), int(k), int(F))
+
+
+def fp8_moe_few(x, ids, weights, w13, w13_inv, w2, w2_inv, fmt, out, ws, packed=False, stream=None):
+    """The expert layer for at most 64 tokens: x [T][D] bf16, ids [T][k] int32, weights [T][k] fp32 ->
+    out [T][D] bf16. w13 holds the e4m3 codes of [E][2F][D] (gate rows, then up rows), w2 those of
+    [E][D][F], with w13_inv [E][2F] and w2_inv [E][D]; packed: k-packed codes."""
+    import torch
+    fn, f32, u8 = "fp8_moe_few", torch.float32, torch.uint8
+    T, D = x.shape
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"{fn}: ids must be [T][k]")
+    if w13_inv.dim() != 2 or w13_inv.shape[1] % 2:
+        raise ValueError(f"{fn}: w13_inv must be [E][2F]")
+    k = ids.shape[1]
+    E, F = w13_inv.shape[0], w13_inv.shape[1] // 2
+    dev = _args(fn, ("x", x, 2 * T * D, torch.bfloat16), ("ids", ids, 4 * T * k, torch.int32),
+                ("weights", weights, 4 * T * k, f32), ("w13", w13, 2 * E * F * D, u8),
+                ("w13_inv", w13_inv, 8 * E * F, f32), ("w2", w2, E * F * D, u8), ("w2_inv", w2_inv, 4 * E * D, f32),
+                ("out", out, 2 * T * D, torch.bfloat16), ("ws", ws, None, None))
+    _launch(fn, dev, stream, _ptr(x), _ptr(ids), _ptr(weights), T, k, _ptr(w13), _ptr(w13_inv), _ptr(w2),
+            _ptr(w2_inv), fmt, E, D, F, 1 if packed else 0, _ptr(out), _ptr(ws), 0 if ws is None else ws.nbytes)
 
 
 # ---- Linear layer -----------------------------------------------------------------

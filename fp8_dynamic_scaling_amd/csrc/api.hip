@@ -5,6 +5,7 @@
 #include <mutex>
 #include <atomic>
 #include <cstring>
+#include <cstdint>
 
 #include "../../include/fp8dyn.h"
 #include "internal.hpp"
@@ -315,6 +316,67 @@ fp8_status fp8_norm_quant_row(const uint16_t* x, const uint16_t* gamma, const ui
   return dev_err(launch_norm_quant_row(a));
 }
 
+fp8_status fp8_add_norm_quant_row(const uint16_t* x, const uint16_t* res, const uint16_t* gamma, const uint16_t* beta,
+                                  int64_t rows, int64_t cols, fp8_norm kind, double norm_eps, fp8_format fmt,
+                                  double eps, uint16_t* h, uint16_t* y, uint8_t* q, float* scale, float* inv_scale,
+                                  float* mean, float* rstd, void* stream) {
+  if (rows < 0 || cols < 0 || bad_eps(eps) || !(std::isfinite(norm_eps) && norm_eps >= 0.0))
+    return FP8_ERR_INVALID_ARGUMENT;
+  if (kind != FP8_NORM_RMS && kind != FP8_NORM_LAYER) return FP8_ERR_INVALID_ARGUMENT;
+  if (kind == FP8_NORM_RMS && (beta || mean)) return FP8_ERR_INVALID_ARGUMENT;
+  if (h && !res) return FP8_ERR_INVALID_ARGUMENT;  // without a residual h is x itself
+  if (rows == 0) return FP8_OK;
+  if (cols == 0) return empty_group_scales(fmt, false, eps, scale, inv_scale, scale ? rows : 0, stream);
+  if (!x || !gamma || (!y && !q) || (q && !scale)) return FP8_ERR_INVALID_ARGUMENT;
+  if (cols % 8 != 0) return FP8_ERR_ALIGNMENT;
+  if (cols > 16384 || rows >= ((int64_t)1 << 31)) return FP8_ERR_UNSUPPORTED;  // the row lives in registers
+  if (!aligned(x, 16) || !aligned(gamma, 16) || (res && !aligned(res, 16)) || (beta && !aligned(beta, 16)) ||
+      (h && !aligned(h, 16)) || (y && !aligned(y, 16)) || (q && !aligned(q, 8)) || (scale && !aligned(scale, 4)) ||
+      (inv_scale && !aligned(inv_scale, 4)) || (mean && !aligned(mean, 4)) || (rstd && !aligned(rstd, 4)))
+    return FP8_ERR_ALIGNMENT;
+  bool e5;
+  double fm;
+  fp8_status st;
+  if ((st = resolve(fmt, &e5, &fm)) != FP8_OK) return st;
+  NormQuantArgs a{x, gamma, beta, rows, cols, kind == FP8_NORM_LAYER, norm_eps, e5, fm, eps, y, q, scale, inv_scale,
+                  (hipStream_t)stream, res, h, mean, rstd};
+  return dev_err(launch_add_norm_quant_row(a));
+}
+
+size_t fp8_add_norm_bwd_ws_bytes(int64_t rows, int64_t cols, fp8_norm kind) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return (size_t)norm_bwd_ws_floats(rows, cols, kind == FP8_NORM_LAYER) * 4;
+}
+
+fp8_status fp8_add_norm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* gamma,
+                            const float* mean, const float* rstd, int64_t rows, int64_t cols, fp8_norm kind,
+                            uint16_t* dx, uint16_t* dgamma, uint16_t* dbeta, void* ws, size_t ws_bytes,
+                            void* stream) {
+  if (rows < 0 || cols < 0) return FP8_ERR_INVALID_ARGUMENT;
+  if (kind != FP8_NORM_RMS && kind != FP8_NORM_LAYER) return FP8_ERR_INVALID_ARGUMENT;
+  if (kind == FP8_NORM_RMS && (mean || dbeta)) return FP8_ERR_INVALID_ARGUMENT;
+  if (cols == 0) return FP8_OK;
+  if (cols % 8 != 0) return FP8_ERR_ALIGNMENT;
+  if ((dgamma && !aligned(dgamma, 2)) || (dbeta && !aligned(dbeta, 2))) return FP8_ERR_ALIGNMENT;
+  if (rows == 0) {  // no rows: the empty sum
+    fp8_status st = dgamma ? dev_err(launch_zero_fill(dgamma, cols * 2, (hipStream_t)stream)) : FP8_OK;
+    if (st == FP8_OK && dbeta) st = dev_err(launch_zero_fill(dbeta, cols * 2, (hipStream_t)stream));
+    return st;
+  }
+  if (!dy || !h || !gamma || !rstd || !dx || (kind == FP8_NORM_LAYER && !mean)) return FP8_ERR_INVALID_ARGUMENT;
+  if (cols > 16384) return FP8_ERR_UNSUPPORTED;
+  if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(gamma, 16) || (dh && !aligned(dh, 16)) || !aligned(dx, 16) ||
+      !aligned(rstd, 4) || (mean && !aligned(mean, 4)))
+    return FP8_ERR_ALIGNMENT;
+  if (dgamma || dbeta) {
+    if (!ws || ws_bytes < fp8_add_norm_bwd_ws_bytes(rows, cols, kind)) return FP8_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return FP8_ERR_ALIGNMENT;
+  }
+  NormBwdArgs a{dy, dh, h, gamma, mean, rstd, rows, cols, kind == FP8_NORM_LAYER, dx, dgamma, dbeta, (float*)ws,
+                (hipStream_t)stream};
+  return dev_err(launch_norm_bwd(a));
+}
+
 size_t fp8_quant_dual_ws_bytes(void) { return 256; }
 
 fp8_status fp8_quant_dual(const uint16_t* gy, const uint16_t* x, int64_t M, int64_t N, int64_t K, fp8_format g_fmt,
@@ -536,6 +598,89 @@ fp8_status fp8_grouped_wgrad_bf16(const uint16_t* gy, const uint16_t* x, const i
   if (32 * (N > K ? N : K) * 2 >= ((int64_t)1 << 31)) return FP8_ERR_UNSUPPORTED;
   GroupedWgradArgs w{gy, x, offsets, E, Mtot, N, K, gw, (hipStream_t)stream};
   return dev_err(launch_grouped_wgrad_bf16(w));
+}
+
+static fp8_status check_route(fp8_out logits_type, int64_t T, int32_t E, int32_t k, fp8_gate gate) {
+  if (T < 0 || E < 1 || k < 1 || k > E) return FP8_ERR_INVALID_ARGUMENT;
+  if (logits_type != FP8_OUT_BF16 && logits_type != FP8_OUT_F32) return FP8_ERR_INVALID_ARGUMENT;
+  if ((int)gate < 0 || (int)gate > 2) return FP8_ERR_INVALID_ARGUMENT;
+  // an expert's logits live in registers; pairs are numbered in 32 bits
+  if (E > 1024 || k > 32 || T > INT32_MAX / k) return FP8_ERR_UNSUPPORTED;
+  return FP8_OK;
+}
+
+size_t fp8_moe_route_ws_bytes(int64_t T, int32_t E, int32_t k) {
+  if (check_route(FP8_OUT_BF16, T, E, k, FP8_GATE_SOFTMAX) != FP8_OK) return 0;
+  return (size_t)route_ws_words(T, E) * 4;
+}
+
+fp8_status fp8_moe_route(const void* logits, fp8_out logits_type, int64_t T, int32_t E, int32_t k, fp8_gate gate,
+                         int32_t* ids, float* weights, int32_t* offsets, int32_t* order, int32_t* slot, void* ws,
+                         size_t ws_bytes, void* stream) {
+  fp8_status st = check_route(logits_type, T, E, k, gate);
+  if (st != FP8_OK) return st;
+  if (!aligned(offsets, 4) || !aligned(order, 4) || !aligned(slot, 4)) return FP8_ERR_ALIGNMENT;
+  if (T == 0) return offsets ? dev_err(launch_zero_fill(offsets, 4 * ((int64_t)E + 1), (hipStream_t)stream)) : FP8_OK;
+  if (!logits || !ids || !weights) return FP8_ERR_INVALID_ARGUMENT;
+  if ((offsets || order || slot) && !(offsets && order && slot)) return FP8_ERR_INVALID_ARGUMENT;
+  if (!aligned(logits, logits_type == FP8_OUT_F32 ? 4 : 2) || !aligned(ids, 4) || !aligned(weights, 4))
+    return FP8_ERR_ALIGNMENT;
+  if (offsets && route_ws_words(T, E) > 0) {
+    if (!ws || ws_bytes < fp8_moe_route_ws_bytes(T, E, k)) return FP8_ERR_WORKSPACE;
+    if (!aligned(ws, 4)) return FP8_ERR_ALIGNMENT;
+  }
+  RouteArgs a{logits, logits_type == FP8_OUT_F32, T, E, k, (int)gate, ids, weights, offsets, order, slot,
+              (uint32_t*)ws, (hipStream_t)stream};
+  return dev_err(launch_moe_route(a));
+}
+
+fp8_status fp8_moe_route_bwd(const void* logits, fp8_out logits_type, int64_t T, int32_t E, int32_t k, fp8_gate gate,
+                             const int32_t* ids, const float* weights, const float* dweights, void* dlogits,
+                             void* stream) {
+  fp8_status st = check_route(logits_type, T, E, k, gate);
+  if (st != FP8_OK || T == 0) return st;
+  if (!logits || !ids || !weights || !dweights || !dlogits) return FP8_ERR_INVALID_ARGUMENT;
+  const size_t esz = logits_type == FP8_OUT_F32 ? 4 : 2;
+  if (!aligned(logits, esz) || !aligned(dlogits, esz) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(dweights, 4))
+    return FP8_ERR_ALIGNMENT;
+  RouteBwdArgs a{logits, logits_type == FP8_OUT_F32, T, E, k, (int)gate, ids, weights, dweights, dlogits,
+                 (hipStream_t)stream};
+  return dev_err(launch_moe_route_bwd(a));
+}
+
+size_t fp8_moe_few_ws_bytes(int64_t T, int32_t k, int64_t F) {
+  if (T <= 0 || T > 64 || k <= 0 || k > 32 || F <= 0 || F >= (1 << 24)) return 0;
+  return (size_t)T * k * F * 2;
+}
+
+fp8_status fp8_moe_few(const uint16_t* x, const int32_t* ids, const float* weights, int64_t T, int32_t k,
+                       const uint8_t* w13, const float* w13_inv, const uint8_t* w2, const float* w2_inv,
+                       fp8_format fmt, int32_t E, int64_t D, int64_t F, int packed, uint16_t* out, void* ws,
+                       size_t ws_bytes, void* stream) {
+  if (T < 0 || k < 1 || E < 1 || D < 0 || F < 0) return FP8_ERR_INVALID_ARGUMENT;
+  if (T > 64 || k > 32 || E > 1024 || D >= (1 << 24) || F >= (1 << 24)) return FP8_ERR_UNSUPPORTED;
+  const int step = packed ? 64 : 16;
+  if (D % step != 0 || F % step != 0) return FP8_ERR_ALIGNMENT;
+  if (T == 0 || D == 0) return FP8_OK;
+  if (!out) return FP8_ERR_INVALID_ARGUMENT;
+  if (!aligned(out, 16)) return FP8_ERR_ALIGNMENT;
+  if (F == 0) return dev_err(launch_zero_fill(out, T * D * 2, (hipStream_t)stream));  // the empty sum
+  if (!x || !ids || !weights || !w13 || !w13_inv || !w2 || !w2_inv) return FP8_ERR_INVALID_ARGUMENT;
+  if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(w13_inv, 4) || !aligned(w2_inv, 4))
+    return FP8_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < fp8_moe_few_ws_bytes(T, k, F)) return FP8_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return FP8_ERR_ALIGNMENT;
+  bool e5;
+  double fm;
+  fp8_status st;
+  if (fmt == FP8_E5M2 || fmt == FP8_E5M2FNUZ || fmt == FP8_E5M2_NATIVE) return FP8_ERR_UNSUPPORTED;
+  if ((st = resolve(fmt, &e5, &fm)) != FP8_OK) return st;
+  if (e5 || fm != 448.0) return FP8_ERR_UNSUPPORTED;  // the decode is that of e4m3fn
+  MoeFewArgs a{x, ids, weights, w13, w13_inv, w2, w2_inv, T, E, k, D, F, packed != 0, out, (uint16_t*)ws,
+               (hipStream_t)stream};
+  return dev_err(launch_moe_few(a));
 }
 
 fp8_status fp8_validate_offsets(const int32_t* host_offsets, int32_t E, int64_t Mtot) {

@@ -49,8 +49,85 @@ struct NormQuantArgs {
   float* scale;
   float* inv;
   hipStream_t stream;
+  // launch_add_norm_quant_row only: the row normalized is h = bf16(x + res)
+  const uint16_t* res = nullptr;  // or nullptr: h = x
+  uint16_t* h = nullptr;          // written when set and res is; may be x or res
+  float* mean = nullptr;          // mean32, rstd32 of each row, written when set
+  float* rstd = nullptr;
 };
 hipError_t launch_norm_quant_row(const NormQuantArgs& a);
+hipError_t launch_add_norm_quant_row(const NormQuantArgs& a);
+
+// Backward of the row normalization, with the residual stream's gradient.
+struct NormBwdArgs {
+  const uint16_t* dy;     // [rows][cols]
+  const uint16_t* dh;     // [rows][cols] or nullptr
+  const uint16_t* h;      // [rows][cols], the normalized rows
+  const uint16_t* gamma;  // [cols]
+  const float* mean;      // [rows] (LayerNorm)
+  const float* rstd;      // [rows]
+  int64_t rows, cols;     // cols % 8 == 0, cols <= 16384
+  bool layer;
+  uint16_t* dx;           // [rows][cols]; may be dy or dh
+  uint16_t* dgamma;       // [cols] or nullptr
+  uint16_t* dbeta;        // [cols] or nullptr
+  float* ws;              // norm_bwd_ws_floats()
+  hipStream_t stream;
+};
+hipError_t launch_norm_bwd(const NormBwdArgs& a);
+int64_t norm_bwd_ws_floats(int64_t rows, int64_t cols, bool layer);
+
+// Expert router: the k largest logits of each token, gate weights, and the
+// rows sorted by expert.
+enum GateKind : int { kGateSoftmax = 0, kGateSoftmaxTopk = 1, kGateSigmoid = 2 };
+struct RouteArgs {
+  const void* logits;  // [T][E], bf16 or fp32
+  bool f32;
+  int64_t T;           // T * k < 2^31
+  int32_t E, k;        // E <= 1024, 1 <= k <= min(E, 32)
+  int gate;
+  int32_t* ids;        // [T][k]
+  float* weights;      // [T][k]
+  int32_t* offsets;    // [E + 1], or nullptr (then order and slot too)
+  int32_t* order;      // [T * k]
+  int32_t* slot;       // [T][k]
+  uint32_t* ws;        // route_ws_words()
+  hipStream_t stream;
+};
+hipError_t launch_moe_route(const RouteArgs& a);
+int64_t route_ws_words(int64_t T, int32_t E);
+struct RouteBwdArgs {
+  const void* logits;
+  bool f32;
+  int64_t T;
+  int32_t E, k;
+  int gate;
+  const int32_t* ids;
+  const float* weights;
+  const float* dweights;
+  void* dlogits;       // [T][E], the logits' type; may be logits itself
+  hipStream_t stream;
+};
+hipError_t launch_moe_route_bwd(const RouteBwdArgs& a);
+
+// Mixture-of-experts layer for a few tokens.
+struct MoeFewArgs {
+  const uint16_t* x;      // [T][D] bf16
+  const int32_t* ids;     // [T][k]; outside [0, E): no expert
+  const float* weights;   // [T][k]
+  const uint8_t* w13;     // [E][2F][D] e4m3, gate rows first
+  const float* inv13;     // [E][2F]
+  const uint8_t* w2;      // [E][D][F] e4m3
+  const float* inv2;      // [E][D]
+  int64_t T;              // <= 64
+  int32_t E, k;           // E <= 1024, k <= 32
+  int64_t D, F;           // % 16 == 0 (packed: % 64 == 0), < 2^20
+  bool packed;
+  uint16_t* out;          // [T][D]
+  uint16_t* act;          // workspace [T * k][F] bf16
+  hipStream_t stream;
+};
+hipError_t launch_moe_few(const MoeFewArgs& a);
 
 // Tensorwise quantization of up to kMaxTJobs tensors in three launches (clear
 // the amax words, amax of every tensor, one cast launch): each tensor gets its

@@ -1261,13 +1261,26 @@ __device__ __forceinline__ void exact_add(uint32_t b, long long* L1, long long* 
   if (t >> 32) atomicAdd(reinterpret_cast<unsigned long long*>(&L2[(s2 >> 5) + 1]), (unsigned long long)(t >> 32));
 }
 
-template <int TPR, int J, bool E5, bool LAYER>
-__global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* __restrict__ x,
-                                                        const uint16_t* __restrict__ gamma,
+// ADD: the row is the residual stream h = bf16(x + res) (one fp32 addition,
+// rounded to bf16: the stream is stored in that type, and the norm is that of
+// the stored row, so that a backward pass that reads h sees the same values);
+// res may be null (h = x). h is written where asked, and mean32 and rstd32 for
+// the backward. Each lane writes just the elements of h it has read, after it
+// read them, so h may be x or res itself.
+struct NormAdd {
+  const uint16_t* res;
+  uint16_t* h;
+  float* mean;
+  float* rstd;
+};
+
+template <int TPR, int J, bool E5, bool LAYER, bool ADD>
+__global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const uint16_t* __restrict__ gamma,
                                                         const uint16_t* __restrict__ beta, int64_t rows, int64_t cols,
                                                         double norm_eps, uint16_t* __restrict__ y,
                                                         uint8_t* __restrict__ q, float* __restrict__ scale,
-                                                        float* __restrict__ inv, double fmax, double eps) {
+                                                        float* __restrict__ inv, double fmax, double eps,
+                                                        NormAdd add) {
   // TPR threads per row: 64 (one wavefront per row, 4 rows per workgroup, no
   // barrier; LDS only in the exact-sum path) for rows up to 4096 elements,
   // else 256
@@ -1292,6 +1305,30 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* __restri
   for (int j = 0; j < J; ++j) {
     const int64_t c = 8 * (t + TPR * j);
     v[j] = c < cols ? ld_nt16(xr + c) : make_uint4(0, 0, 0, 0);
+  }
+  if constexpr (ADD) {
+    if (add.res) {
+      uint4 r[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int64_t c = 8 * (t + TPR * j);
+        r[j] = c < cols ? ld_nt16(add.res + row * cols + c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int64_t c = 8 * (t + TPR * j);
+        const uint32_t a[4] = {v[j].x, v[j].y, v[j].z, v[j].w}, b[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bf16x2_t s = {(__bf16)__fadd_rn(bf16_lo(a[k]), bf16_lo(b[k])),
+                              (__bf16)__fadd_rn(bf16_hi(a[k]), bf16_hi(b[k]))};
+          o[k] = __builtin_bit_cast(uint32_t, s);
+        }
+        v[j] = make_uint4(o[0], o[1], o[2], o[3]);
+        if (add.h && c < cols) *reinterpret_cast<uint4*>(add.h + row * cols + c) = v[j];
+      }
+    }
   }
 #pragma unroll
   for (int j = 0; j < J; ++j) {
@@ -1395,6 +1432,13 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* __restri
     mean32 = __double2float_rn(mean);
     rstd32 = __double2float_rn(rstd);
   }
+  if constexpr (ADD) {
+    if (t == 0) {
+      if (add.mean) add.mean[row] = mean32;
+      if (add.rstd) add.rstd[row] = rstd32;
+    }
+    if (!y && !q) return;
+  }
   // normalize, keep as bf16 in registers (and store to y)
   float m = 0.0f;
 #pragma unroll
@@ -1448,36 +1492,46 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* __restri
   }
 }
 
-template <bool E5, bool LAYER>
+template <bool E5, bool LAYER, bool ADD>
 static void launch_norm_quant_t(const NormQuantArgs& a) {
   const dim3 block(256);
+  const NormAdd add{a.res, a.h, a.mean, a.rstd};
   auto go = [&](auto kern, int64_t blocks) {
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), block, 0, a.stream, a.x, a.gamma, a.beta, a.rows, a.cols,
-                       a.norm_eps, a.y, a.q, a.scale, a.inv, a.fmax, a.eps);
+                       a.norm_eps, a.y, a.q, a.scale, a.inv, a.fmax, a.eps, add);
   };
   if (a.cols <= 512 * 8) {  // one wavefront per row
     const int64_t J = (a.cols + 511) / 512, blocks = (a.rows + 3) / 4;
     if (J <= 2)
-      go(k_norm_quant_row<64, 2, E5, LAYER>, blocks);
+      go(k_norm_quant_row<64, 2, E5, LAYER, ADD>, blocks);
     else if (J <= 4)
-      go(k_norm_quant_row<64, 4, E5, LAYER>, blocks);
+      go(k_norm_quant_row<64, 4, E5, LAYER, ADD>, blocks);
     else
-      go(k_norm_quant_row<64, 8, E5, LAYER>, blocks);
+      go(k_norm_quant_row<64, 8, E5, LAYER, ADD>, blocks);
   } else {
     const int64_t J = (a.cols + 2047) / 2048;
     if (J <= 4)
-      go(k_norm_quant_row<256, 4, E5, LAYER>, a.rows);
+      go(k_norm_quant_row<256, 4, E5, LAYER, ADD>, a.rows);
     else
-      go(k_norm_quant_row<256, 8, E5, LAYER>, a.rows);
+      go(k_norm_quant_row<256, 8, E5, LAYER, ADD>, a.rows);
   }
 }
 
 hipError_t launch_norm_quant_row(const NormQuantArgs& a) {
   if (a.rows == 0 || a.cols == 0) return hipSuccess;
   if (a.layer)
-    a.e5 ? launch_norm_quant_t<true, true>(a) : launch_norm_quant_t<false, true>(a);
+    a.e5 ? launch_norm_quant_t<true, true, false>(a) : launch_norm_quant_t<false, true, false>(a);
   else
-    a.e5 ? launch_norm_quant_t<true, false>(a) : launch_norm_quant_t<false, false>(a);
+    a.e5 ? launch_norm_quant_t<true, false, false>(a) : launch_norm_quant_t<false, false, false>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_add_norm_quant_row(const NormQuantArgs& a) {
+  if (a.rows == 0 || a.cols == 0) return hipSuccess;
+  if (a.layer)
+    a.e5 ? launch_norm_quant_t<true, true, true>(a) : launch_norm_quant_t<false, true, true>(a);
+  else
+    a.e5 ? launch_norm_quant_t<true, false, true>(a) : launch_norm_quant_t<false, false, true>(a);
   return hipGetLastError();
 }
 

@@ -112,6 +112,13 @@ typedef enum {
     FP8_RECIPE_ROWWISE_BF16_WGRAD = 1 /* rowwise FP8 forward and grad-input; BF16 grad-weight */
 } fp8_recipe;
 
+/* Gate weights of a token's chosen experts (fp8_moe_route). */
+typedef enum {
+    FP8_GATE_SOFTMAX = 0,      /* softmax over all experts, the chosen ones' values */
+    FP8_GATE_SOFTMAX_TOPK = 1, /* softmax over the chosen experts (they sum to 1) */
+    FP8_GATE_SIGMOID = 2       /* sigmoid of each chosen logit */
+} fp8_gate;
+
 /* ---- device facts -------------------------------------------------------- */
 
 /* Measures, on `device`, which e4m3 and e5m2 variants the hardware FP8
@@ -237,6 +244,40 @@ FP8DYN_API fp8_status fp8_norm_quant_row(const uint16_t* x, const uint16_t* gamm
                                          int64_t rows, int64_t cols, fp8_norm kind, double norm_eps,
                                          fp8_format fmt, double eps, uint16_t* y, uint8_t* q, float* scale,
                                          float* inv_scale, void* stream);
+
+/* fp8_norm_quant_row of the residual stream, with the residual's addition in
+ * the same pass: per row, h = bf16(x + res) (one fp32 addition, RNE), then y, q,
+ * scale and inv_scale as fp8_norm_quant_row(h) writes them, bit for bit. h
+ * [rows][cols] is written if non-NULL (the stream that the next addition
+ * takes) and may be x or res itself; res may be NULL (then h = x, and h must be
+ * NULL). mean [rows] (LAYER only) and rstd [rows] are mean32 and rstd32,
+ * written if non-NULL, for fp8_add_norm_bwd. y or q (or both) must be given; y
+ * and q overlap no input. Limits, alignment and formats as for
+ * fp8_norm_quant_row; rows < 2^31. */
+FP8DYN_API fp8_status fp8_add_norm_quant_row(const uint16_t* x, const uint16_t* res, const uint16_t* gamma,
+                                             const uint16_t* beta, int64_t rows, int64_t cols, fp8_norm kind,
+                                             double norm_eps, fp8_format fmt, double eps, uint16_t* h, uint16_t* y,
+                                             uint8_t* q, float* scale, float* inv_scale, float* mean, float* rstd,
+                                             void* stream);
+
+/* Backward of fp8_add_norm_quant_row's y and h. dy [rows][cols]: the gradient
+ * of y; dh [rows][cols] or NULL (zeros): the gradient that reaches h from the
+ * stream behind it; h, mean (LAYER) and rstd: the forward's. With xh =
+ * (h - mean) * rstd and g = dy * gamma, in fp32:
+ *   dx = dh + rstd * (g - mean(g) [LAYER only] - xh * mean(g * xh)),
+ * the gradient of x and of res alike; dgamma = sum over rows of dy * xh, dbeta
+ * [LAYER only] = sum over rows of dy, summed in fp32 in a fixed order. All
+ * written as bf16 (RNE). dx may be dy or dh itself; dgamma, dbeta may be NULL
+ * (not wanted; with both NULL no workspace is needed). rows = 0 writes zeros
+ * to dgamma and dbeta. cols % 8 == 0, 16-byte aligned dy, dh, h, gamma, dx
+ * (else FP8_ERR_ALIGNMENT), cols <= 16384 (else FP8_ERR_UNSUPPORTED). ws:
+ * fp8_add_norm_bwd_ws_bytes(rows, cols, kind) bytes, 16-byte aligned, content
+ * on entry of no matter; calls that may run at the same time need one each. */
+FP8DYN_API fp8_status fp8_add_norm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h,
+                                       const uint16_t* gamma, const float* mean, const float* rstd, int64_t rows,
+                                       int64_t cols, fp8_norm kind, uint16_t* dx, uint16_t* dgamma, uint16_t* dbeta,
+                                       void* ws, size_t ws_bytes, void* stream);
+FP8DYN_API size_t fp8_add_norm_bwd_ws_bytes(int64_t rows, int64_t cols, fp8_norm kind);
 
 /* Dual tensorwise quantization for the all-FP8 Linear backward ["FP8
  * Training: Quantization, Autograd, Torchao" section 4: grad_weight =
@@ -389,6 +430,67 @@ FP8DYN_API fp8_status fp8_wgrad_bf16(const uint16_t* gy, const uint16_t* x, int6
 FP8DYN_API fp8_status fp8_grouped_wgrad_bf16(const uint16_t* gy, const uint16_t* x, const int32_t* offsets,
                                              int32_t E, int64_t Mtot, int64_t N, int64_t K, uint16_t* gw,
                                              void* stream);
+
+/* ---- mixture of experts around the grouped GEMM -----------------------------------
+ * [P-AMD "Scaling FP8 to MoE Architectures" Figure 3: the offset tensor that
+ * routes rows to experts]. */
+
+/* The router: for each of T tokens the k largest of its E logits (logits
+ * [T][E] row-major, bf16 or fp32 by logits_type; equal logits: the lowest
+ * expert first), as ids [T][k] in falling order of the logit, and their gate
+ * weights [T][k], fp32. A logit of -inf masks an expert: it is never chosen, and
+ * a token with fewer than k others gets id -1 and weight 0 in the slots left (a
+ * padding row of -inf: in all of them). A NaN logit is never chosen either, and
+ * makes the weights of its token NaN. Where offsets, order and slot are given
+ * (all or none) the chosen pairs are also sorted by expert, tokens in order
+ * within one (a stable sort, the same on every run): offsets [E + 1], as
+ * fp8_grouped_mm takes them (offsets[E] pairs in all); order [T * k]: the pair
+ * t * k + j of each sorted row, -1 behind the last; slot [T][k]: the sorted row
+ * of each pair, -1 where there is none. T = 0 writes zeros to offsets. E <= 1024,
+ * k <= 32, T * k < 2^31 (else FP8_ERR_UNSUPPORTED); k <= E. ws:
+ * fp8_moe_route_ws_bytes(T, E, k) bytes (0 up to 64 tokens, or without
+ * offsets), 4-byte aligned, content on entry of no matter; calls that may run
+ * at the same time need one each. */
+FP8DYN_API fp8_status fp8_moe_route(const void* logits, fp8_out logits_type, int64_t T, int32_t E, int32_t k,
+                                    fp8_gate gate, int32_t* ids, float* weights, int32_t* offsets, int32_t* order,
+                                    int32_t* slot, void* ws, size_t ws_bytes, void* stream);
+FP8DYN_API size_t fp8_moe_route_ws_bytes(int64_t T, int32_t E, int32_t k);
+
+/* Gradient of the gate weights: dlogits [T][E] (the logits' type, every element
+ * written) from dweights [T][k] fp32 and the forward's logits, ids and weights.
+ * With w the weights and p the softmax over all experts:
+ *   SOFTMAX       dl_e = p_e * (dw_e [e chosen] - sum over chosen of w * dw)
+ *   SOFTMAX_TOPK  dl_e = w_e * (dw_e - sum over chosen of w * dw), chosen only
+ *   SIGMOID       dl_e = w_e * (1 - w_e) * dw_e, chosen only
+ * and 0 elsewhere. The choice itself has no gradient. dlogits may be logits.
+ * Limits as for fp8_moe_route. */
+FP8DYN_API fp8_status fp8_moe_route_bwd(const void* logits, fp8_out logits_type, int64_t T, int32_t E, int32_t k,
+                                        fp8_gate gate, const int32_t* ids, const float* weights,
+                                        const float* dweights, void* dlogits, void* stream);
+
+/* A mixture-of-experts layer for a few tokens (T <= 64, else
+ * FP8_ERR_UNSUPPORTED), as serving meets them, in two launches:
+ *   a[t][j] = weights[t][j] * silu(x_t Wg_e^T) * (x_t Wu_e^T),  e = ids[t][j]
+ *   out[t]  = sum over j of a[t][j] W2_e^T
+ * x [T][D] bf16; ids, weights [T][k] as fp8_moe_route writes them. w13
+ * [E][2F][D]: the e4m3 codes of the gate rows, then the up rows, w13_inv
+ * [E][2F] their inverse scales; w2 [E][D][F], w2_inv [E][D]: as fp8_quant_row
+ * writes them, or with packed nonzero as fp8_quant_row_kpacked does, the
+ * operands of fp8_grouped_mm(_kpacked). Only the named experts' codes are read,
+ * once. x is not quantized: the products are bf16 (codes decoded exactly) with
+ * fp32 sums; a is rounded to bf16 once, out [T][D] to bf16 once. An id outside
+ * [0, E) names no expert; one that a token names twice counts with the sum of
+ * its weights; a token that names none gets zeros. The order of all sums is
+ * fixed. D % 16 == 0 and F % 16 == 0 (packed: % 64), 16-byte aligned x, w13, w2,
+ * out, ws (else FP8_ERR_ALIGNMENT); k <= 32, E <= 1024, D, F < 2^24 (else
+ * FP8_ERR_UNSUPPORTED); fmt the native e4m3. F = 0 writes zeros. ws:
+ * fp8_moe_few_ws_bytes(T, k, F) = 2 * T * k * F bytes, content on entry of no
+ * matter; calls that may run at the same time need one each. */
+FP8DYN_API fp8_status fp8_moe_few(const uint16_t* x, const int32_t* ids, const float* weights, int64_t T, int32_t k,
+                                  const uint8_t* w13, const float* w13_inv, const uint8_t* w2, const float* w2_inv,
+                                  fp8_format fmt, int32_t E, int64_t D, int64_t F, int packed, uint16_t* out,
+                                  void* ws, size_t ws_bytes, void* stream);
+FP8DYN_API size_t fp8_moe_few_ws_bytes(int64_t T, int32_t k, int64_t F);
 
 /* ---- one Linear layer [P-TAO section 6; P-AMD "AMD FP8 format in TorchAO"] ---
  * Forward y = x w^T: x [M][K], w [N][K] bf16; quantize both (TENSORWISE: one
