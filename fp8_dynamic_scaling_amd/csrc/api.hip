@@ -651,7 +651,7 @@ fp8_status fp8_moe_route_bwd(const void* logits, fp8_out logits_type, int64_t T,
 
 size_t fp8_moe_few_ws_bytes(int64_t T, int32_t k, int64_t F) {
   if (T <= 0 || T > 64 || k <= 0 || k > 32 || F <= 0 || F >= (1 << 24)) return 0;
-  return (size_t)T * k * F * 2;
+  return moe_few_ws_bytes(T, k, F);
 }
 
 fp8_status fp8_moe_few(const uint16_t* x, const int32_t* ids, const float* weights, int64_t T, int32_t k,

@@ -124,10 +124,11 @@ struct MoeFewArgs {
   int64_t D, F;           // % 16 == 0 (packed: % 64 == 0), < 2^20
   bool packed;
   uint16_t* out;          // [T][D]
-  uint16_t* act;          // workspace [T * k][F] bf16
+  uint16_t* act;          // workspace, moe_few_ws_bytes(): [T * k][F] bf16 and the experts' tokens
   hipStream_t stream;
 };
-hipError_t launch_moe_few(const MoeFewArgs& a);
+hipError_t launch_moe_few(const MoeFewArgs& a);  // F > 0
+size_t moe_few_ws_bytes(int64_t T, int k, int64_t F);
 
 // Tensorwise quantization of up to kMaxTJobs tensors in three launches (clear
 // the amax words, amax of every tensor, one cast launch): each tensor gets its

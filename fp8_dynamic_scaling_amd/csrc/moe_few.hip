@@ -10,14 +10,17 @@
 // and multiplied by 16 tokens at a time with the BF16 matrix-core instruction,
 // which sums at fp32 precision; x and a are bf16 and come from the caches.
 //  - k_moe_up: a workgroup has one expert and 16 gate and 16 up rows; its waves
-//    share D among them, so that thousands of waves each read some 20 KB and all
-//    of their loads are in flight at once. The waves' partial sums meet in LDS,
-//    in a fixed order.
+//    share D among them. The waves' partial sums meet in LDS, in a fixed order.
 //  - k_moe_down: a workgroup has 16 rows of D for all experts; its waves share
-//    the (expert, piece of F) units. A token's sum over its experts stays in
-//    fp32 registers, so no partial output is written and no atomics are needed:
-//    the same inputs give the same bits.
-// The rounding of a to bf16 (with its gate weight, half a step: 2^-9 relative)
+//    the (expert, piece of F) units. A wave adds what it has of a token to its
+//    own fp32 sums in LDS, and the waves' sums are added in order at the end: no
+//    partial output in memory and no atomics, so the same inputs give the same
+//    bits.
+// A wave's unit of work is 16 rows (k_moe_up: twice 16) x 128 values of the
+// contraction and the same 128 values of its tokens; the loads of the next
+// units are in flight while one is multiplied. An expert's tokens are compacted
+// into tiles of 16.
+// The rounding of a to bf16 (with its gate weight, half a step: 2^-8 relative)
 // is that of the activations the grouped GEMMs take; everything else is fp32
 // up to the one rounding of the output.
 //
@@ -28,11 +31,32 @@
 namespace fp8dyn {
 
 namespace {
-constexpr int kUpWaves = 8;
+constexpr int kUpWaves = 4;
 constexpr int kDownWaves = 8;
 constexpr int kFewT = 64;
 constexpr int kFewK = 32;
+
+// What k_moe_up leaves in the workspace for k_moe_down, behind a: the number of
+// named experts, each one's id and number of tokens, and its pairs (t * k + j).
+struct FewMeta {
+  int32_t* head;   // [0] the number of experts
+  int32_t* expert;  // [T * k]
+  int32_t* count;   // [T * k]
+  uint16_t* pairs;  // [T * k][kFewT]
+};
+__host__ __device__ inline FewMeta few_meta(uint16_t* act, int64_t T, int k, int64_t F) {
+  FewMeta m;
+  m.head = reinterpret_cast<int32_t*>(act + T * k * F);
+  m.expert = m.head + 4;
+  m.count = m.expert + T * k;
+  m.pairs = reinterpret_cast<uint16_t*>(m.count + T * k);
+  return m;
+}
 }  // namespace
+
+size_t moe_few_ws_bytes(int64_t T, int k, int64_t F) {
+  return (size_t)(T * k) * (2 * F + 8 + 2 * kFewT) + 16;
+}
 
 // Eight e4m3 codes -> eight bf16 (every e4m3 value is a bf16 value).
 __device__ __forceinline__ v8bf decode8(uint32_t d0, uint32_t d1) {
@@ -43,14 +67,96 @@ __device__ __forceinline__ v8bf decode8(uint32_t d0, uint32_t d1) {
   return (v8bf){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// Byte offset of the 16 codes (row, kc .. kc + 15) of an [N][K] matrix.
+// 16-byte pieces of a row-major or k-packed [N][K] matrix of codes: where the
+// lane's piece of rows [16 i, 16 i + 16) begins, and the bytes from one 64-value
+// step of the contraction to the next (the packed 1 KB chunks of 16 x 64 follow
+// each other).
 template <bool PACKED>
-__device__ __forceinline__ int64_t code_at(int64_t row, int64_t kc, int64_t K) {
-  if constexpr (PACKED)
-    return ((row >> 4) * (K >> 6) + (kc >> 6)) * 1024 + (row & 15) * 64 + (kc & 63);
-  else
-    return row * K + kc;
+__device__ __forceinline__ const uint8_t* code_ptr(const uint8_t* w, int64_t row0, int64_t K) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4;
+  return PACKED ? w + row0 * K + lr * 64 + kg * 16 : w + (row0 + lr) * K + kg * 16;
 }
+template <bool PACKED>
+constexpr int kStep = PACKED ? 1024 : 64;
+
+// The operands of one unit, 128 values of the contraction: R tiles of 16 weight
+// rows (lane: row l & 15, values 16 (l >> 4) .. + 15 of each 64) and NT tiles of
+// 16 tokens (lane: token l & 15, the same values).
+template <int R, int NT>
+struct Unit {
+  uint4 w[R][2];
+  uint4 x[NT][4];
+};
+
+template <int R, int NT, bool PACKED>
+__device__ __forceinline__ void load_unit(Unit<R, NT>& s, const uint8_t* const (&wp)[R],
+                                          const uint16_t* const (&xp)[NT], int u, int K) {
+  const int kg = (threadIdx.x & 63) >> 4;
+  const bool full = 128 * (u + 1) <= K;  // else lanes past K hold zeros
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const bool in = full || 128 * u + 64 * h + 16 * kg < K;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      s.w[r][h] = in ? ld_nt16(wp[r] + (int64_t)(2 * u + h) * kStep<PACKED>) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint4* q = reinterpret_cast<const uint4*>(xp[n] + 128 * u + 64 * h);
+      s.x[n][2 * h] = in ? q[0] : make_uint4(0, 0, 0, 0);
+      s.x[n][2 * h + 1] = in ? q[1] : make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+template <int R, int NT>
+__device__ __forceinline__ void multiply_unit(const Unit<R, NT>& s, v4f (&acc)[R][NT]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    v8bf a[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      a[2 * h] = decode8(s.w[r][h].x, s.w[r][h].y);
+      a[2 * h + 1] = decode8(s.w[r][h].z, s.w[r][h].w);
+    }
+    // two wait states between the converts and the matrix instructions
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 1" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const v8bf b = __builtin_bit_cast(v8bf, s.x[n][q]);
+        acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], b, acc[r][n], 0, 0, 0);
+        keep_live(b);
+      }
+    }
+    asm volatile("" ::"v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]));
+  }
+}
+
+// acc += the products of units [u0, u1), P of them in flight.
+template <int R, int NT, int P, bool PACKED>
+__device__ __forceinline__ void stream_units(const uint8_t* const (&wp)[R], const uint16_t* const (&xp)[NT], int u0,
+                                             int u1, int K, v4f (&acc)[R][NT]) {
+  Unit<R, NT> s[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (u0 + i < u1) load_unit<R, NT, PACKED>(s[i], wp, xp, u0 + i, K);
+  for (int u = u0; u < u1; u += P) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (u + i >= u1) break;
+      multiply_unit<R, NT>(s[i], acc);
+      if (u + i + P < u1) load_unit<R, NT, PACKED>(s[i], wp, xp, u + i + P, K);
+    }
+  }
+}
+
+// Units in flight by the tiles of tokens: the registers of P units, 16 R + 16 NT
+// each, stay near 128.
+template <int NT>
+constexpr int kInFlight = NT == 1 ? 4 : NT == 2 ? 3 : 2;
 
 // The ids in LDS and a bit for each expert that some token names.
 __device__ __forceinline__ void few_ids(const int32_t* __restrict__ ids, int n, int E, int32_t* sid, uint32_t* bits) {
@@ -84,75 +190,34 @@ __device__ __forceinline__ int few_expert(const uint32_t* bits, int s) {
   return 32 * word + __ffs(v) - 1;
 }
 
-// One wave's products of 16 weight rows with NT tiles of 16 tokens over a unit of
-// 128 values of the contraction: w holds two 16-byte pieces a lane (64 values
-// apart), x the same values of the lane's tokens.
-template <int NT>
-__device__ __forceinline__ void unit_products(const uint4 (&w)[2], const uint4 (&x)[NT][4], v4f (&acc)[NT]) {
-  v8bf a[4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    a[2 * h] = decode8(w[h].x, w[h].y);
-    a[2 * h + 1] = decode8(w[h].z, w[h].w);
-  }
-  // two wait states between the converts and the matrix instructions
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_nop 1" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const v8bf b = __builtin_bit_cast(v8bf, x[n][q]);
-      acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], b, acc[n], 0, 0, 0);
-      keep_live(b);
-    }
-  }
-  asm volatile("" ::"v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]));
-}
-
 template <int NT, bool PACKED>
 __device__ __forceinline__ void moe_up_tile(const MoeFewArgs& p, int e, int m, const int32_t* list, int64_t f0,
                                             const int32_t* sid, float4* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane & 15, kg = lane >> 4;
   const uint8_t* wb = p.w13 + (int64_t)e * 2 * p.F * p.D;
+  const uint8_t* const wp[2] = {code_ptr<PACKED>(wb, f0, p.D), code_ptr<PACKED>(wb, p.F + f0, p.D)};
   const uint16_t* xp[NT];
-  bool has[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int i = 16 * n + lr;
-    has[n] = i < m;
-    xp[n] = p.x + (int64_t)(has[n] ? list[i] / p.k : 0) * p.D;
+    // a lane past the last token takes the first one's values: a column of the
+    // product that nobody reads
+    const int i = 16 * n + lr < m ? 16 * n + lr : 0;
+    xp[n] = p.x + (int64_t)(list[i] / p.k) * p.D + 16 * kg;
   }
-  v4f ag[NT], au[NT];
+  v4f acc[2][NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) ag[n] = au[n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t units = (p.D + 127) / 128;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int64_t u = wave; u < units; u += kUpWaves) {
-    uint4 wg[2], wu[2], xv[NT][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t kc = 128 * u + 64 * h + 16 * kg;
-      const bool in = kc < p.D;
-      wg[h] = in ? ld_nt16(wb + code_at<PACKED>(f0 + lr, kc, p.D)) : zero;
-      wu[h] = in ? ld_nt16(wb + code_at<PACKED>(p.F + f0 + lr, kc, p.D)) : zero;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint4* xs = reinterpret_cast<const uint4*>(xp[n] + kc);
-        xv[n][2 * h] = in && has[n] ? xs[0] : zero;
-        xv[n][2 * h + 1] = in && has[n] ? xs[1] : zero;
-      }
-    }
-    unit_products<NT>(wg, xv, ag);
-    unit_products<NT>(wu, xv, au);
-  }
+  for (int n = 0; n < NT; ++n) acc[0][n] = acc[1][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+  const int units = (int)((p.D + 127) / 128);
+  stream_units<2, NT, kInFlight<NT>, PACKED>(wp, xp, units * wave / kUpWaves, units * (wave + 1) / kUpWaves, (int)p.D,
+                                             acc);
   // partial sums of the waves
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    red[((2 * n) * kUpWaves + wave) * 64 + lane] = make_float4(ag[n][0], ag[n][1], ag[n][2], ag[n][3]);
-    red[((2 * n + 1) * kUpWaves + wave) * 64 + lane] = make_float4(au[n][0], au[n][1], au[n][2], au[n][3]);
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      red[((2 * n + r) * kUpWaves + wave) * 64 + lane] =
+          make_float4(acc[r][n][0], acc[r][n][1], acc[r][n][2], acc[r][n][3]);
   }
   __syncthreads();
   if (wave >= NT) return;
@@ -198,6 +263,12 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeFewArgs p) {
   __shared__ int count;
   const int n = (int)p.T * p.k;
   few_ids(p.ids, n, p.E, sid, bits);
+  const FewMeta meta = few_meta(p.act, p.T, p.k, p.F);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    int c = 0;
+    for (int i = 0; i < 32; ++i) c += __popc(bits[i]);
+    meta.head[0] = c;
+  }
   const int e = few_expert(bits, blockIdx.y);
   if (e < 0) return;
   // the expert's pairs in order, the first of each token's only
@@ -216,6 +287,13 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeFewArgs p) {
   }
   __syncthreads();
   const int m = count;
+  if (blockIdx.x == 0) {
+    if (threadIdx.x < m) meta.pairs[blockIdx.y * kFewT + threadIdx.x] = (uint16_t)list[threadIdx.x];
+    if (threadIdx.x == 0) {
+      meta.expert[blockIdx.y] = e;
+      meta.count[blockIdx.y] = m;
+    }
+  }
   const int64_t f0 = 16 * (int64_t)blockIdx.x;
   if constexpr (NTM >= 4) {
     if (m > 32) return moe_up_tile<4, PACKED>(p, e, m, list, f0, sid, red);
@@ -226,102 +304,89 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeFewArgs p) {
   moe_up_tile<1, PACKED>(p, e, m, list, f0, sid, red);
 }
 
+// Units [u0, u1) of one expert for 16 rows, added to the wave's sums [T][16].
 template <int NT, bool PACKED>
-__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeFewArgs p) {
-  __shared__ float4 red[NT * kDownWaves * 64];
-  __shared__ int32_t sid[kFewT * kFewK];
-  __shared__ int32_t act_e[kMaxExperts];
-  __shared__ uint32_t bits[32];
-  __shared__ int count;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int lr = lane & 15, kg = lane >> 4;
-  const int T = (int)p.T, k = p.k;
-  few_ids(p.ids, T * k, p.E, sid, bits);
-  // the named experts in order
-  if (threadIdx.x < 64) {
-    const uint32_t w = lane < 32 ? bits[lane] : 0;
-    int upto = __popc(w);
+__device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, int e, int m, const uint16_t* pairs, int64_t d0,
+                                             int u0, int u1, float* sum) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4;
+  const uint8_t* const wp[1] = {code_ptr<PACKED>(p.w2 + (int64_t)e * p.D * p.F, d0, p.F)};
+  const uint16_t* xp[NT];
+  int tok[NT];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up(upto, o, 64);
-      if (lane >= o) upto += u;
-    }
-    int at = upto - __popc(w);
-    for (uint32_t v = w; v; v &= v - 1) act_e[at++] = 32 * lane + __ffs(v) - 1;
-    if (lane == 31) count = upto;
+  for (int n = 0; n < NT; ++n) {
+    const int pair = pairs[16 * n + lr < m ? 16 * n + lr : 0];
+    tok[n] = pair / p.k;
+    xp[n] = p.act + (int64_t)pair * p.F + 16 * kg;
   }
+  v4f acc[1][NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[0][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+  stream_units<1, NT, kInFlight<NT>, PACKED>(wp, xp, u0, u1, (int)p.F, acc);
+  const float* sc = p.inv2 + (int64_t)e * p.D + d0 + 4 * kg;
+  const float s0 = sc[0], s1 = sc[1], s2 = sc[2], s3 = sc[3];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    // an expert's tokens differ, so no two lanes meet
+    if (16 * n + lr >= m) continue;
+    float4* d = reinterpret_cast<float4*>(sum + tok[n] * 16 + 4 * kg);
+    float4 v = *d;
+    v.x += acc[0][n][0] * s0;
+    v.y += acc[0][n][1] * s1;
+    v.z += acc[0][n][2] * s2;
+    v.w += acc[0][n][3] * s3;
+    *d = v;
+  }
+}
+
+template <int NTM, bool PACKED>
+__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeFewArgs p) {
+  constexpr int kTok = 16 * NTM;
+  __shared__ float4 sums[kDownWaves * kTok * 4];  // [wave][token][16]
+  const int wave = threadIdx.x >> 6;
+  const FewMeta meta = few_meta(p.act, p.T, p.k, p.F);
+  for (int i = threadIdx.x; i < kDownWaves * kTok * 4; i += 64 * kDownWaves) sums[i] = make_float4(0, 0, 0, 0);
   __syncthreads();
-  const int nact = count;
   const int64_t d0 = 16 * (int64_t)blockIdx.x;
   const int units = (int)((p.F + 127) / 128);
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  v4f sum[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) sum[n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  for (int a = 0; a < nact; ++a) {
-    // the waves take the units in turn; where an expert has no unit left for
-    // this wave there is nothing to scale
-    int u = (wave - a * units) % kDownWaves;
-    u = u < 0 ? u + kDownWaves : u;
-    if (u >= units) continue;
-    const int e = act_e[a];
-    const uint8_t* wb = p.w2 + (int64_t)e * p.D * p.F;
-    const uint16_t* ap[NT];
-    bool has[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int t = 16 * n + lr;
-      int at = -1;
-      for (int j = k - 1; t < T && j >= 0; --j) at = sid[t * k + j] == e ? j : at;
-      has[n] = at >= 0;
-      ap[n] = p.act + (int64_t)(has[n] ? t * k + at : 0) * p.F;
-    }
-    v4f acc[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-    for (; u < units; u += kDownWaves) {
-      uint4 w[2], xv[NT][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t kc = 128 * (int64_t)u + 64 * h + 16 * kg;
-        const bool in = kc < p.F;
-        w[h] = in ? ld_nt16(wb + code_at<PACKED>(d0 + lr, kc, p.F)) : zero;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4* xs = reinterpret_cast<const uint4*>(ap[n] + kc);
-          xv[n][2 * h] = in && has[n] ? xs[0] : zero;
-          xv[n][2 * h + 1] = in && has[n] ? xs[1] : zero;
-        }
+  const int64_t all = (int64_t)meta.head[0] * units;
+  int64_t i = all * wave / kDownWaves;
+  const int64_t end = all * (wave + 1) / kDownWaves;
+  float* sum = reinterpret_cast<float*>(&sums[wave * kTok * 4]);
+  while (i < end) {
+    const int a = (int)(i / units), u0 = (int)(i % units);
+    const int u1 = (int)(end - i < units - u0 ? u0 + (end - i) : units);
+    const int e = meta.expert[a], m = meta.count[a];
+    const uint16_t* pairs = meta.pairs + a * kFewT;
+    bool done = false;
+    if constexpr (NTM >= 4) {
+      if (m > 32) {
+        moe_down_run<4, PACKED>(p, e, m, pairs, d0, u0, u1, sum);
+        done = true;
       }
-      unit_products<NT>(w, xv, acc);
     }
-    // a lane's products are all of the one token of its column, so only the
-    // tokens that named the expert take its sums (a NaN code stays with them)
-    const float* sc = p.inv2 + (int64_t)e * p.D + d0 + 4 * kg;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum[n][i] += has[n] ? acc[n][i] * sc[i] : 0.0f;
+    if constexpr (NTM >= 2) {
+      if (!done && m > 16) {
+        moe_down_run<2, PACKED>(p, e, m, pairs, d0, u0, u1, sum);
+        done = true;
+      }
     }
+    if (!done) moe_down_run<1, PACKED>(p, e, m, pairs, d0, u0, u1, sum);
+    i += u1 - u0;
   }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-    red[(n * kDownWaves + wave) * 64 + lane] = make_float4(sum[n][0], sum[n][1], sum[n][2], sum[n][3]);
   __syncthreads();
-  if (wave >= NT) return;
-  const int t = 16 * wave + lr;
-  if (t >= T) return;
+  const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
+  if (t >= (int)p.T) return;
   float r[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int w = 0; w < kDownWaves; ++w) {
-    const float4 a = red[(wave * kDownWaves + w) * 64 + lane];
+    const float4 a = sums[(w * kTok + t) * 4 + q];
     r[0] += a.x;
     r[1] += a.y;
     r[2] += a.z;
     r[3] += a.w;
   }
   const v2bf lo = {(__bf16)r[0], (__bf16)r[1]}, hi = {(__bf16)r[2], (__bf16)r[3]};
-  *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.D + d0 + 4 * kg) =
+  *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.D + d0 + 4 * q) =
       make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
 }
 
@@ -331,7 +396,7 @@ static hipError_t launch_few_t(const MoeFewArgs& a) {
   const dim3 gu((unsigned)(a.F / 16), (unsigned)(pairs < a.E ? pairs : a.E)), gd((unsigned)(a.D / 16));
   const dim3 bu(64 * kUpWaves), bd(64 * kDownWaves);
   auto go = [&](auto up, auto down) {
-    if (a.F > 0) hipLaunchKernelGGL(up, gu, bu, 0, a.stream, a);
+    hipLaunchKernelGGL(up, gu, bu, 0, a.stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(down, gd, bd, 0, a.stream, a);
@@ -343,7 +408,7 @@ static hipError_t launch_few_t(const MoeFewArgs& a) {
 }
 
 hipError_t launch_moe_few(const MoeFewArgs& a) {
-  if (a.T == 0 || a.D == 0) return hipSuccess;
+  if (a.T == 0 || a.D == 0 || a.F == 0) return hipSuccess;
   return a.packed ? launch_few_t<true>(a) : launch_few_t<false>(a);
 }
 

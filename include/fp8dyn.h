@@ -484,8 +484,8 @@ FP8DYN_API fp8_status fp8_moe_route_bwd(const void* logits, fp8_out logits_type,
  * fixed. D % 16 == 0 and F % 16 == 0 (packed: % 64), 16-byte aligned x, w13, w2,
  * out, ws (else FP8_ERR_ALIGNMENT); k <= 32, E <= 1024, D, F < 2^24 (else
  * FP8_ERR_UNSUPPORTED); fmt the native e4m3. F = 0 writes zeros. ws:
- * fp8_moe_few_ws_bytes(T, k, F) = 2 * T * k * F bytes, content on entry of no
- * matter; calls that may run at the same time need one each. */
+ * fp8_moe_few_ws_bytes(T, k, F) bytes (2 * T * k * F and some), content on
+ * entry of no matter; calls that may run at the same time need one each. */
 FP8DYN_API fp8_status fp8_moe_few(const uint16_t* x, const int32_t* ids, const float* weights, int64_t T, int32_t k,
                                   const uint8_t* w13, const float* w13_inv, const uint8_t* w2, const float* w2_inv,
                                   fp8_format fmt, int32_t E, int64_t D, int64_t F, int packed, uint16_t* out,

