@@ -650,7 +650,7 @@ fp8_status fp8_moe_route_bwd(const void* logits, fp8_out logits_type, int64_t T,
 }
 
 size_t fp8_moe_few_ws_bytes(int64_t T, int32_t k, int64_t F) {
-  if (T <= 0 || T > 64 || k <= 0 || k > 32 || F <= 0 || F >= (1 << 24)) return 0;
+  if (T <= 0 || T > 64 || k <= 0 || k > 32 || F <= 0 || F >= (1 << 20)) return 0;
   return moe_few_ws_bytes(T, k, F);
 }
 
@@ -659,7 +659,7 @@ fp8_status fp8_moe_few(const uint16_t* x, const int32_t* ids, const float* weigh
                        fp8_format fmt, int32_t E, int64_t D, int64_t F, int packed, uint16_t* out, void* ws,
                        size_t ws_bytes, void* stream) {
   if (T < 0 || k < 1 || E < 1 || D < 0 || F < 0) return FP8_ERR_INVALID_ARGUMENT;
-  if (T > 64 || k > 32 || E > 1024 || D >= (1 << 24) || F >= (1 << 24)) return FP8_ERR_UNSUPPORTED;
+  if (T > 64 || k > 32 || E > 1024 || D >= (1 << 20) || F >= (1 << 20)) return FP8_ERR_UNSUPPORTED;
   const int step = packed ? 64 : 16;
   if (D % step != 0 || F % step != 0) return FP8_ERR_ALIGNMENT;
   if (T == 0 || D == 0) return FP8_OK;

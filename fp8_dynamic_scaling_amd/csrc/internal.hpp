@@ -121,7 +121,7 @@ struct MoeFewArgs {
   const float* inv2;      // [E][D]
   int64_t T;              // <= 64
   int32_t E, k;           // E <= 1024, k <= 32
-  int64_t D, F;           // % 16 == 0 (packed: % 64 == 0), < 2^20
+  int64_t D, F;           // % 16 == 0 (packed: % 64 == 0), < 2^20: 32-bit byte offsets in x and act
   bool packed;
   uint16_t* out;          // [T][D]
   uint16_t* act;          // workspace, moe_few_ws_bytes(): [T * k][F] bf16 and the experts' tokens

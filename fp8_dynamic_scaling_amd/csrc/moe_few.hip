@@ -9,8 +9,9 @@
 // straight from HBM to registers, 16 bytes a lane, are decoded to bf16 (exact)
 // and multiplied by 16 tokens at a time with the BF16 matrix-core instruction,
 // which sums at fp32 precision; x and a are bf16 and come from the caches.
-//  - k_moe_up: a workgroup has one expert and 16 gate and 16 up rows; its waves
-//    share D among them. The waves' partial sums meet in LDS, in a fixed order.
+//  - k_moe_up: two workgroups a CU share the named experts' tiles of 16 gate and
+//    16 up rows evenly; a workgroup's waves share D among them. The waves'
+//    partial sums meet in LDS, in a fixed order.
 //  - k_moe_down: a workgroup has 16 rows of D for all experts; its waves share
 //    the (expert, piece of F) units. A wave adds what it has of a token to its
 //    own fp32 sums in LDS, and the waves' sums are added in order at the end: no
@@ -20,6 +21,15 @@
 // contraction and the same 128 values of its tokens; the loads of the next
 // units are in flight while one is multiplied. An expert's tokens are compacted
 // into tiles of 16.
+//
+// After HBM the loads' own rate is the next bound: measured, a 16-byte load of
+// a wavefront takes 17 clocks of its CU's load path where each four neighbouring
+// lanes read 64 bytes in a row, 33 where they read 64-byte steps (a packed chunk
+// as the matrix instruction's lanes want it) and 65 where they read four rows.
+// So rows (x, row-major codes) are loaded with neighbouring lanes along the
+// row and turned in a wave's own piece of LDS, and a is written in the order in
+// which k_moe_down's lanes read it.
+//
 // The rounding of a to bf16 (with its gate weight, half a step: 2^-8 relative)
 // is that of the activations the grouped GEMMs take; everything else is fp32
 // up to the one rounding of the output.
@@ -32,31 +42,32 @@ namespace fp8dyn {
 
 namespace {
 constexpr int kUpWaves = 4;
+constexpr int kUpBlocks = 512;  // two a CU
 constexpr int kDownWaves = 8;
 constexpr int kFewT = 64;
 constexpr int kFewK = 32;
 
-// What k_moe_up leaves in the workspace for k_moe_down, behind a: the number of
-// named experts, each one's id and number of tokens, and its pairs (t * k + j).
+// What k_moe_up leaves in the workspace for k_moe_down: a, an expert's part at
+// start * F, in it value f of its i-th of m tokens at ((f / 8) m + i) 8 + f % 8;
+// the number of named experts; each one's id, in order, where its pairs begin,
+// and the tokens of the pairs.
 struct FewMeta {
-  int32_t* head;   // [0] the number of experts
-  int32_t* expert;  // [T * k]
-  int32_t* count;   // [T * k]
-  uint16_t* pairs;  // [T * k][kFewT]
+  int32_t* head;     // [0]: the number of experts
+  uint16_t* expert;  // [T * k]
+  uint16_t* start;   // [T * k + 1]
+  uint16_t* token;   // [T * k]
 };
 __host__ __device__ inline FewMeta few_meta(uint16_t* act, int64_t T, int k, int64_t F) {
   FewMeta m;
   m.head = reinterpret_cast<int32_t*>(act + T * k * F);
-  m.expert = m.head + 4;
-  m.count = m.expert + T * k;
-  m.pairs = reinterpret_cast<uint16_t*>(m.count + T * k);
+  m.expert = reinterpret_cast<uint16_t*>(m.head + 1);
+  m.start = m.expert + T * k;
+  m.token = m.start + T * k + 1;
   return m;
 }
 }  // namespace
 
-size_t moe_few_ws_bytes(int64_t T, int k, int64_t F) {
-  return (size_t)(T * k) * (2 * F + 8 + 2 * kFewT) + 16;
-}
+size_t moe_few_ws_bytes(int64_t T, int k, int64_t F) { return (size_t)(T * k) * (2 * F + 6) + 8; }
 
 // Eight e4m3 codes -> eight bf16 (every e4m3 value is a bf16 value).
 __device__ __forceinline__ v8bf decode8(uint32_t d0, uint32_t d1) {
@@ -67,56 +78,117 @@ __device__ __forceinline__ v8bf decode8(uint32_t d0, uint32_t d1) {
   return (v8bf){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// 16-byte pieces of a row-major or k-packed [N][K] matrix of codes: where the
-// lane's piece of rows [16 i, 16 i + 16) begins, and the bytes from one 64-value
-// step of the contraction to the next (the packed 1 KB chunks of 16 x 64 follow
-// each other).
-template <bool PACKED>
-__device__ __forceinline__ const uint8_t* code_ptr(const uint8_t* w, int64_t row0, int64_t K) {
-  const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4;
-  return PACKED ? w + row0 * K + lr * 64 + kg * 16 : w + (row0 + lr) * K + kg * 16;
+// The wavefront's number, known to be the same in all of its lanes.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// Orders a wavefront's LDS reads behind its writes (LDS serves a wavefront in order).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
+
+// ---- one unit's operands --------------------------------------------------------
+//
+// A tile of codes, 16 rows x 128 values, as two 16-byte loads a lane. Packed:
+// the lanes' own operands, row l & 15 and values 16 (l >> 4) .. + 15 of each 64
+// (1 KB chunks of 16 x 64, one behind the other along the contraction).
+// Row-major: load i has rows 8 i + (l >> 3), 16 bytes l & 7, and goes through LDS.
 template <bool PACKED>
-constexpr int kStep = PACKED ? 1024 : 64;
-
-// The operands of one unit, 128 values of the contraction: R tiles of 16 weight
-// rows (lane: row l & 15, values 16 (l >> 4) .. + 15 of each 64) and NT tiles of
-// 16 tokens (lane: token l & 15, the same values).
-template <int R, int NT>
-struct Unit {
-  uint4 w[R][2];
-  uint4 x[NT][4];
-};
-
-template <int R, int NT, bool PACKED>
-__device__ __forceinline__ void load_unit(Unit<R, NT>& s, const uint8_t* const (&wp)[R],
-                                          const uint16_t* const (&xp)[NT], int u, int K) {
-  const int kg = (threadIdx.x & 63) >> 4;
-  const bool full = 128 * (u + 1) <= K;  // else lanes past K hold zeros
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const bool in = full || 128 * u + 64 * h + 16 * kg < K;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      s.w[r][h] = in ? ld_nt16(wp[r] + (int64_t)(2 * u + h) * kStep<PACKED>) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint4* q = reinterpret_cast<const uint4*>(xp[n] + 128 * u + 64 * h);
-      s.x[n][2 * h] = in ? q[0] : make_uint4(0, 0, 0, 0);
-      s.x[n][2 * h + 1] = in ? q[1] : make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ uint32_t code_off(int64_t K) {
+  const int l = threadIdx.x & 63;
+  return PACKED ? (l & 15) * 64 + (l >> 4) * 16 : (l >> 3) * (uint32_t)K + (l & 7) * 16;
+}
+// base: the tile's first row at the unit's first value
+template <bool PACKED>
+__device__ __forceinline__ void load_codes(uint4 (&w)[2], const uint8_t* tile, uint32_t off, int u, int K) {
+  const int l = threadIdx.x & 63;
+  if constexpr (PACKED) {
+    const uint8_t* p = tile + (int64_t)u * 2048;
+    w[0] = ld_nt16(p + off);
+    if (128 * u + 64 < K)  // K % 64 == 0: the last unit may be half
+      w[1] = ld_nt16(p + 1024 + off);
+    else
+      w[1] = make_uint4(0, 0, 0, 0);
+  } else {
+    const uint8_t* p = tile + 128 * u;
+    if (128 * (u + 1) <= K) {
+      w[0] = *reinterpret_cast<const uint4*>(p + off);
+      w[1] = *reinterpret_cast<const uint4*>(p + 8 * (int64_t)K + off);
+    } else {
+      w[0] = w[1] = make_uint4(0, 0, 0, 0);
+      if (128 * u + 16 * (l & 7) < K) {
+        w[0] = *reinterpret_cast<const uint4*>(p + off);
+        w[1] = *reinterpret_cast<const uint4*>(p + 8 * (int64_t)K + off);
+      }
     }
   }
 }
+// The lanes' operands of a loaded tile. Row-major, through 2 KB of LDS: row r's
+// piece c lies at r * 128 + 16 (c ^ (r / 2 % 8)), so that the 16 rows of a
+// column of pieces fall on all banks.
+template <bool PACKED>
+__device__ __forceinline__ void turn_codes(uint4 (&w)[2], uint8_t* lds) {
+  if constexpr (!PACKED) {
+    const int l = threadIdx.x & 63, lr = l & 15, kg = l >> 4;
+    const int r = l >> 3, c = l & 7;
+    *reinterpret_cast<uint4*>(lds + r * 128 + 16 * (c ^ (r >> 1))) = w[0];
+    *reinterpret_cast<uint4*>(lds + (r + 8) * 128 + 16 * (c ^ ((r >> 1) + 4))) = w[1];
+    wave_lds_fence();
+    w[0] = *reinterpret_cast<const uint4*>(lds + lr * 128 + 16 * (kg ^ (lr >> 1)));
+    w[1] = *reinterpret_cast<const uint4*>(lds + lr * 128 + 16 * ((4 + kg) ^ (lr >> 1)));
+    wave_lds_fence();
+  }
+}
 
+// A tile of x, 16 tokens x 128 values: load i has tokens 4 i + (l >> 4), 16
+// bytes l & 15. Loads of tokens past the last are left out.
+struct RowTile {
+  v8bf v[4];
+};
+__device__ __forceinline__ void load_rows(RowTile& x, const uint16_t* base, const uint32_t (&off)[4], int n, int u,
+                                          int K) {
+  const int l = threadIdx.x & 63;
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(base + 128 * u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (4 * i >= n) break;
+    if (128 * (u + 1) <= K) {
+      x.v[i] = *reinterpret_cast<const v8bf*>(p + off[i]);
+    } else {
+      x.v[i] = (v8bf){};
+      if (128 * u + 8 * (l & 15) < K) x.v[i] = *reinterpret_cast<const v8bf*>(p + off[i]);
+    }
+  }
+}
+// Through 4 KB of LDS: token r's piece c lies at r * 256 + 16 (c ^ r). The
+// operand of matrix instruction q is piece 8 (q / 2) + 2 (l >> 4) + q % 2 of
+// token l & 15, the values of the codes' bytes 8 (q % 2) .. + 7 of load q / 2.
+__device__ __forceinline__ void turn_rows(RowTile& x, int n, uint8_t* lds) {
+  const int l = threadIdx.x & 63, lr = l & 15, kg = l >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (4 * i >= n) break;
+    const int r = 4 * i + kg;
+    *reinterpret_cast<v8bf*>(lds + r * 256 + 16 * (lr ^ r)) = x.v[i];
+  }
+  wave_lds_fence();
+  // tokens past the last are whatever LDS holds: columns that nobody reads
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    x.v[q] = *reinterpret_cast<const v8bf*>(lds + lr * 256 + 16 * ((8 * (q >> 1) + 2 * kg + (q & 1)) ^ lr));
+  wave_lds_fence();
+}
+
+// The products of R tiles of codes with NT tiles of tokens.
 template <int R, int NT>
-__device__ __forceinline__ void multiply_unit(const Unit<R, NT>& s, v4f (&acc)[R][NT]) {
+__device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const RowTile (&x)[NT], v4f (&acc)[R][NT]) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     v8bf a[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      a[2 * h] = decode8(s.w[r][h].x, s.w[r][h].y);
-      a[2 * h + 1] = decode8(s.w[r][h].z, s.w[r][h].w);
+      a[2 * h] = decode8(w[r][h].x, w[r][h].y);
+      a[2 * h + 1] = decode8(w[r][h].z, w[r][h].w);
     }
     // two wait states between the converts and the matrix instructions
     __builtin_amdgcn_sched_barrier(0);
@@ -125,38 +197,26 @@ __device__ __forceinline__ void multiply_unit(const Unit<R, NT>& s, v4f (&acc)[R
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const v8bf b = __builtin_bit_cast(v8bf, s.x[n][q]);
-        acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], b, acc[r][n], 0, 0, 0);
-        keep_live(b);
-      }
+      for (int q = 0; q < 4; ++q)
+        acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], x[n].v[q], acc[r][n], 0, 0, 0);
     }
-    asm volatile("" ::"v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]));
+    // the operands stay live past the matrix instructions, which nothing may
+    // move behind this point: no destination shares a source's registers
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      keep_live(a[q]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) keep_live(x[n].v[q]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// acc += the products of units [u0, u1), P of them in flight.
-template <int R, int NT, int P, bool PACKED>
-__device__ __forceinline__ void stream_units(const uint8_t* const (&wp)[R], const uint16_t* const (&xp)[NT], int u0,
-                                             int u1, int K, v4f (&acc)[R][NT]) {
-  Unit<R, NT> s[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i)
-    if (u0 + i < u1) load_unit<R, NT, PACKED>(s[i], wp, xp, u0 + i, K);
-  for (int u = u0; u < u1; u += P) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      if (u + i >= u1) break;
-      multiply_unit<R, NT>(s[i], acc);
-      if (u + i + P < u1) load_unit<R, NT, PACKED>(s[i], wp, xp, u + i + P, K);
-    }
-  }
-}
-
-// Units in flight by the tiles of tokens: the registers of P units, 16 R + 16 NT
-// each, stay near 128.
+// Units in flight by the tiles of tokens: their registers, 8 a tile of codes and
+// 16 a tile of tokens, stay below 128.
 template <int NT>
-constexpr int kInFlight = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+constexpr int kInFlight = NT == 1 ? 3 : NT == 2 ? 2 : 1;
 
 // The ids in LDS and a bit for each expert that some token names.
 __device__ __forceinline__ void few_ids(const int32_t* __restrict__ ids, int n, int E, int32_t* sid, uint32_t* bits) {
@@ -171,170 +231,311 @@ __device__ __forceinline__ void few_ids(const int32_t* __restrict__ ids, int n, 
   __syncthreads();
 }
 
-// The s-th named expert in order, or -1 past the last (the same in every lane).
-__device__ __forceinline__ int few_expert(const uint32_t* bits, int s) {
+// Inclusive count of the bits up to each of the 32 words, in lanes 0 to 31.
+__device__ __forceinline__ int few_count(uint32_t w) {
   const int lane = threadIdx.x & 63;
-  const uint32_t w = lane < 32 ? bits[lane] : 0;
   int upto = __popc(w);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up(upto, o, 64);
     if (lane >= o) upto += u;
   }
+  return upto;
+}
+
+// The s-th named expert in order, s below their number (the same in every lane).
+__device__ __forceinline__ int few_expert(const uint32_t* bits, int s) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t w = lane < 32 ? bits[lane] : 0;
+  const int upto = few_count(w);
   const int before = upto - __popc(w);
   const uint64_t hit = __ballot(lane < 32 && s >= before && s < upto);
-  if (!hit) return -1;
   const int word = __ffsll((unsigned long long)hit) - 1;
   uint32_t v = __shfl(w, word, 64);
   for (int r = s - __shfl(before, word, 64); r > 0; --r) v &= v - 1;
-  return 32 * word + __ffs(v) - 1;
+  return __builtin_amdgcn_readfirstlane(32 * word + __ffs(v) - 1);
 }
 
+// Tiles [0, nt) of 16 gate and 16 up rows of one expert from row f0 on. The
+// units of a tile that a wave has go through P register slots in turn; a slot
+// is loaded again as soon as it has been multiplied, with the first units of
+// the next tile at the end of one, so that loads stay in flight while the
+// waves' sums are added.
+struct UpShared {
+  int32_t sid[kFewT * kFewK];
+  int32_t list[kFewT];
+  float gate[kFewT];
+  float scale[2][32];
+  uint32_t bits[32];
+  int count[2];
+};
+
 template <int NT, bool PACKED>
-__device__ __forceinline__ void moe_up_tile(const MoeFewArgs& p, int e, int m, const int32_t* list, int64_t f0,
-                                            const int32_t* sid, float4* red) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, int64_t act0, int64_t f0, int nt,
+                                             UpShared& sh, float4* red, uint8_t* turn) {
+  constexpr int P = kInFlight<NT>;
+  const int lane = threadIdx.x & 63, wave = wave_id();
   const int lr = lane & 15, kg = lane >> 4;
   const uint8_t* wb = p.w13 + (int64_t)e * 2 * p.F * p.D;
-  const uint8_t* const wp[2] = {code_ptr<PACKED>(wb, f0, p.D), code_ptr<PACKED>(wb, p.F + f0, p.D)};
-  const uint16_t* xp[NT];
+  const float* sc = p.inv13 + (int64_t)e * 2 * p.F + (lane & 16 ? p.F : 0) + f0 + lr;
+  const uint32_t woff = code_off<PACKED>(p.D);
+  uint32_t xoff[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    // a lane past the last token takes the first one's values: a column of the
-    // product that nobody reads
-    const int i = 16 * n + lr < m ? 16 * n + lr : 0;
-    xp[n] = p.x + (int64_t)(list[i] / p.k) * p.D + 16 * kg;
-  }
-  v4f acc[2][NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) acc[0][n] = acc[1][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 4; ++i) {
+      const int it = 16 * n + 4 * i + kg < m ? 16 * n + 4 * i + kg : 0;
+      xoff[n][i] = 2 * ((uint32_t)(sh.list[it] / p.k) * (uint32_t)p.D + 8 * lr);
+    }
+  }
   const int units = (int)((p.D + 127) / 128);
-  stream_units<2, NT, kInFlight<NT>, PACKED>(wp, xp, units * wave / kUpWaves, units * (wave + 1) / kUpWaves, (int)p.D,
-                                             acc);
-  // partial sums of the waves
+  const int u0 = units * wave / kUpWaves, nu = units * (wave + 1) / kUpWaves - u0;
+  uint4 w[P][2][2];
+  RowTile x[P][NT];
+  auto load = [&](uint4 (&dw)[2][2], RowTile (&dx)[NT], int tile, int u) {
+    load_codes<PACKED>(dw[0], wb + (f0 + 16 * tile) * p.D, woff, u0 + u, (int)p.D);
+    load_codes<PACKED>(dw[1], wb + (p.F + f0 + 16 * tile) * p.D, woff, u0 + u, (int)p.D);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n) load_rows(dx[n], p.x, xoff[n], m - 16 * n, u0 + u, (int)p.D);
+  };
+  float scale = wave == 0 && lane < 32 ? sc[0] : 0.0f;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      red[((2 * n + r) * kUpWaves + wave) * 64 + lane] =
-          make_float4(acc[r][n][0], acc[r][n][1], acc[r][n][2], acc[r][n][3]);
+  for (int i = 0; i < P; ++i)
+    if (i < nu) load(w[i], x[i], 0, i);
+  uint8_t* mine = turn + wave * 4096;
+  for (int tile = 0; tile < nt; ++tile) {
+    const float next = wave == 0 && lane < 32 && tile + 1 < nt ? sc[16 * (tile + 1)] : 0.0f;
+    v4f acc[2][NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[0][n] = acc[1][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int u = 0; u < nu; u += P) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (u + i >= nu) break;
+        turn_codes<PACKED>(w[i][0], mine);
+        turn_codes<PACKED>(w[i][1], mine);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) turn_rows(x[i][n], m - 16 * n, mine);
+        multiply<2, NT>(w[i], x[i], acc);
+        const bool here = u + i + P < nu;
+        if (here || tile + 1 < nt) load(w[i], x[i], tile + !here, here ? u + i + P : i);
+      }
+    }
+    // The waves' partial sums (and the rows' scales), in one of two buffers: a
+    // wave writes it again two tiles on, behind a barrier that the reader
+    // reaches after reading. Four token tiles have one buffer, which lets two
+    // workgroups share a CU's LDS, and a barrier before it is written again.
+    if (NT == 4 && tile > 0) __syncthreads();
+    float4* r = red + (NT < 4 ? tile & 1 : 0) * (NT * 2 * kUpWaves * 64);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+        r[((2 * n + z) * kUpWaves + wave) * 64 + lane] =
+            make_float4(acc[z][n][0], acc[z][n][1], acc[z][n][2], acc[z][n][3]);
+    }
+    if (wave == 0 && lane < 32) sh.scale[tile & 1][lane] = scale;
+    scale = next;
+    __syncthreads();
+    const int n = (wave + tile) % kUpWaves;  // the waves finish token tiles in turn
+    const int item = 16 * n + lr;
+    if (n >= NT || item >= m) continue;
+    float g[4] = {0, 0, 0, 0}, uu[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kUpWaves; ++i) {
+      const float4 a = r[((2 * n) * kUpWaves + i) * 64 + lane];
+      const float4 b = r[((2 * n + 1) * kUpWaves + i) * 64 + lane];
+      g[0] += a.x;
+      g[1] += a.y;
+      g[2] += a.z;
+      g[3] += a.w;
+      uu[0] += b.x;
+      uu[1] += b.y;
+      uu[2] += b.z;
+      uu[3] += b.w;
+    }
+    const float gate = sh.gate[item];
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float gv = g[i] * sh.scale[tile & 1][4 * kg + i], uv = uu[i] * sh.scale[tile & 1][16 + 4 * kg + i];
+      v[i] = gate * (gv / (1.0f + expf(-gv)) * uv);
+    }
+    const v2bf lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
+    const int64_t f = f0 + 16 * tile + 4 * kg;
+    *reinterpret_cast<uint2*>(p.act + act0 * p.F + ((f >> 3) * m + item) * 8 + (f & 7)) =
+        make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
   }
-  __syncthreads();
-  if (wave >= NT) return;
-  const int item = 16 * wave + lr;  // this wave finishes tile `wave`
-  if (item >= m) return;
-  float g[4] = {0, 0, 0, 0}, uu[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int w = 0; w < kUpWaves; ++w) {
-    const float4 a = red[((2 * wave) * kUpWaves + w) * 64 + lane];
-    const float4 b = red[((2 * wave + 1) * kUpWaves + w) * 64 + lane];
-    g[0] += a.x;
-    g[1] += a.y;
-    g[2] += a.z;
-    g[3] += a.w;
-    uu[0] += b.x;
-    uu[1] += b.y;
-    uu[2] += b.z;
-    uu[3] += b.w;
-  }
-  const int64_t f = f0 + 4 * kg;
-  const float* sc = p.inv13 + (int64_t)e * 2 * p.F;
-  const int it = list[item];
-  const int t = it / p.k;
-  float gate = 0.0f;  // the weights of all the token's slots that name e
-  for (int j = it % p.k; j < p.k; ++j) gate += sid[t * p.k + j] == e ? p.weights[t * p.k + j] : 0.0f;
-  float r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float gv = g[i] * sc[f + i], uv = uu[i] * sc[p.F + f + i];
-    r[i] = gate * (gv / (1.0f + expf(-gv)) * uv);
-  }
-  const v2bf lo = {(__bf16)r[0], (__bf16)r[1]}, hi = {(__bf16)r[2], (__bf16)r[3]};
-  *reinterpret_cast<uint2*>(p.act + (int64_t)it * p.F + f) =
-      make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
 }
 
+// The workgroups share the named experts' tiles of 16 columns of F evenly, each
+// a run of neighbours: an expert's tokens are looked up once or twice a
+// workgroup, and its codes are read in long runs.
 template <int NTM, bool PACKED>
-__global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(MoeFewArgs p) {
-  __shared__ float4 red[NTM * 2 * kUpWaves * 64];
-  __shared__ int32_t sid[kFewT * kFewK];
-  __shared__ int32_t list[kFewT];
-  __shared__ uint32_t bits[32];
-  __shared__ int count;
+__global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeFewArgs p) {
+  __shared__ float4 red[(NTM < 4 ? 2 : 1) * NTM * 2 * kUpWaves * 64];
+  __shared__ __align__(16) uint8_t turn[kUpWaves * 4096];
+  __shared__ UpShared sh;
+  const int lane = threadIdx.x & 63;
   const int n = (int)p.T * p.k;
-  few_ids(p.ids, n, p.E, sid, bits);
+  few_ids(p.ids, n, p.E, sh.sid, sh.bits);
+  const int nact = __builtin_amdgcn_readlane(few_count(lane < 32 ? sh.bits[lane] : 0), 31);
   const FewMeta meta = few_meta(p.act, p.T, p.k, p.F);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-    int c = 0;
-    for (int i = 0; i < 32; ++i) c += __popc(bits[i]);
-    meta.head[0] = c;
-  }
-  const int e = few_expert(bits, blockIdx.y);
-  if (e < 0) return;
-  // the expert's pairs in order, the first of each token's only
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    int m = 0;
-    for (int i0 = 0; i0 < n; i0 += 64) {
-      const int i = i0 + lane;
-      bool mine = i < n && sid[i] == e;
-      for (int j = i - i % p.k; mine && j < i; ++j) mine = sid[j] != e;
-      const uint64_t b = __ballot(mine);
-      if (mine) list[m + __popcll(b & ((1ull << lane) - 1))] = i;
-      m += __popcll(b);
+  if (blockIdx.x == 0 && threadIdx.x == 0) meta.head[0] = nact;
+  const int per = (int)(p.F / 16);
+  const int64_t all = (int64_t)nact * per;
+  int64_t tile = all * blockIdx.x / gridDim.x;
+  const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
+  while (tile < end) {
+    const int a = (int)(tile / per), first = (int)(tile % per);
+    const int nt = (int)(end - tile < per - first ? end - tile : per - first);
+    const int e = few_expert(sh.bits, a);
+    // the expert's pairs in order, the first of each token's only, with the
+    // weights of all the token's slots that name e, and the number of pairs of
+    // the experts before it
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      int m = 0, below = 0;
+      for (int i0 = 0; i0 < n; i0 += 64) {
+        const int i = i0 + lane;
+        const int id = i < n ? sh.sid[i] : -1;
+        bool head = id >= 0 && id <= e;
+        for (int j = i - i % p.k; head && j < i; ++j) head = sh.sid[j] != id;
+        const uint64_t b = __ballot(head && id == e);
+        if (head && id == e) {
+          const int at = m + __popcll(b & ((1ull << lane) - 1));
+          float gate = 0.0f;
+          for (int j = i; j < i - i % p.k + p.k; ++j) gate += sh.sid[j] == e ? p.weights[j] : 0.0f;
+          sh.list[at] = i;
+          sh.gate[at] = gate;
+        }
+        m += __popcll(b);
+        below += __popcll(__ballot(head && id < e));
+      }
+      if (lane == 0) {
+        sh.count[0] = m;
+        sh.count[1] = below;
+      }
     }
-    if (lane == 0) count = m;
-  }
-  __syncthreads();
-  const int m = count;
-  if (blockIdx.x == 0) {
-    if (threadIdx.x < m) meta.pairs[blockIdx.y * kFewT + threadIdx.x] = (uint16_t)list[threadIdx.x];
-    if (threadIdx.x == 0) {
-      meta.expert[blockIdx.y] = e;
-      meta.count[blockIdx.y] = m;
+    __syncthreads();
+    const int m = __builtin_amdgcn_readfirstlane(sh.count[0]), act0 = __builtin_amdgcn_readfirstlane(sh.count[1]);
+    if (first == 0) {  // one workgroup of the expert's says who its tokens are
+      if (threadIdx.x < m) meta.token[act0 + threadIdx.x] = (uint16_t)(sh.list[threadIdx.x] / p.k);
+      if (threadIdx.x == 0) {
+        meta.expert[a] = (uint16_t)e;
+        meta.start[a] = (uint16_t)act0;
+        if (a == nact - 1) meta.start[nact] = (uint16_t)(act0 + m);
+      }
     }
+    const int64_t f0 = 16 * (int64_t)first;
+    bool done = false;
+    if constexpr (NTM >= 4) {
+      if (m > 32) {
+        moe_up_tiles<4, PACKED>(p, e, m, act0, f0, nt, sh, red, turn);
+        done = true;
+      }
+    }
+    if constexpr (NTM >= 2) {
+      if (!done && m > 16) {
+        moe_up_tiles<2, PACKED>(p, e, m, act0, f0, nt, sh, red, turn);
+        done = true;
+      }
+    }
+    if (!done) moe_up_tiles<1, PACKED>(p, e, m, act0, f0, nt, sh, red, turn);
+    tile += nt;
   }
-  const int64_t f0 = 16 * (int64_t)blockIdx.x;
-  if constexpr (NTM >= 4) {
-    if (m > 32) return moe_up_tile<4, PACKED>(p, e, m, list, f0, sid, red);
-  }
-  if constexpr (NTM >= 2) {
-    if (m > 16) return moe_up_tile<2, PACKED>(p, e, m, list, f0, sid, red);
-  }
-  moe_up_tile<1, PACKED>(p, e, m, list, f0, sid, red);
 }
 
-// Units [u0, u1) of one expert for 16 rows, added to the wave's sums [T][16].
+struct DownShared {
+  uint16_t expert[kMaxExperts], start[kMaxExperts + 1], token[kFewT * kFewK];
+  int count;
+};
+
+// A wave's run [begin, end) of the (expert, unit) pairs of 16 rows. P units are
+// in flight across the experts' borders; at an expert's last unit its sums,
+// times the rows' scales, are added to the wave's sums [token][16].
 template <int NT, bool PACKED>
-__device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, int e, int m, const uint16_t* pairs, int64_t d0,
-                                             int u0, int u1, float* sum) {
+__device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShared& sh, int64_t d0, int units, int i,
+                                             int end, float* sum, uint8_t* turn) {
+  constexpr int P = kInFlight<NT>;
   const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4;
-  const uint8_t* const wp[1] = {code_ptr<PACKED>(p.w2 + (int64_t)e * p.D * p.F, d0, p.F)};
-  const uint16_t* xp[NT];
-  int tok[NT];
+  uint4 w[P][1][2];
+  RowTile x[P][NT];
+  float4 sc[P];
+  const uint32_t woff = code_off<PACKED>(p.F);
+  // the load side: the expert and unit of the next load, and its pointers
+  int la = i / units, lu = i % units, m = 0;
+  const uint8_t* wp = nullptr;
+  const uint16_t* ap = nullptr;
+  const float* sp = nullptr;
+  auto point = [&]() {
+    const int64_t e = __builtin_amdgcn_readfirstlane(sh.expert[la]);
+    const int b = __builtin_amdgcn_readfirstlane(sh.start[la]);
+    m = __builtin_amdgcn_readfirstlane(sh.start[la + 1]) - b;
+    wp = p.w2 + (e * p.D + d0) * p.F;
+    ap = p.act + (int64_t)b * p.F;
+    sp = p.inv2 + e * p.D + d0;
+  };
+  auto load = [&](uint4 (&dw)[1][2], RowTile (&dx)[NT], float4& c, bool last) {
+    load_codes<PACKED>(dw[0], wp, woff, lu, (int)p.F);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int pair = pairs[16 * n + lr < m ? 16 * n + lr : 0];
-    tok[n] = pair / p.k;
-    xp[n] = p.act + (int64_t)pair * p.F + 16 * kg;
-  }
+    for (int n = 0; n < NT; ++n) {
+      // lanes without a token read the last one's value: a column nobody reads
+      const int item = 16 * n + lr < m ? 16 * n + lr : m - 1;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int g = 16 * lu + 8 * (q >> 1) + 2 * kg + (q & 1);
+        if (128 * (lu + 1) <= (int)p.F) {
+          dx[n].v[q] = *reinterpret_cast<const v8bf*>(ap + (uint32_t)(8 * (g * m + item)));
+        } else {
+          dx[n].v[q] = (v8bf){};
+          if (8 * g < (int)p.F) dx[n].v[q] = *reinterpret_cast<const v8bf*>(ap + (uint32_t)(8 * (g * m + item)));
+        }
+      }
+    }
+    ++lu;
+    if (lu == units || last) c = make_float4(sp[4 * kg], sp[4 * kg + 1], sp[4 * kg + 2], sp[4 * kg + 3]);
+    if (lu == units && !last) {
+      lu = 0;
+      ++la;
+      point();
+    }
+  };
+  int ca = la, cu = lu;  // the multiply side
+  point();
+#pragma unroll
+  for (int j = 0; j < P; ++j)
+    if (i + j < end) load(w[j], x[j], sc[j], i + j + 1 == end);
   v4f acc[1][NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) acc[0][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  stream_units<1, NT, kInFlight<NT>, PACKED>(wp, xp, u0, u1, (int)p.F, acc);
-  const float* sc = p.inv2 + (int64_t)e * p.D + d0 + 4 * kg;
-  const float s0 = sc[0], s1 = sc[1], s2 = sc[2], s3 = sc[3];
+  for (; i < end; i += P) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    // an expert's tokens differ, so no two lanes meet
-    if (16 * n + lr >= m) continue;
-    float4* d = reinterpret_cast<float4*>(sum + tok[n] * 16 + 4 * kg);
-    float4 v = *d;
-    v.x += acc[0][n][0] * s0;
-    v.y += acc[0][n][1] * s1;
-    v.z += acc[0][n][2] * s2;
-    v.w += acc[0][n][3] * s3;
-    *d = v;
+    for (int j = 0; j < P; ++j) {
+      if (i + j >= end) break;
+      turn_codes<PACKED>(w[j][0], turn);
+      multiply<1, NT>(w[j], x[j], acc);
+      if (++cu == units || i + j + 1 == end) {
+        const int b = sh.start[ca], mc = sh.start[ca + 1] - b;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          // an expert's tokens differ, so no two lanes meet
+          if (16 * n + lr < mc) {
+            float4* d = reinterpret_cast<float4*>(sum + sh.token[b + 16 * n + lr] * 16 + 4 * kg);
+            float4 v = *d;
+            v.x += acc[0][n][0] * sc[j].x;
+            v.y += acc[0][n][1] * sc[j].y;
+            v.z += acc[0][n][2] * sc[j].z;
+            v.w += acc[0][n][3] * sc[j].w;
+            *d = v;
+          }
+          acc[0][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        cu = 0;
+        ++ca;
+      }
+      if (i + j + P < end) load(w[j], x[j], sc[j], i + j + P + 1 == end);
+    }
   }
 }
 
@@ -342,36 +543,45 @@ template <int NTM, bool PACKED>
 __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeFewArgs p) {
   constexpr int kTok = 16 * NTM;
   __shared__ float4 sums[kDownWaves * kTok * 4];  // [wave][token][16]
-  const int wave = threadIdx.x >> 6;
+  __shared__ __align__(16) uint8_t turn[PACKED ? 16 : kDownWaves * 2048];
+  __shared__ DownShared sh;
+  const int wave = wave_id(), lane = threadIdx.x & 63;
   const FewMeta meta = few_meta(p.act, p.T, p.k, p.F);
+  const int n = (int)p.T * p.k, slots = n < p.E ? n : p.E;
   for (int i = threadIdx.x; i < kDownWaves * kTok * 4; i += 64 * kDownWaves) sums[i] = make_float4(0, 0, 0, 0);
+  // all that the workspace may hold of the lists; k_moe_up wrote the parts that are used
+  for (int i = threadIdx.x; i < n; i += 64 * kDownWaves) {
+    sh.token[i] = meta.token[i];
+    if (i < slots) sh.expert[i] = meta.expert[i];
+  }
+  for (int i = threadIdx.x; i <= slots; i += 64 * kDownWaves) sh.start[i] = meta.start[i];
+  if (threadIdx.x == 0) sh.count = meta.head[0];
   __syncthreads();
+  const int nact = __builtin_amdgcn_readfirstlane(sh.count);
+  int most = 0;  // the largest number of tokens of an expert
+  for (int a = lane; a < nact; a += 64) most = max(most, sh.start[a + 1] - sh.start[a]);
+  const bool over16 = __ballot(most > 16) != 0, over32 = __ballot(most > 32) != 0;
   const int64_t d0 = 16 * (int64_t)blockIdx.x;
   const int units = (int)((p.F + 127) / 128);
-  const int64_t all = (int64_t)meta.head[0] * units;
-  int64_t i = all * wave / kDownWaves;
-  const int64_t end = all * (wave + 1) / kDownWaves;
+  const int64_t all = (int64_t)nact * units;
+  const int i0 = (int)(all * wave / kDownWaves), i1 = (int)(all * (wave + 1) / kDownWaves);
   float* sum = reinterpret_cast<float*>(&sums[wave * kTok * 4]);
-  while (i < end) {
-    const int a = (int)(i / units), u0 = (int)(i % units);
-    const int u1 = (int)(end - i < units - u0 ? u0 + (end - i) : units);
-    const int e = meta.expert[a], m = meta.count[a];
-    const uint16_t* pairs = meta.pairs + a * kFewT;
+  uint8_t* mine = PACKED ? turn : turn + wave * 2048;
+  if (i0 < i1) {
     bool done = false;
     if constexpr (NTM >= 4) {
-      if (m > 32) {
-        moe_down_run<4, PACKED>(p, e, m, pairs, d0, u0, u1, sum);
+      if (over32) {
+        moe_down_run<4, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
         done = true;
       }
     }
     if constexpr (NTM >= 2) {
-      if (!done && m > 16) {
-        moe_down_run<2, PACKED>(p, e, m, pairs, d0, u0, u1, sum);
+      if (!done && over16) {
+        moe_down_run<2, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
         done = true;
       }
     }
-    if (!done) moe_down_run<1, PACKED>(p, e, m, pairs, d0, u0, u1, sum);
-    i += u1 - u0;
+    if (!done) moe_down_run<1, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
   }
   __syncthreads();
   const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
@@ -392,8 +602,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeFewArgs p) {
 
 template <bool PACKED>
 static hipError_t launch_few_t(const MoeFewArgs& a) {
-  const int64_t pairs = a.T * a.k;
-  const dim3 gu((unsigned)(a.F / 16), (unsigned)(pairs < a.E ? pairs : a.E)), gd((unsigned)(a.D / 16));
+  const int64_t pairs = a.T * a.k, most = (pairs < a.E ? pairs : a.E) * (a.F / 16);
+  const dim3 gu((unsigned)(most < kUpBlocks ? most : kUpBlocks)), gd((unsigned)(a.D / 16));
   const dim3 bu(64 * kUpWaves), bd(64 * kDownWaves);
   auto go = [&](auto up, auto down) {
     hipLaunchKernelGGL(up, gu, bu, 0, a.stream, a);

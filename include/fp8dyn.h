@@ -482,7 +482,7 @@ FP8DYN_API fp8_status fp8_moe_route_bwd(const void* logits, fp8_out logits_type,
  * [0, E) names no expert; one that a token names twice counts with the sum of
  * its weights; a token that names none gets zeros. The order of all sums is
  * fixed. D % 16 == 0 and F % 16 == 0 (packed: % 64), 16-byte aligned x, w13, w2,
- * out, ws (else FP8_ERR_ALIGNMENT); k <= 32, E <= 1024, D, F < 2^24 (else
+ * out, ws (else FP8_ERR_ALIGNMENT); k <= 32, E <= 1024, D, F < 2^20 (else
  * FP8_ERR_UNSUPPORTED); fmt the native e4m3. F = 0 writes zeros. ws:
  * fp8_moe_few_ws_bytes(T, k, F) bytes (2 * T * k * F and some), content on
  * entry of no matter; calls that may run at the same time need one each. */

@@ -117,7 +117,7 @@ def test_route_bwd_refusals(lib, kw, want):
     (dict(T=-1), f.ERR_INVALID_ARGUMENT), (dict(k=0), f.ERR_INVALID_ARGUMENT), (dict(E=0), f.ERR_INVALID_ARGUMENT),
     (dict(D=-16), f.ERR_INVALID_ARGUMENT), (dict(F=-16), f.ERR_INVALID_ARGUMENT),
     (dict(T=65), f.ERR_UNSUPPORTED), (dict(k=33), f.ERR_UNSUPPORTED), (dict(E=1025), f.ERR_UNSUPPORTED),
-    (dict(D=1 << 24), f.ERR_UNSUPPORTED), (dict(F=1 << 24), f.ERR_UNSUPPORTED),
+    (dict(D=1 << 20), f.ERR_UNSUPPORTED), (dict(F=1 << 20), f.ERR_UNSUPPORTED),
     (dict(D=264), f.ERR_ALIGNMENT), (dict(F=40), f.ERR_ALIGNMENT), (dict(D=272, packed=1), f.ERR_ALIGNMENT),
     (dict(F=80, packed=1), f.ERR_ALIGNMENT),
     *[({n: None}, f.ERR_INVALID_ARGUMENT) for n in ("x", "ids", "w", "w13", "i13", "w2", "i2", "out")],
