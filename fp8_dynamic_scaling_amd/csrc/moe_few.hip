@@ -12,11 +12,11 @@
 //  - k_moe_up: two workgroups a CU share the named experts' tiles of 16 gate and
 //    16 up rows evenly; a workgroup's waves share D among them. The waves'
 //    partial sums meet in LDS, in a fixed order.
-//  - k_moe_down: a workgroup has 16 rows of D for all experts; its waves share
-//    the (expert, piece of F) units. A wave adds what it has of a token to its
-//    own fp32 sums in LDS, and the waves' sums are added in order at the end: no
-//    partial output in memory and no atomics, so the same inputs give the same
-//    bits.
+//  - k_moe_down: the workgroups share the tiles of 16 rows of D, each for all
+//    experts, evenly; the waves share a tile's (expert, piece of F) units. A wave
+//    adds what it has of a token to its own fp32 sums in LDS, the waves' sums are
+//    added in order, and so are those of workgroups that share a tile: the same
+//    inputs give the same bits.
 // A wave's unit of work is 16 rows (k_moe_up: twice 16) x 128 values of the
 // contraction and the same 128 values of its tokens; the loads of the next
 // units are in flight while one is multiplied. An expert's tokens are compacted
@@ -44,14 +44,18 @@ namespace {
 constexpr int kUpWaves = 4;
 constexpr int kUpBlocks = 512;  // two a CU
 constexpr int kDownWaves = 8;
+constexpr int kDownBlocks = 512;  // two a CU
 constexpr int kFewT = 64;
 constexpr int kFewK = 32;
 
 // What k_moe_up leaves in the workspace for k_moe_down: a, an expert's part at
 // start * F, in it value f of its i-th of m tokens at ((f / 8) m + i) 8 + f % 8;
 // the number of named experts; each one's id, in order, where its pairs begin,
-// and the tokens of the pairs.
+// and the tokens of the pairs. k_moe_down joins split sums by `done` (counters
+// that k_moe_up clears) and `part` ([workgroup][first or last tile][T][16]).
 struct FewMeta {
+  float* part;       // [kDownBlocks][2][T * 16]
+  uint32_t* done;    // [kDownBlocks]
   int32_t* head;     // [0]: the number of experts
   uint16_t* expert;  // [T * k]
   uint16_t* start;   // [T * k + 1]
@@ -59,7 +63,9 @@ struct FewMeta {
 };
 __host__ __device__ inline FewMeta few_meta(uint16_t* act, int64_t T, int k, int64_t F) {
   FewMeta m;
-  m.head = reinterpret_cast<int32_t*>(act + T * k * F);
+  m.part = reinterpret_cast<float*>(act + T * k * F);
+  m.done = reinterpret_cast<uint32_t*>(m.part + kDownBlocks * 2 * T * 16);
+  m.head = reinterpret_cast<int32_t*>(m.done + kDownBlocks);
   m.expert = reinterpret_cast<uint16_t*>(m.head + 1);
   m.start = m.expert + T * k;
   m.token = m.start + T * k + 1;
@@ -67,7 +73,9 @@ __host__ __device__ inline FewMeta few_meta(uint16_t* act, int64_t T, int k, int
 }
 }  // namespace
 
-size_t moe_few_ws_bytes(int64_t T, int k, int64_t F) { return (size_t)(T * k) * (2 * F + 6) + 8; }
+size_t moe_few_ws_bytes(int64_t T, int k, int64_t F) {
+  return (size_t)(T * k) * (2 * F + 6) + 8 + kDownBlocks * (size_t)(4 + 2 * T * 64);
+}
 
 // Eight e4m3 codes -> eight bf16 (every e4m3 value is a bf16 value).
 __device__ __forceinline__ v8bf decode8(uint32_t d0, uint32_t d1) {
@@ -89,40 +97,38 @@ __device__ __forceinline__ void wave_lds_fence() {
 
 // ---- one unit's operands --------------------------------------------------------
 //
+// A unit is the values [128 u, 128 u + 128) of the contraction, of length K; the
+// last one may hold fewer, a multiple of 16. Every load is unconditional, so that
+// the compiler knows how many are in flight and waits for the oldest unit alone:
+// a lane whose piece would lie behind K loads the unit's first piece, and
+// mask_unit takes its values out.
+//
 // A tile of codes, 16 rows x 128 values, as two 16-byte loads a lane. Packed:
 // the lanes' own operands, row l & 15 and values 16 (l >> 4) .. + 15 of each 64
 // (1 KB chunks of 16 x 64, one behind the other along the contraction).
 // Row-major: load i has rows 8 i + (l >> 3), 16 bytes l & 7, and goes through LDS.
 template <bool PACKED>
-__device__ __forceinline__ uint32_t code_off(int64_t K) {
-  const int l = threadIdx.x & 63;
-  return PACKED ? (l & 15) * 64 + (l >> 4) * 16 : (l >> 3) * (uint32_t)K + (l & 7) * 16;
-}
-// base: the tile's first row at the unit's first value
-template <bool PACKED>
-__device__ __forceinline__ void load_codes(uint4 (&w)[2], const uint8_t* tile, uint32_t off, int u, int K) {
-  const int l = threadIdx.x & 63;
-  if constexpr (PACKED) {
-    const uint8_t* p = tile + (int64_t)u * 2048;
-    w[0] = ld_nt16(p + off);
-    if (128 * u + 64 < K)  // K % 64 == 0: the last unit may be half
-      w[1] = ld_nt16(p + 1024 + off);
-    else
-      w[1] = make_uint4(0, 0, 0, 0);
-  } else {
-    const uint8_t* p = tile + 128 * u;
-    if (128 * (u + 1) <= K) {
-      w[0] = *reinterpret_cast<const uint4*>(p + off);
-      w[1] = *reinterpret_cast<const uint4*>(p + 8 * (int64_t)K + off);
+struct Codes {
+  uint32_t off, last;  // the lane's offset, and in the last unit
+  __device__ __forceinline__ explicit Codes(int K) {
+    const int l = threadIdx.x & 63, c = l & 7, rest = K - (K - 1) / 128 * 128;
+    off = PACKED ? (l & 15) * 64 + (l >> 4) * 16 : (l >> 3) * (uint32_t)K + c * 16;
+    last = PACKED || 16 * c < rest ? off : off - 16 * c;
+  }
+  // tile: the first of the 16 rows
+  __device__ __forceinline__ void load(uint4 (&w)[2], const uint8_t* tile, int u, int K) const {
+    if constexpr (PACKED) {
+      const uint8_t* p = tile + (int64_t)u * 2048;
+      w[0] = ld_nt16(p + off);
+      w[1] = ld_nt16(p + (128 * u + 64 < K ? 1024 : 0) + off);  // K % 64 == 0: the last unit may be half
     } else {
-      w[0] = w[1] = make_uint4(0, 0, 0, 0);
-      if (128 * u + 16 * (l & 7) < K) {
-        w[0] = *reinterpret_cast<const uint4*>(p + off);
-        w[1] = *reinterpret_cast<const uint4*>(p + 8 * (int64_t)K + off);
-      }
+      const uint8_t* p = tile + 128 * u;
+      const uint32_t o = 128 * (u + 1) <= K ? off : last;
+      w[0] = *reinterpret_cast<const uint4*>(p + o);
+      w[1] = *reinterpret_cast<const uint4*>(p + 8 * (int64_t)K + o);
     }
   }
-}
+};
 // The lanes' operands of a loaded tile. Row-major, through 2 KB of LDS: row r's
 // piece c lies at r * 128 + 16 (c ^ (r / 2 % 8)), so that the 16 rows of a
 // column of pieces fall on all banks.
@@ -140,43 +146,48 @@ __device__ __forceinline__ void turn_codes(uint4 (&w)[2], uint8_t* lds) {
   }
 }
 
-// A tile of x, 16 tokens x 128 values: load i has tokens 4 i + (l >> 4), 16
-// bytes l & 15. Loads of tokens past the last are left out.
+// A tile of tokens, 16 x 128 values. Rows of x: load i has tokens 4 i + (l >> 4),
+// 16 bytes l & 15, and goes through 4 KB of LDS: token r's piece c lies at
+// r * 256 + 16 (c ^ r). The operand of matrix instruction q is piece
+// 8 (q / 2) + 2 (l >> 4) + q % 2 of token l & 15, the values of the codes' bytes
+// 8 (q % 2) .. + 7 of load q / 2.
 struct RowTile {
   v8bf v[4];
 };
-__device__ __forceinline__ void load_rows(RowTile& x, const uint16_t* base, const uint32_t (&off)[4], int n, int u,
-                                          int K) {
-  const int l = threadIdx.x & 63;
+__device__ __forceinline__ void load_rows(RowTile& x, const uint16_t* base, const uint32_t (&off)[4], uint32_t back,
+                                          int u, int K) {
   const uint8_t* p = reinterpret_cast<const uint8_t*>(base + 128 * u);
+  const uint32_t o = 128 * (u + 1) <= K ? 0 : back;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (4 * i >= n) break;
-    if (128 * (u + 1) <= K) {
-      x.v[i] = *reinterpret_cast<const v8bf*>(p + off[i]);
-    } else {
-      x.v[i] = (v8bf){};
-      if (128 * u + 8 * (l & 15) < K) x.v[i] = *reinterpret_cast<const v8bf*>(p + off[i]);
-    }
-  }
+  for (int i = 0; i < 4; ++i) x.v[i] = *reinterpret_cast<const v8bf*>(p + (off[i] - o));
 }
-// Through 4 KB of LDS: token r's piece c lies at r * 256 + 16 (c ^ r). The
-// operand of matrix instruction q is piece 8 (q / 2) + 2 (l >> 4) + q % 2 of
-// token l & 15, the values of the codes' bytes 8 (q % 2) .. + 7 of load q / 2.
-__device__ __forceinline__ void turn_rows(RowTile& x, int n, uint8_t* lds) {
+__device__ __forceinline__ void turn_rows(RowTile& x, uint8_t* lds) {
   const int l = threadIdx.x & 63, lr = l & 15, kg = l >> 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (4 * i >= n) break;
     const int r = 4 * i + kg;
     *reinterpret_cast<v8bf*>(lds + r * 256 + 16 * (lr ^ r)) = x.v[i];
   }
   wave_lds_fence();
-  // tokens past the last are whatever LDS holds: columns that nobody reads
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     x.v[q] = *reinterpret_cast<const v8bf*>(lds + lr * 256 + 16 * ((8 * (q >> 1) + 2 * kg + (q & 1)) ^ lr));
   wave_lds_fence();
+}
+
+// Zeros for the values of the last unit that lie behind K.
+template <int R, int NT>
+__device__ __forceinline__ void mask_unit(uint4 (&w)[R][2], RowTile (&x)[NT], int u, int K) {
+  if (128 * (u + 1) <= K) return;
+  const int kg = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (128 * u + 64 * h + 16 * kg < K) continue;
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[r][h] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[n].v[2 * h] = x[n].v[2 * h + 1] = (v8bf){};
+  }
 }
 
 // The products of R tiles of codes with NT tiles of tokens.
@@ -217,6 +228,8 @@ __device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const RowTile (
 // 16 a tile of tokens, stay below 128.
 template <int NT>
 constexpr int kInFlight = NT == 1 ? 3 : NT == 2 ? 2 : 1;
+template <int NT>
+constexpr int kInFlightDown = NT == 1 ? 2 : 1;
 
 // The ids in LDS and a bit for each expert that some token names.
 __device__ __forceinline__ void few_ids(const int32_t* __restrict__ ids, int n, int E, int32_t* sid, uint32_t* bits) {
@@ -278,49 +291,46 @@ __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, 
   const int lr = lane & 15, kg = lane >> 4;
   const uint8_t* wb = p.w13 + (int64_t)e * 2 * p.F * p.D;
   const float* sc = p.inv13 + (int64_t)e * 2 * p.F + (lane & 16 ? p.F : 0) + f0 + lr;
-  const uint32_t woff = code_off<PACKED>(p.D);
+  const int D = (int)p.D;
+  const Codes<PACKED> codes(D);
+  // a lane without a token has the first one's values: a column that nobody reads
   uint32_t xoff[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int it = 16 * n + 4 * i + kg < m ? 16 * n + 4 * i + kg : 0;
-      xoff[n][i] = 2 * ((uint32_t)(sh.list[it] / p.k) * (uint32_t)p.D + 8 * lr);
+      xoff[n][i] = 2 * ((uint32_t)(sh.list[it] / p.k) * (uint32_t)D + 8 * lr);
     }
   }
-  const int units = (int)((p.D + 127) / 128);
+  const uint32_t back = 8 * lr < D - (D - 1) / 128 * 128 ? 0 : 16 * lr;
+  const int units = (D + 127) / 128;
   const int u0 = units * wave / kUpWaves, nu = units * (wave + 1) / kUpWaves - u0;
   uint4 w[P][2][2];
   RowTile x[P][NT];
   auto load = [&](uint4 (&dw)[2][2], RowTile (&dx)[NT], int tile, int u) {
-    load_codes<PACKED>(dw[0], wb + (f0 + 16 * tile) * p.D, woff, u0 + u, (int)p.D);
-    load_codes<PACKED>(dw[1], wb + (p.F + f0 + 16 * tile) * p.D, woff, u0 + u, (int)p.D);
+    codes.load(dw[0], wb + (f0 + 16 * tile) * p.D, u, D);
+    codes.load(dw[1], wb + (p.F + f0 + 16 * tile) * p.D, u, D);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) load_rows(dx[n], p.x, xoff[n], m - 16 * n, u0 + u, (int)p.D);
+    for (int n = 0; n < NT; ++n) load_rows(dx[n], p.x, xoff[n], back, u, D);
   };
-  float scale = wave == 0 && lane < 32 ? sc[0] : 0.0f;
-#pragma unroll
-  for (int i = 0; i < P; ++i)
-    if (i < nu) load(w[i], x[i], 0, i);
-  uint8_t* mine = turn + wave * 4096;
-  for (int tile = 0; tile < nt; ++tile) {
-    const float next = wave == 0 && lane < 32 && tile + 1 < nt ? sc[16 * (tile + 1)] : 0.0f;
-    v4f acc[2][NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[0][n] = acc[1][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-    for (int u = 0; u < nu; u += P) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        if (u + i >= nu) break;
-        turn_codes<PACKED>(w[i][0], mine);
-        turn_codes<PACKED>(w[i][1], mine);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) turn_rows(x[i][n], m - 16 * n, mine);
-        multiply<2, NT>(w[i], x[i], acc);
-        const bool here = u + i + P < nu;
-        if (here || tile + 1 < nt) load(w[i], x[i], tile + !here, here ? u + i + P : i);
-      }
+  float scale = sc[0];
+  // the load side: the tile and unit of the next load; it stays at the last one
+  int lt = 0, lu = 0;
+  auto advance = [&]() {
+    if (lu + 1 < nu) {
+      ++lu;
+    } else if (lt + 1 < nt) {
+      lu = 0;
+      ++lt;
     }
+  };
+  uint8_t* mine = turn + wave * 4096;
+  v4f acc[2][NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[0][n] = acc[1][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+  int tile = 0;
+  auto finish = [&]() {
     // The waves' partial sums (and the rows' scales), in one of two buffers: a
     // wave writes it again two tiles on, behind a barrier that the reader
     // reaches after reading. Four token tiles have one buffer, which lets two
@@ -330,41 +340,75 @@ __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, 
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int z = 0; z < 2; ++z)
+      for (int z = 0; z < 2; ++z) {
         r[((2 * n + z) * kUpWaves + wave) * 64 + lane] =
             make_float4(acc[z][n][0], acc[z][n][1], acc[z][n][2], acc[z][n][3]);
+        acc[z][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+      }
     }
     if (wave == 0 && lane < 32) sh.scale[tile & 1][lane] = scale;
-    scale = next;
+    scale = sc[16 * (tile + 1 < nt ? tile + 1 : tile)];
     __syncthreads();
     const int n = (wave + tile) % kUpWaves;  // the waves finish token tiles in turn
     const int item = 16 * n + lr;
-    if (n >= NT || item >= m) continue;
-    float g[4] = {0, 0, 0, 0}, uu[4] = {0, 0, 0, 0};
+    if (n < NT && item < m) {
+      float g[4] = {0, 0, 0, 0}, uu[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < kUpWaves; ++i) {
-      const float4 a = r[((2 * n) * kUpWaves + i) * 64 + lane];
-      const float4 b = r[((2 * n + 1) * kUpWaves + i) * 64 + lane];
-      g[0] += a.x;
-      g[1] += a.y;
-      g[2] += a.z;
-      g[3] += a.w;
-      uu[0] += b.x;
-      uu[1] += b.y;
-      uu[2] += b.z;
-      uu[3] += b.w;
-    }
-    const float gate = sh.gate[item];
-    float v[4];
+      for (int i = 0; i < kUpWaves; ++i) {
+        const float4 a = r[((2 * n) * kUpWaves + i) * 64 + lane];
+        const float4 b = r[((2 * n + 1) * kUpWaves + i) * 64 + lane];
+        g[0] += a.x;
+        g[1] += a.y;
+        g[2] += a.z;
+        g[3] += a.w;
+        uu[0] += b.x;
+        uu[1] += b.y;
+        uu[2] += b.z;
+        uu[3] += b.w;
+      }
+      const float gate = sh.gate[item];
+      float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float gv = g[i] * sh.scale[tile & 1][4 * kg + i], uv = uu[i] * sh.scale[tile & 1][16 + 4 * kg + i];
-      v[i] = gate * (gv / (1.0f + expf(-gv)) * uv);
+      for (int i = 0; i < 4; ++i) {
+        const float gv = g[i] * sh.scale[tile & 1][4 * kg + i], uv = uu[i] * sh.scale[tile & 1][16 + 4 * kg + i];
+        v[i] = gate * (gv / (1.0f + expf(-gv)) * uv);
+      }
+      const v2bf lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
+      const int64_t f = f0 + 16 * tile + 4 * kg;
+      *reinterpret_cast<uint2*>(p.act + act0 * p.F + ((f >> 3) * m + item) * 8 + (f & 7)) =
+          make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
     }
-    const v2bf lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
-    const int64_t f = f0 + 16 * tile + 4 * kg;
-    *reinterpret_cast<uint2*>(p.act + act0 * p.F + ((f >> 3) * m + item) * 8 + (f & 7)) =
-        make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+    ++tile;
+  };
+  if (nu == 0) {  // fewer units than waves: this wave has zeros to add
+    while (tile < nt) finish();
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    load(w[i], x[i], lt, u0 + lu);
+    advance();
+  }
+  // the multiply side. No way out between the slots, so that the loads in flight
+  // are the same at each: behind the last unit the slots hold it again, and what
+  // they add to acc is not read
+  int cu = 0;
+  for (int left = nu * nt; left > 0; left -= P) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      turn_codes<PACKED>(w[i][0], mine);
+      turn_codes<PACKED>(w[i][1], mine);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) turn_rows(x[i][n], mine);
+      mask_unit<2, NT>(w[i], x[i], u0 + cu, D);
+      multiply<2, NT>(w[i], x[i], acc);
+      load(w[i], x[i], lt, u0 + lu);
+      advance();
+      if (++cu == nu && i < left) {
+        cu = 0;
+        finish();
+      }
+    }
   }
 }
 
@@ -381,7 +425,10 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeFewArgs p) {
   few_ids(p.ids, n, p.E, sh.sid, sh.bits);
   const int nact = __builtin_amdgcn_readlane(few_count(lane < 32 ? sh.bits[lane] : 0), 31);
   const FewMeta meta = few_meta(p.act, p.T, p.k, p.F);
-  if (blockIdx.x == 0 && threadIdx.x == 0) meta.head[0] = nact;
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) meta.head[0] = nact;
+    for (int i = threadIdx.x; i < kDownBlocks; i += 64 * kUpWaves) meta.done[i] = 0;
+  }
   const int per = (int)(p.F / 16);
   const int64_t all = (int64_t)nact * per;
   int64_t tile = all * blockIdx.x / gridDim.x;
@@ -457,65 +504,80 @@ struct DownShared {
 template <int NT, bool PACKED>
 __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShared& sh, int64_t d0, int units, int i,
                                              int end, float* sum, uint8_t* turn) {
-  constexpr int P = kInFlight<NT>;
-  const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4;
+  constexpr int P = kInFlightDown<NT>;
+  const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4, F = (int)p.F;
   uint4 w[P][1][2];
   RowTile x[P][NT];
-  float4 sc[P];
-  const uint32_t woff = code_off<PACKED>(p.F);
-  // the load side: the expert and unit of the next load, and its pointers
-  int la = i / units, lu = i % units, m = 0;
+  const Codes<PACKED> codes(F);
+  // the load side: the expert and unit of the next load, and its pointers; it
+  // stays at the run's last unit
+  int la = i / units, lu = i % units, more = end - i - 1, m = 0;
   const uint8_t* wp = nullptr;
   const uint16_t* ap = nullptr;
-  const float* sp = nullptr;
+  uint32_t aoff[NT][4];  // bytes from a unit's first group of 8 values x m tokens
   auto point = [&]() {
     const int64_t e = __builtin_amdgcn_readfirstlane(sh.expert[la]);
     const int b = __builtin_amdgcn_readfirstlane(sh.start[la]);
     m = __builtin_amdgcn_readfirstlane(sh.start[la + 1]) - b;
     wp = p.w2 + (e * p.D + d0) * p.F;
     ap = p.act + (int64_t)b * p.F;
-    sp = p.inv2 + e * p.D + d0;
-  };
-  auto load = [&](uint4 (&dw)[1][2], RowTile (&dx)[NT], float4& c, bool last) {
-    load_codes<PACKED>(dw[0], wp, woff, lu, (int)p.F);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      // lanes without a token read the last one's value: a column nobody reads
+      // a lane without a token has the last one's values: a column that nobody reads
       const int item = 16 * n + lr < m ? 16 * n + lr : m - 1;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int g = 16 * lu + 8 * (q >> 1) + 2 * kg + (q & 1);
-        if (128 * (lu + 1) <= (int)p.F) {
-          dx[n].v[q] = *reinterpret_cast<const v8bf*>(ap + (uint32_t)(8 * (g * m + item)));
-        } else {
-          dx[n].v[q] = (v8bf){};
-          if (8 * g < (int)p.F) dx[n].v[q] = *reinterpret_cast<const v8bf*>(ap + (uint32_t)(8 * (g * m + item)));
-        }
-      }
-    }
-    ++lu;
-    if (lu == units || last) c = make_float4(sp[4 * kg], sp[4 * kg + 1], sp[4 * kg + 2], sp[4 * kg + 3]);
-    if (lu == units && !last) {
-      lu = 0;
-      ++la;
-      point();
+      for (int q = 0; q < 4; ++q) aoff[n][q] = 16 * ((8 * (q >> 1) + 2 * kg + (q & 1)) * m + item);
     }
   };
-  int ca = la, cu = lu;  // the multiply side
+  auto load = [&](uint4 (&dw)[1][2], RowTile (&dx)[NT]) {
+    codes.load(dw[0], wp, lu, F);
+    const uint8_t* u = reinterpret_cast<const uint8_t*>(ap) + (int64_t)lu * 256 * m;
+    const bool full = 128 * (lu + 1) <= F;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // behind F: group 0 of the unit
+        const uint32_t o = full || 128 * lu + 64 * (q >> 1) + 16 * kg < F ? aoff[n][q] : 0;
+        dx[n].v[q] = *reinterpret_cast<const v8bf*>(u + o);
+      }
+    }
+    if (more > 0) {
+      --more;
+      if (++lu == units) {
+        lu = 0;
+        ++la;
+        point();
+      }
+    }
+  };
+  // the multiply side; no way out between the slots, as in moe_up_tiles
+  int ca = la, cu = lu;
   point();
 #pragma unroll
-  for (int j = 0; j < P; ++j)
-    if (i + j < end) load(w[j], x[j], sc[j], i + j + 1 == end);
+  for (int j = 0; j < P; ++j) load(w[j], x[j]);
   v4f acc[1][NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) acc[0][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  for (; i < end; i += P) {
+  for (int left = end - i; left > 0; left -= P) {
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      if (i + j >= end) break;
       turn_codes<PACKED>(w[j][0], turn);
+      mask_unit<1, NT>(w[j], x[j], cu, F);
       multiply<1, NT>(w[j], x[j], acc);
-      if (++cu == units || i + j + 1 == end) {
+      load(w[j], x[j]);
+      if (j < left && (++cu == units || j + 1 == left)) {
+        // the rows' scales through the scalar cache, past the loads in flight
+        typedef const __attribute__((address_space(4))) float* ScalarPtr;
+        const ScalarPtr sp =
+            (ScalarPtr)(uintptr_t)(p.inv2 + (int64_t)__builtin_amdgcn_readfirstlane(sh.expert[ca]) * p.D + d0);
+        float c[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          float v[4] = {sp[z], sp[4 + z], sp[8 + z], sp[12 + z]};
+          asm("" : "+s"(v[0]), "+s"(v[1]), "+s"(v[2]), "+s"(v[3]));  // loaded as scalars, then chosen by lane
+          c[z] = kg < 2 ? (kg == 0 ? v[0] : v[1]) : (kg == 2 ? v[2] : v[3]);
+        }
         const int b = sh.start[ca], mc = sh.start[ca + 1] - b;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -523,10 +585,10 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
           if (16 * n + lr < mc) {
             float4* d = reinterpret_cast<float4*>(sum + sh.token[b + 16 * n + lr] * 16 + 4 * kg);
             float4 v = *d;
-            v.x += acc[0][n][0] * sc[j].x;
-            v.y += acc[0][n][1] * sc[j].y;
-            v.z += acc[0][n][2] * sc[j].z;
-            v.w += acc[0][n][3] * sc[j].w;
+            v.x += acc[0][n][0] * c[0];
+            v.y += acc[0][n][1] * c[1];
+            v.z += acc[0][n][2] * c[2];
+            v.w += acc[0][n][3] * c[3];
             *d = v;
           }
           acc[0][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
@@ -534,13 +596,16 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
         cu = 0;
         ++ca;
       }
-      if (i + j + P < end) load(w[j], x[j], sc[j], i + j + P + 1 == end);
     }
   }
 }
 
+// The workgroups share the (16 rows, expert, unit) triples evenly, so a
+// workgroup has an end of a tile of rows, whole ones, and a beginning. The sums
+// of a tile that several share meet in memory, and the one that comes last adds
+// them, in the workgroups' order. Where a tile has few units it is not split.
 template <int NTM, bool PACKED>
-__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeFewArgs p) {
+__global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(MoeFewArgs p) {
   constexpr int kTok = 16 * NTM;
   __shared__ float4 sums[kDownWaves * kTok * 4];  // [wave][token][16]
   __shared__ __align__(16) uint8_t turn[PACKED ? 16 : kDownWaves * 2048];
@@ -548,7 +613,6 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeFewArgs p) {
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const FewMeta meta = few_meta(p.act, p.T, p.k, p.F);
   const int n = (int)p.T * p.k, slots = n < p.E ? n : p.E;
-  for (int i = threadIdx.x; i < kDownWaves * kTok * 4; i += 64 * kDownWaves) sums[i] = make_float4(0, 0, 0, 0);
   // all that the workspace may hold of the lists; k_moe_up wrote the parts that are used
   for (int i = threadIdx.x; i < n; i += 64 * kDownWaves) {
     sh.token[i] = meta.token[i];
@@ -561,49 +625,105 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(MoeFewArgs p) {
   int most = 0;  // the largest number of tokens of an expert
   for (int a = lane; a < nact; a += 64) most = max(most, sh.start[a + 1] - sh.start[a]);
   const bool over16 = __ballot(most > 16) != 0, over32 = __ballot(most > 32) != 0;
-  const int64_t d0 = 16 * (int64_t)blockIdx.x;
   const int units = (int)((p.F + 127) / 128);
-  const int64_t all = (int64_t)nact * units;
-  const int i0 = (int)(all * wave / kDownWaves), i1 = (int)(all * (wave + 1) / kDownWaves);
-  float* sum = reinterpret_cast<float*>(&sums[wave * kTok * 4]);
-  uint8_t* mine = PACKED ? turn : turn + wave * 2048;
-  if (i0 < i1) {
-    bool done = false;
-    if constexpr (NTM >= 4) {
-      if (over32) {
-        moe_down_run<4, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
-        done = true;
-      }
-    }
-    if constexpr (NTM >= 2) {
-      if (!done && over16) {
-        moe_down_run<2, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
-        done = true;
-      }
-    }
-    if (!done) moe_down_run<1, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
+  const int64_t tiles = p.D / 16, per = (int64_t)nact * units, all = tiles * per;
+  if (nact == 0) {  // no token has an expert: zeros
+    for (int64_t i = (int64_t)blockIdx.x * 64 * kDownWaves + threadIdx.x; i < p.T * p.D / 8;
+         i += (int64_t)gridDim.x * 64 * kDownWaves)
+      reinterpret_cast<uint4*>(p.out)[i] = make_uint4(0, 0, 0, 0);
+    return;
   }
-  __syncthreads();
-  const int t = threadIdx.x >> 2, q = threadIdx.x & 3;
-  if (t >= (int)p.T) return;
-  float r[4] = {0, 0, 0, 0};
+  int64_t share = (all + gridDim.x - 1) / gridDim.x;
+  if (share < kDownWaves * 4) share = kDownWaves * 4;
+  if (share < per && per <= kDownWaves * 8) share = per;
+  int64_t i = share * blockIdx.x;
+  const int64_t end = i + share < all ? i + share : all;
+  const int t = threadIdx.x >> 2, q = threadIdx.x & 3;  // the values that this thread adds up
+  const bool adds = t < (int)p.T;
+  while (i < end) {
+    const int64_t tile = i / per, d0 = 16 * tile;
+    const int from = (int)(i - tile * per);
+    const int to = (int)(end - tile * per < per ? end - tile * per : per);
+    float* sum = reinterpret_cast<float*>(&sums[wave * kTok * 4]);
+    for (int z = lane; z < kTok * 4; z += 64) sums[wave * kTok * 4 + z] = make_float4(0, 0, 0, 0);
+    wave_lds_fence();
+    const int i0 = from + (int)((int64_t)(to - from) * wave / kDownWaves);
+    const int i1 = from + (int)((int64_t)(to - from) * (wave + 1) / kDownWaves);
+    uint8_t* mine = PACKED ? turn : turn + wave * 2048;
+    if (i0 < i1) {
+      bool done = false;
+      if constexpr (NTM >= 4) {
+        if (over32) {
+          moe_down_run<4, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
+          done = true;
+        }
+      }
+      if constexpr (NTM >= 2) {
+        if (!done && over16) {
+          moe_down_run<2, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
+          done = true;
+        }
+      }
+      if (!done) moe_down_run<1, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
+    }
+    __syncthreads();
+    float r[4] = {0, 0, 0, 0};
+    if (adds) {
 #pragma unroll
-  for (int w = 0; w < kDownWaves; ++w) {
-    const float4 a = sums[(w * kTok + t) * 4 + q];
-    r[0] += a.x;
-    r[1] += a.y;
-    r[2] += a.z;
-    r[3] += a.w;
+      for (int w = 0; w < kDownWaves; ++w) {
+        const float4 a = sums[(w * kTok + t) * 4 + q];
+        r[0] += a.x;
+        r[1] += a.y;
+        r[2] += a.z;
+        r[3] += a.w;
+      }
+    }
+    bool write = true;
+    if (to - from < per) {
+      // the workgroups that share this tile, from b0 to b1; b0 has its counter
+      const int64_t b0 = tile * per / share, b1 = ((tile + 1) * per - 1) / share;
+      auto slot = [&](int64_t b) {
+        const int64_t first = share * b / per;  // a workgroup's first tile
+        return meta.part + (2 * b + (tile != first)) * p.T * 16;
+      };
+      if (adds) {
+        float* d = slot(blockIdx.x) + t * 16 + 4 * q;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) __hip_atomic_store(d + z, r[z], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      // Every value that crosses workgroups is stored and loaded by an atomic of
+      // agent scope, which reaches the memory that all XCDs share, so no cache
+      // has to be written back or emptied; the wait has the stores there before
+      // the barrier, and the count goes up behind it.
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (threadIdx.x == 0)
+        sh.count = (int)__hip_atomic_fetch_add(&meta.done[b0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      write = sh.count == (int)(b1 - b0);
+      if (write && adds) {
+        r[0] = r[1] = r[2] = r[3] = 0.0f;
+        for (int64_t b = b0; b <= b1; ++b) {
+          const float* d = slot(b) + t * 16 + 4 * q;
+#pragma unroll
+          for (int z = 0; z < 4; ++z) r[z] += __hip_atomic_load(d + z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+      }
+    }
+    if (write && adds) {
+      const v2bf lo = {(__bf16)r[0], (__bf16)r[1]}, hi = {(__bf16)r[2], (__bf16)r[3]};
+      *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.D + d0 + 4 * q) =
+          make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+    }
+    i += to - from;
+    if (i < end) __syncthreads();  // the sums are read before they are cleared
   }
-  const v2bf lo = {(__bf16)r[0], (__bf16)r[1]}, hi = {(__bf16)r[2], (__bf16)r[3]};
-  *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.D + d0 + 4 * q) =
-      make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
 }
 
 template <bool PACKED>
 static hipError_t launch_few_t(const MoeFewArgs& a) {
   const int64_t pairs = a.T * a.k, most = (pairs < a.E ? pairs : a.E) * (a.F / 16);
-  const dim3 gu((unsigned)(most < kUpBlocks ? most : kUpBlocks)), gd((unsigned)(a.D / 16));
+  const dim3 gu((unsigned)(most < kUpBlocks ? most : kUpBlocks)), gd(kDownBlocks);
   const dim3 bu(64 * kUpWaves), bd(64 * kDownWaves);
   auto go = [&](auto up, auto down) {
     hipLaunchKernelGGL(up, gu, bu, 0, a.stream, a);
