@@ -24,11 +24,12 @@
 //
 // After HBM the loads' own rate is the next bound: measured, a 16-byte load of
 // a wavefront takes 17 clocks of its CU's load path where each four neighbouring
-// lanes read 64 bytes in a row, 33 where they read 64-byte steps (a packed chunk
-// as the matrix instruction's lanes want it) and 65 where they read four rows.
-// So rows (x, row-major codes) are loaded with neighbouring lanes along the
-// row and turned in a wave's own piece of LDS, and a is written in the order in
-// which k_moe_down's lanes read it.
+// lanes read an aligned 64 bytes, 33 where they read 64-byte steps (a packed
+// chunk as the matrix instruction's lanes want it) and 65 where they read four
+// rows. So codes and rows of x are loaded with neighbouring lanes along the row
+// and turned in a wave's own piece of LDS, a is written in the order in which
+// k_moe_down reads it, and tokens are loaded by fours: one load of a unit
+// for up to 4 tokens of an expert, two up to 8.
 //
 // The rounding of a to bf16 (with its gate weight, half a step: 2^-8 relative)
 // is that of the activations the grouped GEMMs take; everything else is fp32
@@ -36,6 +37,8 @@
 //
 // A token may name an expert twice: its first slot carries the sum of the
 // weights. Ids outside [0, E) name none.
+#include <type_traits>
+
 #include "gemm_common.hpp"
 
 namespace fp8dyn {
@@ -49,8 +52,8 @@ constexpr int kFewT = 64;
 constexpr int kFewK = 32;
 
 // What k_moe_up leaves in the workspace for k_moe_down: a, an expert's part at
-// start * F, in it value f of its i-th of m tokens at ((f / 8) m + i) 8 + f % 8;
-// the number of named experts; each one's id, in order, where its pairs begin,
+// 4 start F (room for m tokens, rounded up to a multiple mp of four), in it value
+// f of its i-th token at ((f / 8) mp + i) 8 + f % 8; the number of named experts; each one's id, in order, where its pairs begin,
 // and the tokens of the pairs. k_moe_down joins split sums by `done` (counters
 // that k_moe_up clears) and `part` ([workgroup][first or last tile][T][16]).
 struct FewMeta {
@@ -63,7 +66,7 @@ struct FewMeta {
 };
 __host__ __device__ inline FewMeta few_meta(uint16_t* act, int64_t T, int k, int64_t F) {
   FewMeta m;
-  m.part = reinterpret_cast<float*>(act + T * k * F);
+  m.part = reinterpret_cast<float*>(act + 4 * T * k * F);
   m.done = reinterpret_cast<uint32_t*>(m.part + kDownBlocks * 2 * T * 16);
   m.head = reinterpret_cast<int32_t*>(m.done + kDownBlocks);
   m.expert = reinterpret_cast<uint16_t*>(m.head + 1);
@@ -74,7 +77,7 @@ __host__ __device__ inline FewMeta few_meta(uint16_t* act, int64_t T, int k, int
 }  // namespace
 
 size_t moe_few_ws_bytes(int64_t T, int k, int64_t F) {
-  return (size_t)(T * k) * (2 * F + 6) + 8 + kDownBlocks * (size_t)(4 + 2 * T * 64);
+  return (size_t)(T * k) * (8 * F + 6) + 8 + kDownBlocks * (size_t)(4 + 2 * T * 64);
 }
 
 // Eight e4m3 codes -> eight bf16 (every e4m3 value is a bf16 value).
@@ -104,15 +107,15 @@ __device__ __forceinline__ void wave_lds_fence() {
 // mask_unit takes its values out.
 //
 // A tile of codes, 16 rows x 128 values, as two 16-byte loads a lane. Packed:
-// the lanes' own operands, row l & 15 and values 16 (l >> 4) .. + 15 of each 64
-// (1 KB chunks of 16 x 64, one behind the other along the contraction).
-// Row-major: load i has rows 8 i + (l >> 3), 16 bytes l & 7, and goes through LDS.
+// load h is the 1 KB chunk of 64 values, row l >> 2, 16 bytes l & 3 (the chunks
+// follow each other along the contraction). Row-major: load i has rows
+// 8 i + (l >> 3), 16 bytes l & 7.
 template <bool PACKED>
 struct Codes {
   uint32_t off, last;  // the lane's offset, and in the last unit
   __device__ __forceinline__ explicit Codes(int K) {
     const int l = threadIdx.x & 63, c = l & 7, rest = K - (K - 1) / 128 * 128;
-    off = PACKED ? (l & 15) * 64 + (l >> 4) * 16 : (l >> 3) * (uint32_t)K + c * 16;
+    off = PACKED ? l * 16 : (l >> 3) * (uint32_t)K + c * 16;
     last = PACKED || 16 * c < rest ? off : off - 16 * c;
   }
   // tile: the first of the 16 rows
@@ -129,55 +132,73 @@ struct Codes {
     }
   }
 };
-// The lanes' operands of a loaded tile. Row-major, through 2 KB of LDS: row r's
-// piece c lies at r * 128 + 16 (c ^ (r / 2 % 8)), so that the 16 rows of a
-// column of pieces fall on all banks.
+// The lanes' operands of a loaded tile, row l & 15 and values 16 (l >> 4) .. + 15
+// of each 64, through 2 KB of LDS. Pieces of 16 bytes are placed so that the 16
+// rows of a column of pieces fall on all banks: packed, row r's piece c of a
+// chunk at r * 64 + 16 (c ^ (r / 4)); row-major, at r * 128 + 16 (c ^ (r / 2 % 8)).
 template <bool PACKED>
 __device__ __forceinline__ void turn_codes(uint4 (&w)[2], uint8_t* lds) {
-  if constexpr (!PACKED) {
-    const int l = threadIdx.x & 63, lr = l & 15, kg = l >> 4;
+  const int l = threadIdx.x & 63, lr = l & 15, kg = l >> 4;
+  if constexpr (PACKED) {
+    const int r = l >> 2, c = l & 3;
+    uint8_t* d = lds + r * 64 + 16 * (c ^ (r >> 2));
+    *reinterpret_cast<uint4*>(d) = w[0];
+    *reinterpret_cast<uint4*>(d + 1024) = w[1];
+    wave_lds_fence();
+    const uint8_t* q = lds + lr * 64 + 16 * (kg ^ (lr >> 2));
+    w[0] = *reinterpret_cast<const uint4*>(q);
+    w[1] = *reinterpret_cast<const uint4*>(q + 1024);
+  } else {
     const int r = l >> 3, c = l & 7;
     *reinterpret_cast<uint4*>(lds + r * 128 + 16 * (c ^ (r >> 1))) = w[0];
     *reinterpret_cast<uint4*>(lds + (r + 8) * 128 + 16 * (c ^ ((r >> 1) + 4))) = w[1];
     wave_lds_fence();
     w[0] = *reinterpret_cast<const uint4*>(lds + lr * 128 + 16 * (kg ^ (lr >> 1)));
     w[1] = *reinterpret_cast<const uint4*>(lds + lr * 128 + 16 * ((4 + kg) ^ (lr >> 1)));
-    wave_lds_fence();
   }
+  wave_lds_fence();
 }
 
-// A tile of tokens, 16 x 128 values. Rows of x: load i has tokens 4 i + (l >> 4),
-// 16 bytes l & 15, and goes through 4 KB of LDS: token r's piece c lies at
-// r * 256 + 16 (c ^ r). The operand of matrix instruction q is piece
-// 8 (q / 2) + 2 (l >> 4) + q % 2 of token l & 15, the values of the codes' bytes
-// 8 (q % 2) .. + 7 of load q / 2.
-struct RowTile {
+// The operands of a tile of 16 tokens: of matrix instruction q, the values
+// 64 (q / 2) + 16 (l >> 4) + 8 (q % 2) .. + 7 of token l & 15, those of the codes'
+// bytes 8 (q % 2) .. + 7 of load q / 2.
+struct Tokens {
   v8bf v[4];
 };
-__device__ __forceinline__ void load_rows(RowTile& x, const uint16_t* base, const uint32_t (&off)[4], uint32_t back,
+
+// Rows of x: load i has tokens 4 i + (l >> 4), 16 bytes l & 15, and goes through
+// 4 KB of LDS for 16 tokens: token r's piece c lies at r * 256 + 16 (c ^ r).
+// G loads for 4 G tokens.
+template <int G>
+__device__ __forceinline__ void load_rows(v8bf (&x)[G], const uint16_t* base, const uint32_t (&off)[G], uint32_t back,
                                           int u, int K) {
   const uint8_t* p = reinterpret_cast<const uint8_t*>(base + 128 * u);
   const uint32_t o = 128 * (u + 1) <= K ? 0 : back;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x.v[i] = *reinterpret_cast<const v8bf*>(p + (off[i] - o));
+  for (int i = 0; i < G; ++i) x[i] = *reinterpret_cast<const v8bf*>(p + (off[i] - o));
 }
-__device__ __forceinline__ void turn_rows(RowTile& x, uint8_t* lds) {
+template <int G, int NT>
+__device__ __forceinline__ void turn_rows(const v8bf (&x)[G], Tokens (&t)[NT], uint8_t* lds) {
   const int l = threadIdx.x & 63, lr = l & 15, kg = l >> 4;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * i + kg;
-    *reinterpret_cast<v8bf*>(lds + r * 256 + 16 * (lr ^ r)) = x.v[i];
-  }
-  wave_lds_fence();
+  for (int n = 0; n < NT; ++n) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    x.v[q] = *reinterpret_cast<const v8bf*>(lds + lr * 256 + 16 * ((8 * (q >> 1) + 2 * kg + (q & 1)) ^ lr));
-  wave_lds_fence();
+    for (int i = 0; i < (G < 4 ? G : 4); ++i) {
+      const int r = 4 * i + kg;
+      *reinterpret_cast<v8bf*>(lds + r * 256 + 16 * (lr ^ r)) = x[4 * n + i];
+    }
+    wave_lds_fence();
+    // lanes without a token read what LDS holds: a column that nobody reads
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      t[n].v[q] = *reinterpret_cast<const v8bf*>(lds + lr * 256 + 16 * ((8 * (q >> 1) + 2 * kg + (q & 1)) ^ lr));
+    wave_lds_fence();
+  }
 }
 
 // Zeros for the values of the last unit that lie behind K.
 template <int R, int NT>
-__device__ __forceinline__ void mask_unit(uint4 (&w)[R][2], RowTile (&x)[NT], int u, int K) {
+__device__ __forceinline__ void mask_unit(uint4 (&w)[R][2], Tokens (&x)[NT], int u, int K) {
   if (128 * (u + 1) <= K) return;
   const int kg = (threadIdx.x & 63) >> 4;
 #pragma unroll
@@ -192,7 +213,7 @@ __device__ __forceinline__ void mask_unit(uint4 (&w)[R][2], RowTile (&x)[NT], in
 
 // The products of R tiles of codes with NT tiles of tokens.
 template <int R, int NT>
-__device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const RowTile (&x)[NT], v4f (&acc)[R][NT]) {
+__device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const Tokens (&x)[NT], v4f (&acc)[R][NT]) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     v8bf a[4];
@@ -224,12 +245,12 @@ __device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const RowTile (
   }
 }
 
-// Units in flight by the tiles of tokens: their registers, 8 a tile of codes and
-// 16 a tile of tokens, stay below 128.
-template <int NT>
-constexpr int kInFlight = NT == 1 ? 3 : NT == 2 ? 2 : 1;
-template <int NT>
-constexpr int kInFlightDown = NT == 1 ? 2 : 1;
+// Units in flight by the loads of tokens in one: k_moe_up has 256 registers a
+// lane (two wavefronts a SIMD) and a unit takes 16 + 4 G; k_moe_down 128 and 8 + 4 G.
+template <int G>
+constexpr int kInFlight = G <= 2 ? 4 : G == 4 ? 3 : G == 8 ? 2 : 1;
+template <int G>
+constexpr int kInFlightDown = G <= 2 ? 3 : G == 4 ? 2 : 1;
 
 // The ids in LDS and a bit for each expert that some token names.
 __device__ __forceinline__ void few_ids(const int32_t* __restrict__ ids, int n, int E, int32_t* sid, uint32_t* bits) {
@@ -274,6 +295,21 @@ __device__ __forceinline__ int few_expert(const uint32_t* bits, int s) {
 // is loaded again as soon as it has been multiplied, with the first units of
 // the next tile at the end of one, so that loads stay in flight while the
 // waves' sums are added.
+// Calls go with the loads of four tokens for m tokens, at most 16 NTM.
+template <int NTM, class F>
+__device__ __forceinline__ void by_tokens(int m, F&& go) {
+  if (NTM >= 4 && m > 32)
+    go(std::integral_constant<int, NTM >= 4 ? 16 : 4>{});
+  else if (NTM >= 2 && m > 16)
+    go(std::integral_constant<int, NTM >= 2 ? 8 : 4>{});
+  else if (m > 8)
+    go(std::integral_constant<int, 4>{});
+  else if (m > 4)
+    go(std::integral_constant<int, 2>{});
+  else
+    go(std::integral_constant<int, 1>{});
+}
+
 struct UpShared {
   int32_t sid[kFewT * kFewK];
   int32_t list[kFewT];
@@ -283,36 +319,33 @@ struct UpShared {
   int count[2];
 };
 
-template <int NT, bool PACKED>
+template <int G, bool PACKED>
 __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, int64_t act0, int64_t f0, int nt,
                                              UpShared& sh, float4* red, uint8_t* turn) {
-  constexpr int P = kInFlight<NT>;
+  constexpr int P = kInFlight<G>, NT = (G + 3) / 4;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int lr = lane & 15, kg = lane >> 4;
   const uint8_t* wb = p.w13 + (int64_t)e * 2 * p.F * p.D;
   const float* sc = p.inv13 + (int64_t)e * 2 * p.F + (lane & 16 ? p.F : 0) + f0 + lr;
   const int D = (int)p.D;
   const Codes<PACKED> codes(D);
-  // a lane without a token has the first one's values: a column that nobody reads
-  uint32_t xoff[NT][4];
+  // past the last token the first one's values: a column that nobody reads
+  uint32_t xoff[G];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int it = 16 * n + 4 * i + kg < m ? 16 * n + 4 * i + kg : 0;
-      xoff[n][i] = 2 * ((uint32_t)(sh.list[it] / p.k) * (uint32_t)D + 8 * lr);
-    }
+  for (int i = 0; i < G; ++i) {
+    const int it = 4 * i + kg < m ? 4 * i + kg : 0;
+    xoff[i] = 2 * ((uint32_t)(sh.list[it] / p.k) * (uint32_t)D + 8 * lr);
   }
+  const int mp = (m + 3) & ~3;
   const uint32_t back = 8 * lr < D - (D - 1) / 128 * 128 ? 0 : 16 * lr;
   const int units = (D + 127) / 128;
   const int u0 = units * wave / kUpWaves, nu = units * (wave + 1) / kUpWaves - u0;
   uint4 w[P][2][2];
-  RowTile x[P][NT];
-  auto load = [&](uint4 (&dw)[2][2], RowTile (&dx)[NT], int tile, int u) {
+  v8bf x[P][G];
+  auto load = [&](uint4 (&dw)[2][2], v8bf (&dx)[G], int tile, int u) {
     codes.load(dw[0], wb + (f0 + 16 * tile) * p.D, u, D);
     codes.load(dw[1], wb + (p.F + f0 + 16 * tile) * p.D, u, D);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) load_rows(dx[n], p.x, xoff[n], back, u, D);
+    load_rows<G>(dx, p.x, xoff, back, u, D);
   };
   float scale = sc[0];
   // the load side: the tile and unit of the next load; it stays at the last one
@@ -375,7 +408,7 @@ __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, 
       }
       const v2bf lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
       const int64_t f = f0 + 16 * tile + 4 * kg;
-      *reinterpret_cast<uint2*>(p.act + act0 * p.F + ((f >> 3) * m + item) * 8 + (f & 7)) =
+      *reinterpret_cast<uint2*>(p.act + 4 * act0 * p.F + ((f >> 3) * mp + item) * 8 + (f & 7)) =
           make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
     }
     ++tile;
@@ -398,10 +431,10 @@ __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, 
     for (int i = 0; i < P; ++i) {
       turn_codes<PACKED>(w[i][0], mine);
       turn_codes<PACKED>(w[i][1], mine);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) turn_rows(x[i][n], mine);
-      mask_unit<2, NT>(w[i], x[i], u0 + cu, D);
-      multiply<2, NT>(w[i], x[i], acc);
+      Tokens t[NT];
+      turn_rows<G, NT>(x[i], t, mine);
+      mask_unit<2, NT>(w[i], t, u0 + cu, D);
+      multiply<2, NT>(w[i], t, acc);
       load(w[i], x[i], lt, u0 + lu);
       advance();
       if (++cu == nu && i < left) {
@@ -475,20 +508,8 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeFewArgs p) {
       }
     }
     const int64_t f0 = 16 * (int64_t)first;
-    bool done = false;
-    if constexpr (NTM >= 4) {
-      if (m > 32) {
-        moe_up_tiles<4, PACKED>(p, e, m, act0, f0, nt, sh, red, turn);
-        done = true;
-      }
-    }
-    if constexpr (NTM >= 2) {
-      if (!done && m > 16) {
-        moe_up_tiles<2, PACKED>(p, e, m, act0, f0, nt, sh, red, turn);
-        done = true;
-      }
-    }
-    if (!done) moe_up_tiles<1, PACKED>(p, e, m, act0, f0, nt, sh, red, turn);
+    auto run = [&](auto loads) { moe_up_tiles<loads.value, PACKED>(p, e, m, act0, f0, nt, sh, red, turn); };
+    by_tokens<NTM>(m, run);
     tile += nt;
   }
 }
@@ -501,46 +522,54 @@ struct DownShared {
 // A wave's run [begin, end) of the (expert, unit) pairs of 16 rows. P units are
 // in flight across the experts' borders; at an expert's last unit its sums,
 // times the rows' scales, are added to the wave's sums [token][16].
-template <int NT, bool PACKED>
+template <int G, bool PACKED>
 __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShared& sh, int64_t d0, int units, int i,
                                              int end, float* sum, uint8_t* turn) {
-  constexpr int P = kInFlightDown<NT>;
+  constexpr int P = kInFlightDown<G>, NT = (G + 3) / 4;
   const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4, F = (int)p.F;
   uint4 w[P][1][2];
-  RowTile x[P][NT];
+  v8bf x[P][G];
   const Codes<PACKED> codes(F);
   // the load side: the expert and unit of the next load, and its pointers; it
   // stays at the run's last unit
-  int la = i / units, lu = i % units, more = end - i - 1, m = 0;
+  int la = i / units, lu = i % units, more = end - i - 1, mp = 0;
   const uint8_t* wp = nullptr;
-  const uint16_t* ap = nullptr;
-  uint32_t aoff[NT][4];  // bytes from a unit's first group of 8 values x m tokens
+  const uint8_t* ap = nullptr;
+  // Up to 8 tokens: a unit's 256 mp bytes in a row, mp / 4 loads (with fewer than
+  // G, the first again), turned in LDS. More: the lanes' own operands.
+  uint32_t aoff[G];
   auto point = [&]() {
     const int64_t e = __builtin_amdgcn_readfirstlane(sh.expert[la]);
     const int b = __builtin_amdgcn_readfirstlane(sh.start[la]);
-    m = __builtin_amdgcn_readfirstlane(sh.start[la + 1]) - b;
+    const int m = __builtin_amdgcn_readfirstlane(sh.start[la + 1]) - b;
+    mp = (m + 3) & ~3;
     wp = p.w2 + (e * p.D + d0) * p.F;
-    ap = p.act + (int64_t)b * p.F;
+    ap = reinterpret_cast<const uint8_t*>(p.act + 4 * (int64_t)b * p.F);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      // a lane without a token has the last one's values: a column that nobody reads
-      const int item = 16 * n + lr < m ? 16 * n + lr : m - 1;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) aoff[n][q] = 16 * ((8 * (q >> 1) + 2 * kg + (q & 1)) * m + item);
+    for (int j = 0; j < G; ++j) {
+      if constexpr (G <= 2) {
+        aoff[j] = 16 * lane + (4 * j < mp ? 1024 * j : 0);
+      } else {
+        // past the last token its value: a column that nobody reads
+        const int item = 16 * (j / 4) + lr < m ? 16 * (j / 4) + lr : m - 1, q = j % 4;
+        aoff[j] = 16 * ((8 * (q >> 1) + 2 * kg + (q & 1)) * mp + item);
+      }
     }
   };
-  auto load = [&](uint4 (&dw)[1][2], RowTile (&dx)[NT]) {
+  auto load = [&](uint4 (&dw)[1][2], v8bf (&dx)[G]) {
     codes.load(dw[0], wp, lu, F);
-    const uint8_t* u = reinterpret_cast<const uint8_t*>(ap) + (int64_t)lu * 256 * m;
-    const bool full = 128 * (lu + 1) <= F;
+    const uint8_t* u = ap + (int64_t)lu * 256 * mp;
+    const int rest = F - 128 * lu;  // below 128: the part behind F is not there to be read
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        // behind F: group 0 of the unit
-        const uint32_t o = full || 128 * lu + 64 * (q >> 1) + 16 * kg < F ? aoff[n][q] : 0;
-        dx[n].v[q] = *reinterpret_cast<const v8bf*>(u + o);
+    for (int j = 0; j < G; ++j) {
+      uint32_t o = aoff[j];
+      if (rest < 128) {
+        if constexpr (G <= 2)
+          o = o < (uint32_t)(2 * rest * mp) ? o : 0;
+        else
+          o = 64 * (j % 4 >> 1) + 16 * kg < rest ? o : 0;
       }
+      dx[j] = *reinterpret_cast<const v8bf*>(u + o);
     }
     if (more > 0) {
       --more;
@@ -551,9 +580,25 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
       }
     }
   };
+  auto operands = [&](const v8bf (&dx)[G], Tokens (&t)[NT], int m4) {
+    if constexpr (G <= 2) {
+#pragma unroll
+      for (int j = 0; j < G; ++j) *reinterpret_cast<v8bf*>(turn + 1024 * j + 16 * lane) = dx[j];
+      wave_lds_fence();
+      const int item = lr < m4 ? lr : m4 - 1;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        t[0].v[q] = *reinterpret_cast<const v8bf*>(turn + 16 * ((8 * (q >> 1) + 2 * kg + (q & 1)) * m4 + item));
+      wave_lds_fence();
+    } else {
+#pragma unroll
+      for (int j = 0; j < G; ++j) t[j / 4].v[j % 4] = dx[j];
+    }
+  };
   // the multiply side; no way out between the slots, as in moe_up_tiles
   int ca = la, cu = lu;
   point();
+  int cm = mp;  // as mp, of expert ca
 #pragma unroll
   for (int j = 0; j < P; ++j) load(w[j], x[j]);
   v4f acc[1][NT];
@@ -563,8 +608,10 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       turn_codes<PACKED>(w[j][0], turn);
-      mask_unit<1, NT>(w[j], x[j], cu, F);
-      multiply<1, NT>(w[j], x[j], acc);
+      Tokens t[NT];
+      operands(x[j], t, cm);
+      mask_unit<1, NT>(w[j], t, cu, F);
+      multiply<1, NT>(w[j], t, acc);
       load(w[j], x[j]);
       if (j < left && (++cu == units || j + 1 == left)) {
         // the rows' scales through the scalar cache, past the loads in flight
@@ -595,6 +642,8 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
         }
         cu = 0;
         ++ca;
+        if (j + 1 < left)
+          cm = (__builtin_amdgcn_readfirstlane(sh.start[ca + 1]) - __builtin_amdgcn_readfirstlane(sh.start[ca]) + 3) & ~3;
       }
     }
   }
@@ -608,7 +657,7 @@ template <int NTM, bool PACKED>
 __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(MoeFewArgs p) {
   constexpr int kTok = 16 * NTM;
   __shared__ float4 sums[kDownWaves * kTok * 4];  // [wave][token][16]
-  __shared__ __align__(16) uint8_t turn[PACKED ? 16 : kDownWaves * 2048];
+  __shared__ __align__(16) uint8_t turn[kDownWaves * 2048];
   __shared__ DownShared sh;
   const int wave = wave_id(), lane = threadIdx.x & 63;
   const FewMeta meta = few_meta(p.act, p.T, p.k, p.F);
@@ -624,7 +673,9 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(MoeFewArgs p) {
   const int nact = __builtin_amdgcn_readfirstlane(sh.count);
   int most = 0;  // the largest number of tokens of an expert
   for (int a = lane; a < nact; a += 64) most = max(most, sh.start[a + 1] - sh.start[a]);
-  const bool over16 = __ballot(most > 16) != 0, over32 = __ballot(most > 32) != 0;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o, 64));
+  most = __builtin_amdgcn_readfirstlane(most);
   const int units = (int)((p.F + 127) / 128);
   const int64_t tiles = p.D / 16, per = (int64_t)nact * units, all = tiles * per;
   if (nact == 0) {  // no token has an expert: zeros
@@ -635,7 +686,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(MoeFewArgs p) {
   }
   int64_t share = (all + gridDim.x - 1) / gridDim.x;
   if (share < kDownWaves * 4) share = kDownWaves * 4;
-  if (share < per && per <= kDownWaves * 8) share = per;
+  if (share < per && per <= kDownWaves * 32) share = per;
   int64_t i = share * blockIdx.x;
   const int64_t end = i + share < all ? i + share : all;
   const int t = threadIdx.x >> 2, q = threadIdx.x & 3;  // the values that this thread adds up
@@ -649,22 +700,10 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(MoeFewArgs p) {
     wave_lds_fence();
     const int i0 = from + (int)((int64_t)(to - from) * wave / kDownWaves);
     const int i1 = from + (int)((int64_t)(to - from) * (wave + 1) / kDownWaves);
-    uint8_t* mine = PACKED ? turn : turn + wave * 2048;
+    uint8_t* mine = turn + wave * 2048;
     if (i0 < i1) {
-      bool done = false;
-      if constexpr (NTM >= 4) {
-        if (over32) {
-          moe_down_run<4, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
-          done = true;
-        }
-      }
-      if constexpr (NTM >= 2) {
-        if (!done && over16) {
-          moe_down_run<2, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
-          done = true;
-        }
-      }
-      if (!done) moe_down_run<1, PACKED>(p, sh, d0, units, i0, i1, sum, mine);
+      auto run = [&](auto loads) { moe_down_run<loads.value, PACKED>(p, sh, d0, units, i0, i1, sum, mine); };
+      by_tokens<NTM>(most, run);
     }
     __syncthreads();
     float r[4] = {0, 0, 0, 0};
