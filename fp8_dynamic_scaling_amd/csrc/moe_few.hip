@@ -12,7 +12,7 @@
 //  - k_moe_up: two workgroups a CU share the named experts' tiles of 16 gate and
 //    16 up rows evenly; a workgroup's waves share D among them. The waves'
 //    partial sums meet in LDS, in a fixed order.
-//  - k_moe_down: the workgroups share the tiles of 16 rows of D, each for all
+//  - k_moe_down: the workgroups share the tiles of rows of D, each for all
 //    experts, evenly; the waves share a tile's (expert, piece of F) units. A wave
 //    adds what it has of a token to its own fp32 sums in LDS, the waves' sums are
 //    added in order, and so are those of workgroups that share a tile: the same
@@ -47,7 +47,9 @@ namespace {
 constexpr int kUpWaves = 4;
 constexpr int kUpBlocks = 512;  // two a CU
 constexpr int kDownWaves = 8;
-constexpr int kDownBlocks = 512;  // two a CU
+constexpr int kDownBlocks = 256;  // one a CU
+constexpr int kDownTiles = 2;     // tiles of 16 rows a unit has
+constexpr int kDownRows = 16 * kDownTiles;
 constexpr int kFewT = 64;
 constexpr int kFewK = 32;
 
@@ -55,9 +57,9 @@ constexpr int kFewK = 32;
 // 4 start F (room for m tokens, rounded up to a multiple mp of four), in it value
 // f of its i-th token at ((f / 8) mp + i) 8 + f % 8; the number of named experts; each one's id, in order, where its pairs begin,
 // and the tokens of the pairs. k_moe_down joins split sums by `done` (counters
-// that k_moe_up clears) and `part` ([workgroup][first or last tile][T][16]).
+// that k_moe_up clears) and `part` ([workgroup][first or last tile][T][rows]).
 struct FewMeta {
-  float* part;       // [kDownBlocks][2][T * 16]
+  float* part;       // [kDownBlocks][2][T][kDownRows]
   uint32_t* done;    // [kDownBlocks]
   int32_t* head;     // [0]: the number of experts
   uint16_t* expert;  // [T * k]
@@ -67,7 +69,7 @@ struct FewMeta {
 __host__ __device__ inline FewMeta few_meta(uint16_t* act, int64_t T, int k, int64_t F) {
   FewMeta m;
   m.part = reinterpret_cast<float*>(act + 4 * T * k * F);
-  m.done = reinterpret_cast<uint32_t*>(m.part + kDownBlocks * 2 * T * 16);
+  m.done = reinterpret_cast<uint32_t*>(m.part + kDownBlocks * 2 * T * kDownRows);
   m.head = reinterpret_cast<int32_t*>(m.done + kDownBlocks);
   m.expert = reinterpret_cast<uint16_t*>(m.head + 1);
   m.start = m.expert + T * k;
@@ -77,7 +79,7 @@ __host__ __device__ inline FewMeta few_meta(uint16_t* act, int64_t T, int k, int
 }  // namespace
 
 size_t moe_few_ws_bytes(int64_t T, int k, int64_t F) {
-  return (size_t)(T * k) * (8 * F + 6) + 8 + kDownBlocks * (size_t)(4 + 2 * T * 64);
+  return (size_t)(T * k) * (8 * F + 6) + 8 + kDownBlocks * (size_t)(4 + 8 * T * kDownRows);
 }
 
 // Eight e4m3 codes -> eight bf16 (every e4m3 value is a bf16 value).
@@ -245,12 +247,10 @@ __device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const Tokens (&
   }
 }
 
-// Units in flight by the loads of tokens in one: k_moe_up has 256 registers a
-// lane (two wavefronts a SIMD) and a unit takes 16 + 4 G; k_moe_down 128 and 8 + 4 G.
+// Units in flight by the loads of tokens in one: a unit takes 16 + 4 G of the 256
+// registers a lane that two wavefronts a SIMD have.
 template <int G>
 constexpr int kInFlight = G <= 2 ? 4 : G == 4 ? 3 : G == 8 ? 2 : 1;
-template <int G>
-constexpr int kInFlightDown = G <= 2 ? 3 : G == 4 ? 2 : 1;
 
 // The ids in LDS and a bit for each expert that some token names.
 __device__ __forceinline__ void few_ids(const int32_t* __restrict__ ids, int n, int E, int32_t* sid, uint32_t* bits) {
@@ -519,21 +519,23 @@ struct DownShared {
   int count;
 };
 
-// A wave's run [begin, end) of the (expert, unit) pairs of 16 rows. P units are
+// A wave's run [i, end) of the (expert, unit) pairs of kDownRows rows. P units are
 // in flight across the experts' borders; at an expert's last unit its sums,
-// times the rows' scales, are added to the wave's sums [token][16].
+// times the rows' scales, are added to the wave's sums [token][row].
 template <int G, bool PACKED>
 __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShared& sh, int64_t d0, int units, int i,
                                              int end, float* sum, uint8_t* turn) {
-  constexpr int P = kInFlightDown<G>, NT = (G + 3) / 4;
+  constexpr int P = kInFlight<G>, NT = (G + 3) / 4, R = kDownTiles;
   const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4, F = (int)p.F;
-  uint4 w[P][1][2];
+  uint4 w[P][R][2];
   v8bf x[P][G];
   const Codes<PACKED> codes(F);
   // the load side: the expert and unit of the next load, and its pointers; it
   // stays at the run's last unit
+  // the first row of tile r; behind D the first tile again, whose sums are not written
+  auto row_of = [&](int r) { return d0 + 16 * r < p.D ? d0 + 16 * r : d0; };
   int la = i / units, lu = i % units, more = end - i - 1, mp = 0;
-  const uint8_t* wp = nullptr;
+  const uint8_t* wp[R];
   const uint8_t* ap = nullptr;
   // Up to 8 tokens: a unit's 256 mp bytes in a row, mp / 4 loads (with fewer than
   // G, the first again), turned in LDS. More: the lanes' own operands.
@@ -543,7 +545,8 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
     const int b = __builtin_amdgcn_readfirstlane(sh.start[la]);
     const int m = __builtin_amdgcn_readfirstlane(sh.start[la + 1]) - b;
     mp = (m + 3) & ~3;
-    wp = p.w2 + (e * p.D + d0) * p.F;
+#pragma unroll
+    for (int r = 0; r < R; ++r) wp[r] = p.w2 + (e * p.D + row_of(r)) * p.F;
     ap = reinterpret_cast<const uint8_t*>(p.act + 4 * (int64_t)b * p.F);
 #pragma unroll
     for (int j = 0; j < G; ++j) {
@@ -556,8 +559,9 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
       }
     }
   };
-  auto load = [&](uint4 (&dw)[1][2], v8bf (&dx)[G]) {
-    codes.load(dw[0], wp, lu, F);
+  auto load = [&](uint4 (&dw)[R][2], v8bf (&dx)[G]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) codes.load(dw[r], wp[r], lu, F);
     const uint8_t* u = ap + (int64_t)lu * 256 * mp;
     const int rest = F - 128 * lu;  // below 128: the part behind F is not there to be read
 #pragma unroll
@@ -601,44 +605,50 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
   int cm = mp;  // as mp, of expert ca
 #pragma unroll
   for (int j = 0; j < P; ++j) load(w[j], x[j]);
-  v4f acc[1][NT];
+  v4f acc[R][NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) acc[0][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[r][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
   for (int left = end - i; left > 0; left -= P) {
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      turn_codes<PACKED>(w[j][0], turn);
+#pragma unroll
+      for (int r = 0; r < R; ++r) turn_codes<PACKED>(w[j][r], turn);
       Tokens t[NT];
       operands(x[j], t, cm);
-      mask_unit<1, NT>(w[j], t, cu, F);
-      multiply<1, NT>(w[j], t, acc);
+      mask_unit<R, NT>(w[j], t, cu, F);
+      multiply<R, NT>(w[j], t, acc);
       load(w[j], x[j]);
       if (j < left && (++cu == units || j + 1 == left)) {
         // the rows' scales through the scalar cache, past the loads in flight
         typedef const __attribute__((address_space(4))) float* ScalarPtr;
-        const ScalarPtr sp =
-            (ScalarPtr)(uintptr_t)(p.inv2 + (int64_t)__builtin_amdgcn_readfirstlane(sh.expert[ca]) * p.D + d0);
-        float c[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          float v[4] = {sp[z], sp[4 + z], sp[8 + z], sp[12 + z]};
-          asm("" : "+s"(v[0]), "+s"(v[1]), "+s"(v[2]), "+s"(v[3]));  // loaded as scalars, then chosen by lane
-          c[z] = kg < 2 ? (kg == 0 ? v[0] : v[1]) : (kg == 2 ? v[2] : v[3]);
-        }
+        const float* inv = p.inv2 + (int64_t)__builtin_amdgcn_readfirstlane(sh.expert[ca]) * p.D;
         const int b = sh.start[ca], mc = sh.start[ca + 1] - b;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          // an expert's tokens differ, so no two lanes meet
-          if (16 * n + lr < mc) {
-            float4* d = reinterpret_cast<float4*>(sum + sh.token[b + 16 * n + lr] * 16 + 4 * kg);
-            float4 v = *d;
-            v.x += acc[0][n][0] * c[0];
-            v.y += acc[0][n][1] * c[1];
-            v.z += acc[0][n][2] * c[2];
-            v.w += acc[0][n][3] * c[3];
-            *d = v;
+        for (int r = 0; r < R; ++r) {
+          const ScalarPtr sp = (ScalarPtr)(uintptr_t)(inv + row_of(r));
+          float c[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            float v[4] = {sp[z], sp[4 + z], sp[8 + z], sp[12 + z]};
+            asm("" : "+s"(v[0]), "+s"(v[1]), "+s"(v[2]), "+s"(v[3]));  // loaded as scalars, then chosen by lane
+            c[z] = kg < 2 ? (kg == 0 ? v[0] : v[1]) : (kg == 2 ? v[2] : v[3]);
           }
-          acc[0][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            // an expert's tokens differ, so no two lanes meet
+            if (16 * n + lr < mc) {
+              float4* d = reinterpret_cast<float4*>(sum + sh.token[b + 16 * n + lr] * kDownRows + 16 * r + 4 * kg);
+              float4 v = *d;
+              v.x += acc[r][n][0] * c[0];
+              v.y += acc[r][n][1] * c[1];
+              v.z += acc[r][n][2] * c[2];
+              v.w += acc[r][n][3] * c[3];
+              *d = v;
+            }
+            acc[r][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+          }
         }
         cu = 0;
         ++ca;
@@ -654,9 +664,9 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
 // of a tile that several share meet in memory, and the one that comes last adds
 // them, in the workgroups' order. Where a tile has few units it is not split.
 template <int NTM, bool PACKED>
-__global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(MoeFewArgs p) {
-  constexpr int kTok = 16 * NTM;
-  __shared__ float4 sums[kDownWaves * kTok * 4];  // [wave][token][16]
+__global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeFewArgs p) {
+  constexpr int kQuads = 16 * NTM * kDownRows / 4;  // a wave's sums, by fours
+  __shared__ float4 sums[kDownWaves * kQuads];  // [wave][token][row]
   __shared__ __align__(16) uint8_t turn[kDownWaves * 2048];
   __shared__ DownShared sh;
   const int wave = wave_id(), lane = threadIdx.x & 63;
@@ -677,7 +687,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(MoeFewArgs p) {
   for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o, 64));
   most = __builtin_amdgcn_readfirstlane(most);
   const int units = (int)((p.F + 127) / 128);
-  const int64_t tiles = p.D / 16, per = (int64_t)nact * units, all = tiles * per;
+  const int64_t tiles = (p.D + kDownRows - 1) / kDownRows, per = (int64_t)nact * units, all = tiles * per;
   if (nact == 0) {  // no token has an expert: zeros
     for (int64_t i = (int64_t)blockIdx.x * 64 * kDownWaves + threadIdx.x; i < p.T * p.D / 8;
          i += (int64_t)gridDim.x * 64 * kDownWaves)
@@ -689,14 +699,12 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(MoeFewArgs p) {
   if (share < per && per <= kDownWaves * 32) share = per;
   int64_t i = share * blockIdx.x;
   const int64_t end = i + share < all ? i + share : all;
-  const int t = threadIdx.x >> 2, q = threadIdx.x & 3;  // the values that this thread adds up
-  const bool adds = t < (int)p.T;
   while (i < end) {
-    const int64_t tile = i / per, d0 = 16 * tile;
+    const int64_t tile = i / per, d0 = kDownRows * tile;
     const int from = (int)(i - tile * per);
     const int to = (int)(end - tile * per < per ? end - tile * per : per);
-    float* sum = reinterpret_cast<float*>(&sums[wave * kTok * 4]);
-    for (int z = lane; z < kTok * 4; z += 64) sums[wave * kTok * 4 + z] = make_float4(0, 0, 0, 0);
+    float* sum = reinterpret_cast<float*>(&sums[wave * kQuads]);
+    for (int z = lane; z < kQuads; z += 64) sums[wave * kQuads + z] = make_float4(0, 0, 0, 0);
     wave_lds_fence();
     const int i0 = from + (int)((int64_t)(to - from) * wave / kDownWaves);
     const int i1 = from + (int)((int64_t)(to - from) * (wave + 1) / kDownWaves);
@@ -706,15 +714,22 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(MoeFewArgs p) {
       by_tokens<NTM>(most, run);
     }
     __syncthreads();
-    float r[4] = {0, 0, 0, 0};
-    if (adds) {
+    // each thread adds up the waves' sums of up to two fours of rows of a token
+    constexpr int kMine = (kQuads + 64 * kDownWaves - 1) / (64 * kDownWaves);
+    const int quads = (int)p.T * (kDownRows / 4);
+    float r[kMine][4];
+#pragma unroll
+    for (int y = 0; y < kMine; ++y) {
+      const int z = threadIdx.x + y * 64 * kDownWaves;
+      r[y][0] = r[y][1] = r[y][2] = r[y][3] = 0.0f;
+      if (z >= quads) continue;
 #pragma unroll
       for (int w = 0; w < kDownWaves; ++w) {
-        const float4 a = sums[(w * kTok + t) * 4 + q];
-        r[0] += a.x;
-        r[1] += a.y;
-        r[2] += a.z;
-        r[3] += a.w;
+        const float4 a = sums[w * kQuads + z];
+        r[y][0] += a.x;
+        r[y][1] += a.y;
+        r[y][2] += a.z;
+        r[y][3] += a.w;
       }
     }
     bool write = true;
@@ -723,36 +738,50 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(MoeFewArgs p) {
       const int64_t b0 = tile * per / share, b1 = ((tile + 1) * per - 1) / share;
       auto slot = [&](int64_t b) {
         const int64_t first = share * b / per;  // a workgroup's first tile
-        return meta.part + (2 * b + (tile != first)) * p.T * 16;
+        return meta.part + (2 * b + (tile != first)) * p.T * kDownRows;
       };
-      if (adds) {
-        float* d = slot(blockIdx.x) + t * 16 + 4 * q;
-#pragma unroll
-        for (int z = 0; z < 4; ++z) __hip_atomic_store(d + z, r[z], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
       // Every value that crosses workgroups is stored and loaded by an atomic of
       // agent scope, which reaches the memory that all XCDs share, so no cache
       // has to be written back or emptied; the wait has the stores there before
       // the barrier, and the count goes up behind it.
+#pragma unroll
+      for (int y = 0; y < kMine; ++y) {
+        const int z = threadIdx.x + y * 64 * kDownWaves;
+        if (z >= quads) continue;
+        float* d = slot(blockIdx.x) + 4 * z;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) __hip_atomic_store(d + c, r[y][c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       if (threadIdx.x == 0)
         sh.count = (int)__hip_atomic_fetch_add(&meta.done[b0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();
       write = sh.count == (int)(b1 - b0);
-      if (write && adds) {
-        r[0] = r[1] = r[2] = r[3] = 0.0f;
-        for (int64_t b = b0; b <= b1; ++b) {
-          const float* d = slot(b) + t * 16 + 4 * q;
+      if (write) {
 #pragma unroll
-          for (int z = 0; z < 4; ++z) r[z] += __hip_atomic_load(d + z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        for (int y = 0; y < kMine; ++y) {
+          const int z = threadIdx.x + y * 64 * kDownWaves;
+          if (z >= quads) continue;
+          r[y][0] = r[y][1] = r[y][2] = r[y][3] = 0.0f;
+          for (int64_t b = b0; b <= b1; ++b) {
+            const float* d = slot(b) + 4 * z;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) r[y][c] += __hip_atomic_load(d + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          }
         }
       }
     }
-    if (write && adds) {
-      const v2bf lo = {(__bf16)r[0], (__bf16)r[1]}, hi = {(__bf16)r[2], (__bf16)r[3]};
-      *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.D + d0 + 4 * q) =
-          make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+    if (write) {
+#pragma unroll
+      for (int y = 0; y < kMine; ++y) {
+        const int z = threadIdx.x + y * 64 * kDownWaves, t = z / (kDownRows / 4);
+        const int64_t d = d0 + 4 * (z % (kDownRows / 4));
+        if (z >= quads || d >= p.D) continue;
+        const v2bf lo = {(__bf16)r[y][0], (__bf16)r[y][1]}, hi = {(__bf16)r[y][2], (__bf16)r[y][3]};
+        *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.D + d) =
+            make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+      }
     }
     i += to - from;
     if (i < end) __syncthreads();  // the sums are read before they are cleared
