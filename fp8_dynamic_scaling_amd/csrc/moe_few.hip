@@ -17,10 +17,9 @@
 //    adds what it has of a token to its own fp32 sums in LDS, the waves' sums are
 //    added in order, and so are those of workgroups that share a tile: the same
 //    inputs give the same bits.
-// A wave's unit of work is 16 rows (k_moe_up: twice 16) x 128 values of the
-// contraction and the same 128 values of its tokens; the loads of the next
-// units are in flight while one is multiplied. An expert's tokens are compacted
-// into tiles of 16.
+// A wave's unit of work is twice 16 rows x 128 values of the
+// contraction and the same 128 values of its tokens. An expert's tokens are
+// compacted into tiles of 16.
 //
 // After HBM the loads' own rate is the next bound: measured, a 16-byte load of
 // a wavefront takes 17 clocks of its CU's load path where each four neighbouring
@@ -44,8 +43,8 @@
 namespace fp8dyn {
 
 namespace {
-constexpr int kUpWaves = 4;
-constexpr int kUpBlocks = 512;  // two a CU
+constexpr int kUpWaves = 2;
+constexpr int kUpBlocks = 1024;  // four a CU
 constexpr int kDownWaves = 8;
 constexpr int kDownBlocks = 256;  // one a CU
 constexpr int kDownTiles = 2;     // tiles of 16 rows a unit has
@@ -129,8 +128,8 @@ struct Codes {
     } else {
       const uint8_t* p = tile + 128 * u;
       const uint32_t o = 128 * (u + 1) <= K ? off : last;
-      w[0] = *reinterpret_cast<const uint4*>(p + o);
-      w[1] = *reinterpret_cast<const uint4*>(p + 8 * (int64_t)K + o);
+      w[0] = ld_nt16(p + o);
+      w[1] = ld_nt16(p + 8 * (int64_t)K + o);
     }
   }
 };
@@ -247,11 +246,6 @@ __device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const Tokens (&
   }
 }
 
-// Units in flight by the loads of tokens in one: a unit takes 16 + 4 G of the 256
-// registers a lane that two wavefronts a SIMD have.
-template <int G>
-constexpr int kInFlight = G <= 2 ? 4 : G == 4 ? 3 : G == 8 ? 2 : 1;
-
 // The ids in LDS and a bit for each expert that some token names.
 __device__ __forceinline__ void few_ids(const int32_t* __restrict__ ids, int n, int E, int32_t* sid, uint32_t* bits) {
   if (threadIdx.x < 32) bits[threadIdx.x] = 0;
@@ -291,10 +285,9 @@ __device__ __forceinline__ int few_expert(const uint32_t* bits, int s) {
 }
 
 // Tiles [0, nt) of 16 gate and 16 up rows of one expert from row f0 on. The
-// units of a tile that a wave has go through P register slots in turn; a slot
-// is loaded again as soon as it has been multiplied, with the first units of
-// the next tile at the end of one, so that loads stay in flight while the
-// waves' sums are added.
+// units of a wave follow each other across the tiles' borders: the next one is
+// loaded as soon as one has been multiplied, and is in flight while the waves'
+// sums are added.
 // Calls go with the loads of four tokens for m tokens, at most 16 NTM.
 template <int NTM, class F>
 __device__ __forceinline__ void by_tokens(int m, F&& go) {
@@ -322,7 +315,7 @@ struct UpShared {
 template <int G, bool PACKED>
 __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, int64_t act0, int64_t f0, int nt,
                                              UpShared& sh, float4* red, uint8_t* turn) {
-  constexpr int P = kInFlight<G>, NT = (G + 3) / 4;
+  constexpr int NT = (G + 3) / 4;
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int lr = lane & 15, kg = lane >> 4;
   const uint8_t* wb = p.w13 + (int64_t)e * 2 * p.F * p.D;
@@ -340,24 +333,14 @@ __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, 
   const uint32_t back = 8 * lr < D - (D - 1) / 128 * 128 ? 0 : 16 * lr;
   const int units = (D + 127) / 128;
   const int u0 = units * wave / kUpWaves, nu = units * (wave + 1) / kUpWaves - u0;
-  uint4 w[P][2][2];
-  v8bf x[P][G];
-  auto load = [&](uint4 (&dw)[2][2], v8bf (&dx)[G], int tile, int u) {
-    codes.load(dw[0], wb + (f0 + 16 * tile) * p.D, u, D);
-    codes.load(dw[1], wb + (p.F + f0 + 16 * tile) * p.D, u, D);
-    load_rows<G>(dx, p.x, xoff, back, u, D);
+  uint4 w[2][2];
+  v8bf x[G];
+  auto load = [&](int tile, int u) {
+    codes.load(w[0], wb + (f0 + 16 * tile) * p.D, u0 + u, D);
+    codes.load(w[1], wb + (p.F + f0 + 16 * tile) * p.D, u0 + u, D);
+    load_rows<G>(x, p.x, xoff, back, u0 + u, D);
   };
   float scale = sc[0];
-  // the load side: the tile and unit of the next load; it stays at the last one
-  int lt = 0, lu = 0;
-  auto advance = [&]() {
-    if (lu + 1 < nu) {
-      ++lu;
-    } else if (lt + 1 < nt) {
-      lu = 0;
-      ++lt;
-    }
-  };
   uint8_t* mine = turn + wave * 4096;
   v4f acc[2][NT];
 #pragma unroll
@@ -382,9 +365,12 @@ __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, 
     if (wave == 0 && lane < 32) sh.scale[tile & 1][lane] = scale;
     scale = sc[16 * (tile + 1 < nt ? tile + 1 : tile)];
     __syncthreads();
-    const int n = (wave + tile) % kUpWaves;  // the waves finish token tiles in turn
-    const int item = 16 * n + lr;
-    if (n < NT && item < m) {
+    // the waves finish the token tiles in turn
+#pragma unroll
+    for (int n0 = 0; n0 < NT; n0 += kUpWaves) {
+      const int n = n0 + (wave + tile) % kUpWaves;
+      const int item = 16 * n + lr;
+      if (n >= NT || item >= m) continue;
       float g[4] = {0, 0, 0, 0}, uu[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < kUpWaves; ++i) {
@@ -417,31 +403,19 @@ __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, 
     while (tile < nt) finish();
     return;
   }
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    load(w[i], x[i], lt, u0 + lu);
-    advance();
-  }
-  // the multiply side. No way out between the slots, so that the loads in flight
-  // are the same at each: behind the last unit the slots hold it again, and what
-  // they add to acc is not read
-  int cu = 0;
-  for (int left = nu * nt; left > 0; left -= P) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      turn_codes<PACKED>(w[i][0], mine);
-      turn_codes<PACKED>(w[i][1], mine);
+  load(0, 0);
+  while (tile < nt) {
+    for (int u = 0; u < nu; ++u) {
+      turn_codes<PACKED>(w[0], mine);
+      turn_codes<PACKED>(w[1], mine);
       Tokens t[NT];
-      turn_rows<G, NT>(x[i], t, mine);
-      mask_unit<2, NT>(w[i], t, u0 + cu, D);
-      multiply<2, NT>(w[i], t, acc);
-      load(w[i], x[i], lt, u0 + lu);
-      advance();
-      if (++cu == nu && i < left) {
-        cu = 0;
-        finish();
-      }
+      turn_rows<G, NT>(x, t, mine);
+      mask_unit<2, NT>(w, t, u0 + u, D);
+      multiply<2, NT>(w, t, acc);
+      const bool here = u + 1 < nu;
+      load(here || tile + 1 == nt ? tile : tile + 1, here ? u + 1 : 0);  // behind the last unit one that nobody uses
     }
+    finish();
   }
 }
 
@@ -519,31 +493,30 @@ struct DownShared {
   int count;
 };
 
-// A wave's run [i, end) of the (expert, unit) pairs of kDownRows rows. P units are
-// in flight across the experts' borders; at an expert's last unit its sums,
+// A wave's run [i, end) of the (expert, unit) pairs of kDownRows rows, the next one
+// loaded as soon as one has been multiplied. At an expert's last unit its sums,
 // times the rows' scales, are added to the wave's sums [token][row].
 template <int G, bool PACKED>
 __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShared& sh, int64_t d0, int units, int i,
                                              int end, float* sum, uint8_t* turn) {
-  constexpr int P = kInFlight<G>, NT = (G + 3) / 4, R = kDownTiles;
+  constexpr int NT = (G + 3) / 4, R = kDownTiles;
   const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4, F = (int)p.F;
-  uint4 w[P][R][2];
-  v8bf x[P][G];
+  uint4 w[R][2];
+  v8bf x[G];
   const Codes<PACKED> codes(F);
-  // the load side: the expert and unit of the next load, and its pointers; it
-  // stays at the run's last unit
   // the first row of tile r; behind D the first tile again, whose sums are not written
   auto row_of = [&](int r) { return d0 + 16 * r < p.D ? d0 + 16 * r : d0; };
-  int la = i / units, lu = i % units, more = end - i - 1, mp = 0;
+  // the unit that the registers hold, or that is on its way to them
+  int a = i / units, u = i % units, mp = 0;
   const uint8_t* wp[R];
   const uint8_t* ap = nullptr;
   // Up to 8 tokens: a unit's 256 mp bytes in a row, mp / 4 loads (with fewer than
   // G, the first again), turned in LDS. More: the lanes' own operands.
   uint32_t aoff[G];
   auto point = [&]() {
-    const int64_t e = __builtin_amdgcn_readfirstlane(sh.expert[la]);
-    const int b = __builtin_amdgcn_readfirstlane(sh.start[la]);
-    const int m = __builtin_amdgcn_readfirstlane(sh.start[la + 1]) - b;
+    const int64_t e = __builtin_amdgcn_readfirstlane(sh.expert[a]);
+    const int b = __builtin_amdgcn_readfirstlane(sh.start[a]);
+    const int m = __builtin_amdgcn_readfirstlane(sh.start[a + 1]) - b;
     mp = (m + 3) & ~3;
 #pragma unroll
     for (int r = 0; r < R; ++r) wp[r] = p.w2 + (e * p.D + row_of(r)) * p.F;
@@ -559,11 +532,11 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
       }
     }
   };
-  auto load = [&](uint4 (&dw)[R][2], v8bf (&dx)[G]) {
+  auto load = [&]() {
 #pragma unroll
-    for (int r = 0; r < R; ++r) codes.load(dw[r], wp[r], lu, F);
-    const uint8_t* u = ap + (int64_t)lu * 256 * mp;
-    const int rest = F - 128 * lu;  // below 128: the part behind F is not there to be read
+    for (int r = 0; r < R; ++r) codes.load(w[r], wp[r], u, F);
+    const uint8_t* at = ap + (int64_t)u * 256 * mp;
+    const int rest = F - 128 * u;  // below 128: the part behind F is not there to be read
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       uint32_t o = aoff[j];
@@ -573,87 +546,75 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
         else
           o = 64 * (j % 4 >> 1) + 16 * kg < rest ? o : 0;
       }
-      dx[j] = *reinterpret_cast<const v8bf*>(u + o);
-    }
-    if (more > 0) {
-      --more;
-      if (++lu == units) {
-        lu = 0;
-        ++la;
-        point();
-      }
+      x[j] = *reinterpret_cast<const v8bf*>(at + o);
     }
   };
-  auto operands = [&](const v8bf (&dx)[G], Tokens (&t)[NT], int m4) {
+  auto operands = [&](Tokens (&t)[NT]) {
     if constexpr (G <= 2) {
 #pragma unroll
-      for (int j = 0; j < G; ++j) *reinterpret_cast<v8bf*>(turn + 1024 * j + 16 * lane) = dx[j];
+      for (int j = 0; j < G; ++j) *reinterpret_cast<v8bf*>(turn + 1024 * j + 16 * lane) = x[j];
       wave_lds_fence();
-      const int item = lr < m4 ? lr : m4 - 1;
+      const int item = lr < mp ? lr : mp - 1;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        t[0].v[q] = *reinterpret_cast<const v8bf*>(turn + 16 * ((8 * (q >> 1) + 2 * kg + (q & 1)) * m4 + item));
+        t[0].v[q] = *reinterpret_cast<const v8bf*>(turn + 16 * ((8 * (q >> 1) + 2 * kg + (q & 1)) * mp + item));
       wave_lds_fence();
     } else {
 #pragma unroll
-      for (int j = 0; j < G; ++j) t[j / 4].v[j % 4] = dx[j];
+      for (int j = 0; j < G; ++j) t[j / 4].v[j % 4] = x[j];
     }
   };
-  // the multiply side; no way out between the slots, as in moe_up_tiles
-  int ca = la, cu = lu;
-  point();
-  int cm = mp;  // as mp, of expert ca
-#pragma unroll
-  for (int j = 0; j < P; ++j) load(w[j], x[j]);
   v4f acc[R][NT];
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[r][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  for (int left = end - i; left > 0; left -= P) {
+  point();
+  load();
+  for (; i < end; ++i) {
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
+    for (int r = 0; r < R; ++r) turn_codes<PACKED>(w[r], turn);
+    Tokens t[NT];
+    operands(t);
+    mask_unit<R, NT>(w, t, u, F);
+    multiply<R, NT>(w, t, acc);
+    const int of = a;
+    if (i + 1 < end) {
+      if (++u == units) {
+        u = 0;
+        ++a;
+        point();
+      }
+    }
+    load();  // behind the last unit it again, and nobody uses it
+    if (a == of && i + 1 < end) continue;
+    // the rows' scales through the scalar cache, past the loads in flight
+    typedef const __attribute__((address_space(4))) float* ScalarPtr;
+    const float* inv = p.inv2 + (int64_t)__builtin_amdgcn_readfirstlane(sh.expert[of]) * p.D;
+    const int b = sh.start[of], mc = sh.start[of + 1] - b;
 #pragma unroll
-      for (int r = 0; r < R; ++r) turn_codes<PACKED>(w[j][r], turn);
-      Tokens t[NT];
-      operands(x[j], t, cm);
-      mask_unit<R, NT>(w[j], t, cu, F);
-      multiply<R, NT>(w[j], t, acc);
-      load(w[j], x[j]);
-      if (j < left && (++cu == units || j + 1 == left)) {
-        // the rows' scales through the scalar cache, past the loads in flight
-        typedef const __attribute__((address_space(4))) float* ScalarPtr;
-        const float* inv = p.inv2 + (int64_t)__builtin_amdgcn_readfirstlane(sh.expert[ca]) * p.D;
-        const int b = sh.start[ca], mc = sh.start[ca + 1] - b;
+    for (int r = 0; r < R; ++r) {
+      const ScalarPtr sp = (ScalarPtr)(uintptr_t)(inv + row_of(r));
+      float c[4];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const ScalarPtr sp = (ScalarPtr)(uintptr_t)(inv + row_of(r));
-          float c[4];
+      for (int z = 0; z < 4; ++z) {
+        float v[4] = {sp[z], sp[4 + z], sp[8 + z], sp[12 + z]};
+        asm("" : "+s"(v[0]), "+s"(v[1]), "+s"(v[2]), "+s"(v[3]));  // loaded as scalars, then chosen by lane
+        c[z] = kg < 2 ? (kg == 0 ? v[0] : v[1]) : (kg == 2 ? v[2] : v[3]);
+      }
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            float v[4] = {sp[z], sp[4 + z], sp[8 + z], sp[12 + z]};
-            asm("" : "+s"(v[0]), "+s"(v[1]), "+s"(v[2]), "+s"(v[3]));  // loaded as scalars, then chosen by lane
-            c[z] = kg < 2 ? (kg == 0 ? v[0] : v[1]) : (kg == 2 ? v[2] : v[3]);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            // an expert's tokens differ, so no two lanes meet
-            if (16 * n + lr < mc) {
-              float4* d = reinterpret_cast<float4*>(sum + sh.token[b + 16 * n + lr] * kDownRows + 16 * r + 4 * kg);
-              float4 v = *d;
-              v.x += acc[r][n][0] * c[0];
-              v.y += acc[r][n][1] * c[1];
-              v.z += acc[r][n][2] * c[2];
-              v.w += acc[r][n][3] * c[3];
-              *d = v;
-            }
-            acc[r][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-          }
+      for (int n = 0; n < NT; ++n) {
+        // an expert's tokens differ, so no two lanes meet
+        if (16 * n + lr < mc) {
+          float4* d = reinterpret_cast<float4*>(sum + sh.token[b + 16 * n + lr] * kDownRows + 16 * r + 4 * kg);
+          float4 v = *d;
+          v.x += acc[r][n][0] * c[0];
+          v.y += acc[r][n][1] * c[1];
+          v.z += acc[r][n][2] * c[2];
+          v.w += acc[r][n][3] * c[3];
+          *d = v;
         }
-        cu = 0;
-        ++ca;
-        if (j + 1 < left)
-          cm = (__builtin_amdgcn_readfirstlane(sh.start[ca + 1]) - __builtin_amdgcn_readfirstlane(sh.start[ca]) + 3) & ~3;
+        acc[r][n] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
       }
     }
   }
