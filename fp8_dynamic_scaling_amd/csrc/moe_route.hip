@@ -9,15 +9,18 @@
 // 0, below every other, and are never chosen; a token with fewer than k other
 // logits gets id -1 and weight 0 in the slots left.
 //
-// Sorting is by counting. A block of tokens counts its pairs an expert and
-// numbers each pair among its block's (in token order); a second launch adds,
-// for every block, the counts of the blocks before it and of the experts before
-// it. No atomics: the order is that of a stable sort, whatever the schedule.
-// With one block (up to 64 tokens) a single launch does all.
+// Sorting is by counting. 64 tokens at a time mark themselves in a 64-bit word of
+// each expert they chose: the bits below a token's own are the earlier pairs of
+// that expert, all of them its count. A second launch adds, for every block of
+// tokens, the counts of the blocks before it and of the experts before it. No
+// order but the tokens' enters: it is that of a stable sort, whatever the
+// schedule. With one block (up to 64 tokens) a single launch does all.
 //
-// G lanes share a token and hold its E logits in registers (V each, element v
-// of lane g being expert g + G v), so that a wavefront works on 64 / G tokens
-// at once: a maximum is V - 1 comparisons and log2 G exchanges.
+// G lanes share a token and hold its E logits in registers (V each, by fours:
+// element v of lane g is expert 4 (g + G (v / 4)) + v % 4), so that a wavefront
+// works on 64 / G tokens at once: a maximum is V - 1 comparisons and log2 G
+// exchanges between lanes, up to 16 lanes within the vector unit. What remains is
+// latency: the exchanges, k rounds of them, and two to three trips to memory.
 #include <type_traits>
 
 #include "common.hpp"
@@ -39,12 +42,88 @@ int64_t route_block_tokens(int64_t T) {
 }
 }  // namespace
 
-template <bool F32>
-__device__ __forceinline__ float ld_logit(const void* p, int64_t i) {
-  if constexpr (F32)
-    return static_cast<const float*>(p)[i];
-  else
-    return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+constexpr int kRouteThreads = 512;
+
+template <int G>
+__device__ __forceinline__ int expert_of(int g, int v) {
+  return 4 * (g + G * (v >> 2)) + (v & 3);
+}
+
+// A token's logits in its lanes; -inf behind E and where the token is not live.
+// vec: rows are 16-byte (bf16: 8-byte) aligned and E % 4 == 0.
+template <int G, int V, bool F32>
+__device__ __forceinline__ void load_logits(const void* p, int64_t t, int E, int g, bool live, bool vec,
+                                            float (&l)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; v += 4) {
+    const int e = expert_of<G>(g, v);
+    const int64_t at = t * E + e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l[v + i] = -INFINITY;
+    if (!live || e >= E) continue;
+    if (vec) {
+      if constexpr (F32) {
+        const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+        l[v] = f.x;
+        l[v + 1] = f.y;
+        l[v + 2] = f.z;
+        l[v + 3] = f.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+        l[v] = bf16_lo(w.x);
+        l[v + 1] = bf16_hi(w.x);
+        l[v + 2] = bf16_lo(w.y);
+        l[v + 3] = bf16_hi(w.y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (e + i >= E) continue;
+        if constexpr (F32)
+          l[v + i] = static_cast<const float*>(p)[at + i];
+        else
+          l[v + i] = __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[at + i] << 16);
+      }
+    }
+  }
+}
+
+// The value of the lane that a group's reduction step S pairs this one with:
+// lanes 1, 2 apart, then mirrored in 8 and in 16 (the lanes of a half are equal by
+// then), then 16 and 32 apart.
+template <int S>
+__device__ __forceinline__ uint32_t partner(uint32_t v) {
+  if constexpr (S == 0) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true);
+  if constexpr (S == 1) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true);
+  if constexpr (S == 2) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true);
+  if constexpr (S == 3) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true);
+  return (uint32_t)__shfl_xor((int)v, S == 4 ? 16 : 32, 64);
+}
+// Reduction over the G lanes of a group by op(a, b), symmetric; every lane gets it.
+template <int G, int S = 0, class T, class Op>
+__device__ __forceinline__ T group_reduce(T v, Op op) {
+  if constexpr ((1 << S) >= G) {
+    return v;
+  } else {
+    T w;
+    if constexpr (sizeof(T) == 8)
+      w = ((T)partner<S>((uint32_t)(v >> 32)) << 32) | partner<S>((uint32_t)v);
+    else
+      w = __builtin_bit_cast(T, partner<S>(__builtin_bit_cast(uint32_t, v)));
+    return group_reduce<G, S + 1>(op(v, w), op);
+  }
+}
+template <int G>
+__device__ __forceinline__ uint64_t group_max(uint64_t v) {
+  return group_reduce<G>(v, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+}
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+  return group_reduce<G>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+  return group_reduce<G>(v, [](float a, float b) { return a + b; });
 }
 
 // Order-preserving key of a logit and its expert; 0 for -inf and NaN.
@@ -60,77 +139,63 @@ __device__ __forceinline__ float key_logit(uint64_t key) {
   return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
-template <int G>
-__device__ __forceinline__ uint64_t group_max(uint64_t v) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) {
-    const uint64_t w = __shfl_xor((unsigned long long)v, o, 64);
-    v = w > v ? w : v;
-  }
-  return v;
-}
-template <int G>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-
-// The pair's place among the earlier pairs of its block with the same expert,
-// for 64 pairs of a wavefront in their order; cnt holds the counts so far and
-// is brought up to date. e: the pair's expert, -1 for none.
-__device__ __forceinline__ int wave_rank(int e, int bits, uint32_t* cnt) {
-  uint64_t same = __ballot(e >= 0);
-  for (int b = 0; b < bits; ++b) {
-    const uint64_t set = __ballot((e >> b) & 1);
-    same &= (e >> b) & 1 ? set : ~set;
-  }
+// Exclusive sums of n words in LDS, by the first wavefront; returns the total.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t* x, int n) {
   const int lane = threadIdx.x & 63;
-  const int before = __popcll(same & ((1ull << lane) - 1));
-  const uint32_t c = e >= 0 ? cnt[e] : 0;
-  // the first of an expert's pairs writes, after all of them have read
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  if (e >= 0 && before == 0) cnt[e] = c + (uint32_t)__popcll(same);
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  return (int)c + before;
+  uint32_t run = 0;
+  for (int e0 = 0; e0 < n; e0 += 64) {
+    const int e = e0 + lane;
+    const uint32_t c = e < n ? x[e] : 0;
+    uint32_t s = c;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t u = __shfl_up(s, o, 64);
+      if (lane >= o) s += u;
+    }
+    if (e < n) x[e] = run + s - c;
+    run += __shfl(s, 63, 64);
+  }
+  return run;
 }
 
 template <int G, int V, bool F32>
-__global__ __launch_bounds__(256) void k_moe_route(const void* __restrict__ logits, int64_t T, int E, int k, int gate,
-                                                   int bits, int64_t block_tokens, int32_t* __restrict__ ids,
-                                                   float* __restrict__ weights, int32_t* __restrict__ offsets,
-                                                   int32_t* __restrict__ order, int32_t* __restrict__ slot,
-                                                   uint32_t* __restrict__ counts) {
-  extern __shared__ uint32_t lds[];
-  uint32_t* cnt = lds;                                         // [E]
-  int32_t* cid = reinterpret_cast<int32_t*>(lds + E);          // [kChunk * k]
-  float* cval = reinterpret_cast<float*>(lds + E + kChunk * k);  // [kChunk * k]
+__global__ __launch_bounds__(kRouteThreads) void k_moe_route(const void* __restrict__ logits, int64_t T, int E, int k,
+                                                             int gate, int vec, int64_t block_tokens,
+                                                             int32_t* __restrict__ ids, float* __restrict__ weights,
+                                                             int32_t* __restrict__ offsets,
+                                                             int32_t* __restrict__ order, int32_t* __restrict__ slot,
+                                                             uint32_t* __restrict__ counts) {
+  extern __shared__ uint64_t lds64[];
+  uint64_t* mark = lds64;                                      // [E] the tokens of the chunk that chose e
+  uint32_t* cnt = reinterpret_cast<uint32_t*>(lds64 + E);      // [E] the pairs of the chunks before
+  int32_t* cid = reinterpret_cast<int32_t*>(cnt + E);          // [kChunk * k]
+  float* cval = reinterpret_cast<float*>(cid + kChunk * k);    // [kChunk * k]
+  __shared__ uint32_t total;
   constexpr int PER = 64 / G;  // tokens a wavefront works on at once
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane % G;
   const int64_t first = (int64_t)blockIdx.x * block_tokens;
   const int64_t last = first + block_tokens < T ? first + block_tokens : T;
   const bool sorted = offsets != nullptr;
-  if (sorted)
-    for (int e = threadIdx.x; e < E; e += 256) cnt[e] = 0;
+  if (sorted) {
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+      cnt[e] = 0;
+      mark[e] = 0;
+    }
+    __syncthreads();
+  }
   for (int64_t chunk = first; chunk < last; chunk += kChunk) {
-    for (int base = wave * PER; base < kChunk; base += 4 * PER) {
+    for (int base = wave * PER; base < kChunk; base += kRouteThreads / 64 * PER) {
       const int ct = base + lane / G;
       const int64_t t = chunk + ct;
-      const bool live = t < last && ct < kChunk;
+      const bool live = t < last;
       float l[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = g + G * v;
-        l[v] = live && e < E ? ld_logit<F32>(logits, t * E + e) : -INFINITY;
-      }
+      load_logits<G, V, F32>(logits, t, E, g, live, vec != 0, l);
       uint64_t key[V];
       float bad = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        key[v] = logit_key(l[v], g + G * v);
+        key[v] = logit_key(l[v], expert_of<G>(g, v));
         if (l[v] != l[v]) bad = l[v];
       }
       bad = group_sum<G>(bad);  // 0, or NaN where a logit of the token is
@@ -146,8 +211,10 @@ __global__ __launch_bounds__(256) void k_moe_route(const void* __restrict__ logi
         if (j == 0) top = val;
         zk += m ? expf(val - top) : 0.0f;
         if (g == 0 && live) {
-          cid[ct * k + j] = m ? key_expert(m) : -1;
+          const int e = m ? key_expert(m) : -1;
+          cid[ct * k + j] = e;
           cval[ct * k + j] = val;
+          if (sorted && e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mark[e]), 1ull << ct);
         }
       }
       float z = zk;
@@ -158,9 +225,8 @@ __global__ __launch_bounds__(256) void k_moe_route(const void* __restrict__ logi
         z = group_sum<G>(z);
       }
       // the group's own writes to LDS, read back by its other lanes
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
       if (live) {
         for (int j = g; j < k; j += G) {
           const int e = cid[ct * k + j];
@@ -173,58 +239,37 @@ __global__ __launch_bounds__(256) void k_moe_route(const void* __restrict__ logi
     }
     if (!sorted) continue;
     __syncthreads();
-    if (wave == 0) {
-      const int64_t left = last - chunk;
-      const int n = (int)(left < kChunk ? left : kChunk) * k;
-      for (int i0 = 0; i0 < n; i0 += 64) {
-        const int i = i0 + lane;
-        const int e = i < n ? cid[i] : -1;
-        const int r = wave_rank(e, bits, cnt);
-        if (i < n) slot[chunk * k + i] = e >= 0 ? r : -1;
+    const int n = (int)(last - chunk < kChunk ? last - chunk : kChunk) * k;
+    if (gridDim.x == 1) {
+      // the only block, and its only chunk (block_tokens == kChunk)
+      for (int e = threadIdx.x; e < E; e += kRouteThreads) cnt[e] = __popcll(mark[e]);
+      __syncthreads();
+      if (wave == 0) {
+        const uint32_t sum = wave_scan(cnt, E);
+        if (lane == 0) total = sum;
       }
+      __syncthreads();
+      for (int e = threadIdx.x; e <= E; e += kRouteThreads) offsets[e] = (int32_t)(e < E ? cnt[e] : total);
+    }
+    for (int i = threadIdx.x; i < n; i += kRouteThreads) {
+      const int e = cid[i];
+      const int at = e >= 0 ? (int)cnt[e] + __popcll(mark[e] & ((1ull << (i / k)) - 1)) : -1;
+      slot[chunk * k + i] = at;
+      if (gridDim.x == 1) {
+        if (at >= 0) order[at] = i;
+        if (i >= (int)total) order[i] = -1;
+      }
+    }
+    if (gridDim.x == 1) return;
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+      cnt[e] += __popcll(mark[e]);
+      mark[e] = 0;
     }
     __syncthreads();
   }
-  if (!sorted) return;
-  if (gridDim.x > 1) {
-    for (int e = threadIdx.x; e < E; e += 256) counts[(int64_t)blockIdx.x * E + e] = cnt[e];
-    return;
-  }
-  // one block: its counts are the totals, and the last chunk's ids are at hand
-  // (block_tokens == kChunk)
-  uint32_t run = 0;
-  if (wave == 0) {
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int e = e0 + lane;
-      const uint32_t c = e < E ? cnt[e] : 0;
-      uint32_t s = c;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t u = __shfl_up(s, o, 64);
-        if (lane >= o) s += u;
-      }
-      if (e < E) {
-        cnt[e] = run + s - c;
-        offsets[e] = (int32_t)(run + s - c);
-      }
-      run += __shfl(s, 63, 64);
-    }
-    if (lane == 0) {
-      offsets[E] = (int32_t)run;
-      cval[0] = __uint_as_float(run);  // the gate values are no longer needed
-    }
-  }
-  __syncthreads();
-  const int total = (int)__float_as_uint(cval[0]);
-  for (int i = threadIdx.x; i < (int)(last - first) * k; i += 256) {
-    const int e = cid[i];
-    if (e >= 0) {
-      const int at = (int)cnt[e] + slot[i];
-      slot[i] = at;
-      order[at] = i;
-    }
-    if (i >= total) order[i] = -1;
-  }
+  if (sorted)
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) counts[(int64_t)blockIdx.x * E + e] = cnt[e];
 }
 
 // Second launch, for more than one block: block b's pairs of expert e begin at
@@ -259,28 +304,13 @@ __global__ __launch_bounds__(256) void k_moe_route_place(const uint32_t* __restr
   }
   __syncthreads();
   if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    uint32_t run = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int e = e0 + lane;
-      const uint32_t c = e < E ? total[e] : 0;
-      uint32_t s = c;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t u = __shfl_up(s, o, 64);
-        if (lane >= o) s += u;
-      }
-      if (e < E) {
-        base[e] += run + s - c;
-        if (b == 0) offsets[e] = (int32_t)(run + s - c);
-      }
-      run += __shfl(s, 63, 64);
-    }
-    if (lane == 0) {
-      all = run;
-      if (b == 0) offsets[E] = (int32_t)run;
-    }
+    const uint32_t sum = wave_scan(total, E);
+    if (threadIdx.x == 0) all = sum;
   }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += 256) base[e] += total[e];
+  if (b == 0)
+    for (int e = threadIdx.x; e <= E; e += 256) offsets[e] = (int32_t)(e < E ? total[e] : all);
   __syncthreads();
   const int64_t first = (int64_t)b * block_tokens * k;
   const int64_t last = first + block_tokens * k < T * k ? first + block_tokens * k : T * k;
@@ -319,17 +349,21 @@ static void by_experts(int E, F&& go) {
     go(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
 }
 
+// Whether every row of logits can be loaded by fours.
+static int rows_aligned(const void* logits, int E, bool f32) {
+  return E % 4 == 0 && (uintptr_t)logits % (f32 ? 16 : 8) == 0;
+}
+
 hipError_t launch_moe_route(const RouteArgs& a) {
   if (a.T == 0) return hipSuccess;
   const int64_t bt = route_block_tokens(a.T);
   const int64_t blocks = (a.T + bt - 1) / bt;
-  int bits = 0;
-  while ((1 << bits) < a.E) ++bits;
-  const size_t lds = 4 * ((size_t)a.E + 2 * kChunk * a.k);
+  const size_t lds = 12 * (size_t)a.E + 8 * kChunk * a.k;
+  const int vec = rows_aligned(a.logits, a.E, a.f32);
   by_experts(a.E, [&](auto G, auto V) {
     auto kern = a.f32 ? k_moe_route<G.value, V.value, true> : k_moe_route<G.value, V.value, false>;
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), lds, a.stream, a.logits, a.T, a.E, a.k, a.gate, bits,
-                       bt, a.ids, a.weights, a.offsets, a.order, a.slot, a.ws);
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kRouteThreads), lds, a.stream, a.logits, a.T, a.E, a.k,
+                       a.gate, vec, bt, a.ids, a.weights, a.offsets, a.order, a.slot, a.ws);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || blocks == 1 || !a.offsets) return e;
@@ -345,7 +379,7 @@ hipError_t launch_moe_route(const RouteArgs& a) {
 //   SIGMOID       dl_s = w_s (1 - w_s) dw_s, 0 elsewhere
 // p is computed again from the logits; -inf and a token of -inf alone get 0.
 template <int G, int V, bool F32>
-__global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, int64_t T, int E, int k, int gate,
+__global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, int64_t T, int E, int k, int gate, int vec,
                                                        const int32_t* __restrict__ ids,
                                                        const float* __restrict__ weights,
                                                        const float* __restrict__ dweights, void* dlogits) {
@@ -353,7 +387,8 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, int64
   const int g = threadIdx.x % G;
   const int64_t t = (int64_t)blockIdx.x * PER + threadIdx.x / G;
   const bool live = t < T;
-  float d[V];
+  float l[V], d[V];
+  if (gate == kGateSoftmax) load_logits<G, V, F32>(logits, t, E, g, live, (vec & 1) != 0, l);
 #pragma unroll
   for (int v = 0; v < V; ++v) d[v] = 0.0f;
   float dot = 0.0f;
@@ -361,15 +396,10 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, int64
     dot += ids[t * k + j] >= 0 ? weights[t * k + j] * dweights[t * k + j] : 0.0f;
   dot = group_sum<G>(dot);
   if (gate == kGateSoftmax) {
-    float l[V], top = -INFINITY, z = 0.0f;
+    float top = -INFINITY, z = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = g + G * v;
-      l[v] = live && e < E ? ld_logit<F32>(logits, t * E + e) : -INFINITY;
-      top = fmaxf(top, l[v]);
-    }
-#pragma unroll
-    for (int o = 1; o < G; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    for (int v = 0; v < V; ++v) top = fmaxf(top, l[v]);
+    top = group_max<G>(top);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       // a NaN logit stays one, so the token's gradients are NaN as its weights were
@@ -386,28 +416,43 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, int64
     const float w = weights[t * k + j], dw = dweights[t * k + j];
     const float c = gate == kGateSigmoid ? w * (1.0f - w) * dw : gate == kGateSoftmaxTopk ? w * (dw - dot) : w * dw;
 #pragma unroll
-    for (int v = 0; v < V; ++v) d[v] += e == g + G * v ? c : 0.0f;
+    for (int v = 0; v < V; ++v) d[v] += e == expert_of<G>(g, v) ? c : 0.0f;
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = g + G * v;
+  for (int v = 0; v < V; v += 4) {
+    const int e = expert_of<G>(g, v);
+    const int64_t at = t * E + e;
     if (e >= E) continue;
-    if constexpr (F32) {
-      static_cast<float*>(dlogits)[t * E + e] = d[v];
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 b01 = {(__bf16)d[v], (__bf16)d[v + 1]}, b23 = {(__bf16)d[v + 2], (__bf16)d[v + 3]};
+    const uint2 w = make_uint2(__builtin_bit_cast(uint32_t, b01), __builtin_bit_cast(uint32_t, b23));
+    if (vec & 2) {
+      if constexpr (F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(dlogits) + at) =
+            make_float4(d[v], d[v + 1], d[v + 2], d[v + 3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dlogits) + at) = w;
     } else {
-      const __bf16 b = (__bf16)d[v];
-      static_cast<uint16_t*>(dlogits)[t * E + e] = __builtin_bit_cast(uint16_t, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (e + i >= E) continue;
+        if constexpr (F32)
+          static_cast<float*>(dlogits)[at + i] = d[v + i];
+        else
+          static_cast<uint16_t*>(dlogits)[at + i] = (uint16_t)((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
+      }
     }
   }
 }
 
 hipError_t launch_moe_route_bwd(const RouteBwdArgs& a) {
   if (a.T == 0) return hipSuccess;
+  const int vec = rows_aligned(a.logits, a.E, a.f32) | rows_aligned(a.dlogits, a.E, a.f32) << 1;
   by_experts(a.E, [&](auto G, auto V) {
     auto kern = a.f32 ? k_moe_route_bwd<G.value, V.value, true> : k_moe_route_bwd<G.value, V.value, false>;
     const int64_t per = 256 / G.value;
     hipLaunchKernelGGL(kern, dim3((unsigned)((a.T + per - 1) / per)), dim3(256), 0, a.stream, a.logits, a.T, a.E, a.k,
-                       a.gate, a.ids, a.weights, a.dweights, a.dlogits);
+                       a.gate, vec, a.ids, a.weights, a.dweights, a.dlogits);
   });
   return hipGetLastError();
 }

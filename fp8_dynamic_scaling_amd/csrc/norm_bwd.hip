@@ -12,10 +12,12 @@
 // dgamma and dbeta are rounded once, to bf16.
 //
 // The kernel is bound by HBM: it reads dy, h and dh and writes dx once, 8 B an
-// element. TPR threads hold a row (64, 256 or 1024: at most 16 elements a
-// lane), so that a lane keeps its columns of gamma and of the dgamma and dbeta
-// sums in registers over all the rows of its workgroup; the next row is loaded
-// while the present one is reduced.
+// element. TPR threads hold a row in J pieces of 8 elements each, so that a lane
+// keeps its columns of gamma and of the dgamma and dbeta sums in registers over
+// all the rows of its workgroup; the next row is loaded while the present one
+// is reduced.
+#include <type_traits>
+
 #include "common.hpp"
 #include "internal.hpp"
 
@@ -24,19 +26,19 @@ namespace fp8dyn {
 typedef __bf16 nb_bf16x2 __attribute__((ext_vector_type(2)));
 
 namespace {
-constexpr int kJ = 2;             // 8-element pieces of a row a lane holds
 constexpr int kMaxBwdBlocks = 512;  // workgroups, each with one row of partial column sums
 
-int bwd_tpr(int64_t cols) { return cols <= 64 * 8 * kJ ? 64 : cols <= 256 * 8 * kJ ? 256 : 1024; }
+// Threads a row: as few pieces a lane as there are threads for.
+int bwd_tpr(int64_t cols) { return cols <= 1024 ? 64 : cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024; }
 
-// Workgroups: at most kMaxBwdBlocks (two of 256 threads a CU), and at least 4 rows to
-// each row slot where there are that many, so that the partial sums stay a
-// fraction of the rows read.
+// Workgroups: at most kMaxBwdBlocks (two of 256 threads a CU, or one of 512),
+// and two rows to a row slot where there are that many, so that the partial sums stay
+// below the rows read.
 int64_t bwd_blocks(int64_t rows, int64_t cols) {
   const int tpr = bwd_tpr(cols);
-  const int64_t slots = tpr == 64 ? 4 : 1, most = tpr == 1024 ? kMaxBwdBlocks / 2 : kMaxBwdBlocks;
+  const int64_t slots = tpr == 64 ? 4 : 1, most = tpr >= 512 ? kMaxBwdBlocks / 2 : kMaxBwdBlocks;
   const int64_t groups = (rows + slots - 1) / slots;
-  const int64_t b = (groups + 3) / 4;
+  const int64_t b = (groups + 1) / 2;
   return b < 1 ? 1 : b > most ? most : b;
 }
 }  // namespace
@@ -47,7 +49,8 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-template <int TPR, bool LAYER>
+// AHEAD: the next row is loaded ahead; 1024 threads a row leave no registers for that.
+template <int TPR, int J, bool LAYER, bool AHEAD>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_bwd(
     const uint16_t* dy, const uint16_t* dh, const uint16_t* __restrict__ h, const uint16_t* __restrict__ gamma,
     const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows, int64_t cols, uint16_t* dx,
@@ -56,70 +59,71 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_bwd(
   constexpr int SLOTS = NT / TPR;
   constexpr int WAVES = TPR / 64;  // wavefronts that share a row
   __shared__ float red[2][2][WAVES];
-  __shared__ float comb[SLOTS > 1 ? SLOTS * 64 * 8 * kJ : 1];
+  __shared__ float comb[SLOTS > 1 ? SLOTS * 64 * 8 * J : 1];
   const int t = threadIdx.x % TPR;
   const int slot = threadIdx.x / TPR;
   const int64_t stride = (int64_t)gridDim.x * SLOTS;
   const float inv_n = 1.0f / (float)cols;
-  bool in[kJ];
-  float ga[kJ][8], sg[kJ][8], sb[kJ][8];
+  bool in[J];
+  uint4 ga[J];
+  float sg[J][8], sb[J][8];
 #pragma unroll
-  for (int j = 0; j < kJ; ++j) {
+  for (int j = 0; j < J; ++j) {
     const int64_t c = 8 * (t + TPR * j);
     in[j] = c < cols;
-    const uint4 g = in[j] ? *reinterpret_cast<const uint4*>(gamma + c) : make_uint4(0, 0, 0, 0);
-    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      ga[j][2 * k] = bf16_lo(w[k]);
-      ga[j][2 * k + 1] = bf16_hi(w[k]);
-    }
+    ga[j] = in[j] ? *reinterpret_cast<const uint4*>(gamma + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int k = 0; k < 8; ++k) sg[j][k] = sb[j][k] = 0.0f;
   }
-  uint4 vy[kJ], vh[kJ], vd[kJ];
-  float mu = 0.0f, rs = 0.0f;
+  struct Row {
+    uint4 y[J], h[J], d[J];
+    float mu, rs;
+  } next;
   auto load = [&](int64_t row) {
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
+    for (int j = 0; j < J; ++j) {
       const int64_t o = row * cols + 8 * (t + TPR * j);
-      vy[j] = in[j] ? ld_nt16(dy + o) : make_uint4(0, 0, 0, 0);
-      vh[j] = in[j] ? ld_nt16(h + o) : make_uint4(0, 0, 0, 0);
-      vd[j] = dh && in[j] ? ld_nt16(dh + o) : make_uint4(0, 0, 0, 0);
+      next.y[j] = in[j] ? ld_nt16(dy + o) : make_uint4(0, 0, 0, 0);
+      next.h[j] = in[j] ? ld_nt16(h + o) : make_uint4(0, 0, 0, 0);
+      next.d[j] = dh && in[j] ? ld_nt16(dh + o) : make_uint4(0, 0, 0, 0);
     }
-    rs = rstd[row];
-    if constexpr (LAYER) mu = mean[row];
+    next.rs = rstd[row];
+    next.mu = LAYER ? mean[row] : 0.0f;
   };
   int64_t row = (int64_t)blockIdx.x * SLOTS + slot;
-  if (row < rows) load(row);
+  if (AHEAD && row < rows) load(row);
   int buf = 0;
   // rows of a workgroup with several waves a row are the same for all of them,
   // so every wave reaches every barrier
   for (; row < rows; row += stride) {
-    float g[kJ][8], xh[kJ][8], c1 = 0.0f, c2 = 0.0f;
+    if (!AHEAD) load(row);
+    Row cur = next;
+    if (AHEAD && row + stride < rows) load(row + stride);
+    // element k of piece j: dy, xh and g; zeros in lanes past the row's end
+    auto element = [&](int j, int k, float& y, float& xh, float& g) {
+      const uint32_t a[4] = {cur.y[j].x, cur.y[j].y, cur.y[j].z, cur.y[j].w};
+      const uint32_t b[4] = {cur.h[j].x, cur.h[j].y, cur.h[j].z, cur.h[j].w};
+      const uint32_t c[4] = {ga[j].x, ga[j].y, ga[j].z, ga[j].w};
+      y = k & 1 ? bf16_hi(a[k >> 1]) : bf16_lo(a[k >> 1]);
+      const float x = k & 1 ? bf16_hi(b[k >> 1]) : bf16_lo(b[k >> 1]);
+      xh = LAYER ? (in[j] ? (x - cur.mu) * cur.rs : 0.0f) : x * cur.rs;
+      g = y * (k & 1 ? bf16_hi(c[k >> 1]) : bf16_lo(c[k >> 1]));
+    };
+    float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      const uint32_t a[4] = {vy[j].x, vy[j].y, vy[j].z, vy[j].w}, b[4] = {vh[j].x, vh[j].y, vh[j].z, vh[j].w};
+    for (int j = 0; j < J; ++j) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float y = k & 1 ? bf16_hi(a[k >> 1]) : bf16_lo(a[k >> 1]);
-        const float x = k & 1 ? bf16_hi(b[k >> 1]) : bf16_lo(b[k >> 1]);
-        // lanes past the row's end hold zeros in dy, gamma and h: no term of theirs counts
-        xh[j][k] = LAYER ? (in[j] ? (x - mu) * rs : 0.0f) : x * rs;
-        g[j][k] = y * ga[j][k];
-        c2 += g[j][k] * xh[j][k];
+        float y, xh, g;
+        element(j, k, y, xh, g);
+        c2 += g * xh;
         if constexpr (LAYER) {
-          c1 += g[j][k];
+          c1 += g;
           sb[j][k] += y;
         }
-        sg[j][k] += y * xh[j][k];
+        sg[j][k] += y * xh;
       }
     }
-    uint4 d[kJ];
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) d[j] = vd[j];
-    const float r = rs;
-    if (row + stride < rows) load(row + stride);
     c2 = wave_sum(c2);
     if constexpr (LAYER) c1 = wave_sum(c1);
     if constexpr (WAVES > 1) {
@@ -140,15 +144,26 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_bwd(
     }
     c2 *= inv_n;
     c1 *= inv_n;
+    if constexpr (!AHEAD && LAYER) {
+      // as if the packed row were new: else the compiler keeps g and xh of the
+      // first pass and spills
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
+      for (int j = 0; j < J; ++j)
+        asm volatile("" : "+v"(cur.y[j].x), "+v"(cur.y[j].y), "+v"(cur.y[j].z), "+v"(cur.y[j].w), "+v"(cur.h[j].x),
+                     "+v"(cur.h[j].y), "+v"(cur.h[j].z), "+v"(cur.h[j].w));
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
       if (!in[j]) continue;
-      const uint32_t e[4] = {d[j].x, d[j].y, d[j].z, d[j].w};
+      const uint32_t e[4] = {cur.d[j].x, cur.d[j].y, cur.d[j].z, cur.d[j].w};
       uint32_t o[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float lo = bf16_lo(e[k]) + r * (g[j][2 * k] - c1 - xh[j][2 * k] * c2);
-        const float hi = bf16_hi(e[k]) + r * (g[j][2 * k + 1] - c1 - xh[j][2 * k + 1] * c2);
+        float y, x0, g0, x1, g1;
+        element(j, 2 * k, y, x0, g0);
+        element(j, 2 * k + 1, y, x1, g1);
+        const float lo = bf16_lo(e[k]) + cur.rs * (g0 - c1 - x0 * c2);
+        const float hi = bf16_hi(e[k]) + cur.rs * (g1 - c1 - x1 * c2);
         const nb_bf16x2 p = {(__bf16)lo, (__bf16)hi};
         o[k] = __builtin_bit_cast(uint32_t, p);
       }
@@ -163,20 +178,20 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_bwd(
     if constexpr (SLOTS > 1) {
       if (z) __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kJ; ++j)
+      for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          comb[slot * (64 * 8 * kJ) + 8 * (t + TPR * j) + k] = z ? sb[j][k] : sg[j][k];
+          comb[slot * (64 * 8 * J) + 8 * (t + TPR * j) + k] = z ? sb[j][k] : sg[j][k];
       __syncthreads();
       for (int c = threadIdx.x; c < cols; c += NT) {
         float a = comb[c];
 #pragma unroll
-        for (int i = 1; i < SLOTS; ++i) a += comb[i * (64 * 8 * kJ) + c];
+        for (int i = 1; i < SLOTS; ++i) a += comb[i * (64 * 8 * J) + c];
         dst[c] = a;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
+      for (int j = 0; j < J; ++j) {
         if (!in[j]) continue;
         float4* o = reinterpret_cast<float4*>(dst + 8 * (t + TPR * j));
         const float* v = z ? sb[j] : sg[j];
@@ -232,22 +247,23 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a) {
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(threads), 0, a.stream, a.dy, a.dh, a.h, a.gamma, a.mean,
                        a.rstd, a.rows, a.cols, a.dx, a.ws, want);
   };
+  auto by_kind = [&](auto T, auto P) {
+    const int threads = T.value == 64 ? 256 : T.value;
+    if (a.layer)
+      go(k_norm_bwd<T.value, P.value, true, T.value <= 512>, threads);
+    else
+      go(k_norm_bwd<T.value, P.value, false, T.value <= 512>, threads);
+  };
+  const std::integral_constant<int, 2> two;
   const int tpr = bwd_tpr(a.cols);
-  if (a.layer) {
-    if (tpr == 64)
-      go(k_norm_bwd<64, true>, 256);
-    else if (tpr == 256)
-      go(k_norm_bwd<256, true>, 256);
-    else
-      go(k_norm_bwd<1024, true>, 1024);
-  } else {
-    if (tpr == 64)
-      go(k_norm_bwd<64, false>, 256);
-    else if (tpr == 256)
-      go(k_norm_bwd<256, false>, 256);
-    else
-      go(k_norm_bwd<1024, false>, 1024);
-  }
+  if (tpr == 64)
+    by_kind(std::integral_constant<int, 64>{}, two);
+  else if (tpr == 256)
+    by_kind(std::integral_constant<int, 256>{}, two);
+  else if (tpr == 512)
+    by_kind(std::integral_constant<int, 512>{}, two);
+  else
+    by_kind(std::integral_constant<int, 1024>{}, two);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !want) return e;
   hipLaunchKernelGGL(k_norm_bwd_cols, dim3((unsigned)((a.cols + 31) / 32), a.layer ? 2 : 1), dim3(256), 0, a.stream,

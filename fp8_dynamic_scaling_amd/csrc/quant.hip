@@ -1266,7 +1266,8 @@ __device__ __forceinline__ void exact_add(uint32_t b, long long* L1, long long* 
 // the stored row, so that a backward pass that reads h sees the same values);
 // res may be null (h = x). h is written where asked, and mean32 and rstd32 for
 // the backward. Each lane writes just the elements of h it has read, after it
-// read them, so h may be x or res itself.
+// read them, so h may be x or res itself. h and y are stored past the caches,
+// as q is (8192 x 4096: 59.4 -> 55.5 us).
 struct NormAdd {
   const uint16_t* res;
   uint16_t* h;
@@ -1326,7 +1327,7 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const
           o[k] = __builtin_bit_cast(uint32_t, s);
         }
         v[j] = make_uint4(o[0], o[1], o[2], o[3]);
-        if (add.h && c < cols) *reinterpret_cast<uint4*>(add.h + row * cols + c) = v[j];
+        if (add.h && c < cols) st_nt16(add.h + row * cols + c, v[j]);
       }
     }
   }
@@ -1471,7 +1472,12 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const
     }
     v[j] = make_uint4(o[0], o[1], o[2], o[3]);
     m = amax8(v[j], m);
-    if (y) *reinterpret_cast<uint4*>(y + row * cols + c) = v[j];
+    if (y) {
+      if constexpr (ADD)
+        st_nt16(y + row * cols + c, v[j]);
+      else
+        *reinterpret_cast<uint4*>(y + row * cols + c) = v[j];
+    }
   }
   if (!q) return;
   if constexpr (TPR == 64)
@@ -1500,7 +1506,13 @@ static void launch_norm_quant_t(const NormQuantArgs& a) {
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), block, 0, a.stream, a.x, a.gamma, a.beta, a.rows, a.cols,
                        a.norm_eps, a.y, a.q, a.scale, a.inv, a.fmax, a.eps, add);
   };
-  if (a.cols <= 512 * 8) {  // one wavefront per row
+  if (ADD && a.cols <= 4096 && a.cols > (a.rows <= 1024 ? 1024 : 2048)) {
+    // With two inputs and three outputs a row of over 2048 elements is better
+    // shared by four wavefronts (8192 x 4096 with all outputs: 53.7 us, 55.5 us
+    // with one; 16384 x 2048: 57.9 and 52.9 us); so are fewer rows than SIMDs
+    // (1 x 4096: 3.5 and 6.0 us).
+    go(k_norm_quant_row<256, 2, E5, LAYER, ADD>, a.rows);
+  } else if (a.cols <= 512 * 8) {  // one wavefront per row
     const int64_t J = (a.cols + 511) / 512, blocks = (a.rows + 3) / 4;
     if (J <= 2)
       go(k_norm_quant_row<64, 2, E5, LAYER, ADD>, blocks);
