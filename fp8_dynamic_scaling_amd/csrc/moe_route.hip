@@ -3,10 +3,9 @@
 // offsets that the grouped GEMMs take; and the gate weights' gradient.
 //
 // Choosing compares and never computes, so it is exact: a logit's 32-bit
-// pattern is mapped to an unsigned integer of the same order, with the
-// complement of the expert's index below it, and the largest 64-bit key is
-// taken k times (equal logits: the lowest index first). -inf and NaN have key
-// 0, below every other, and are never chosen; a token with fewer than k other
+// pattern is mapped to an unsigned integer of the same order, and k times the
+// largest is found, then the lowest expert that has it, which is taken out.
+// -inf and NaN have key 0, below every other, and are never chosen; a token with fewer than k other
 // logits gets id -1 and weight 0 in the slots left.
 //
 // Sorting is by counting. 64 tokens at a time mark themselves in a 64-bit word of
@@ -34,15 +33,20 @@ constexpr int kMaxRouteK = 32;
 constexpr int kMaxRouteE = 1024;
 constexpr int kMaxRouteBlocks = 256;
 
-// Tokens a block: a multiple of kChunk, so that at most kMaxRouteBlocks
-// (one a CU) count; the second launch reads all their counts in every block.
+// Tokens a block: all of them up to kChunk; else so that at most kMaxRouteBlocks
+// (one a CU) count, for the second launch reads all their counts in every block.
 int64_t route_block_tokens(int64_t T) {
+  if (T <= kChunk) return kChunk;
   const int64_t per = (T + kMaxRouteBlocks - 1) / kMaxRouteBlocks;
-  return (per + kChunk - 1) / kChunk * kChunk;
+  return per <= kChunk ? (per + 7) / 8 * 8 : (per + kChunk - 1) / kChunk * kChunk;
 }
 }  // namespace
 
-constexpr int kRouteThreads = 512;
+// Threads of a block: a chunk at once for up to 64 experts, and where more lanes
+// share a token as many as a workgroup may have.
+template <int G>
+constexpr int kRouteThreads = G <= 8 ? 512 : 1024;
+constexpr int kPlaceThreads = 1024;
 
 template <int G>
 __device__ __forceinline__ int expert_of(int g, int v) {
@@ -105,17 +109,17 @@ __device__ __forceinline__ T group_reduce(T v, Op op) {
   if constexpr ((1 << S) >= G) {
     return v;
   } else {
-    T w;
-    if constexpr (sizeof(T) == 8)
-      w = ((T)partner<S>((uint32_t)(v >> 32)) << 32) | partner<S>((uint32_t)v);
-    else
-      w = __builtin_bit_cast(T, partner<S>(__builtin_bit_cast(uint32_t, v)));
+    const T w = __builtin_bit_cast(T, partner<S>(__builtin_bit_cast(uint32_t, v)));
     return group_reduce<G, S + 1>(op(v, w), op);
   }
 }
 template <int G>
-__device__ __forceinline__ uint64_t group_max(uint64_t v) {
-  return group_reduce<G>(v, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  return group_reduce<G>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  return group_reduce<G>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
@@ -126,16 +130,13 @@ __device__ __forceinline__ float group_sum(float v) {
   return group_reduce<G>(v, [](float a, float b) { return a + b; });
 }
 
-// Order-preserving key of a logit and its expert; 0 for -inf and NaN.
-__device__ __forceinline__ uint64_t logit_key(float f, int e) {
+// Order-preserving key of a logit; 0 for -inf and NaN.
+__device__ __forceinline__ uint32_t logit_key(float f) {
   if (!(f > -INFINITY)) return 0;
   const uint32_t u = __float_as_uint(f + 0.0f);  // -0 as +0
-  const uint32_t o = u & 0x80000000u ? ~u : u | 0x80000000u;
-  return ((uint64_t)o << 32) | (uint32_t)~e;
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ int key_expert(uint64_t key) { return (int)~(uint32_t)key; }
-__device__ __forceinline__ float key_logit(uint64_t key) {
-  const uint32_t o = (uint32_t)(key >> 32);
+__device__ __forceinline__ float key_logit(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 
@@ -159,7 +160,7 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t* x, int n) {
 }
 
 template <int G, int V, bool F32>
-__global__ __launch_bounds__(kRouteThreads) void k_moe_route(const void* __restrict__ logits, int64_t T, int E, int k,
+__global__ __launch_bounds__(kRouteThreads<G>) void k_moe_route(const void* __restrict__ logits, int64_t T, int E, int k,
                                                              int gate, int vec, int64_t block_tokens,
                                                              int32_t* __restrict__ ids, float* __restrict__ weights,
                                                              int32_t* __restrict__ offsets,
@@ -172,46 +173,52 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(const void* __restr
   float* cval = reinterpret_cast<float*>(cid + kChunk * k);    // [kChunk * k]
   __shared__ uint32_t total;
   constexpr int PER = 64 / G;  // tokens a wavefront works on at once
+  constexpr int NT = kRouteThreads<G>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane % G;
   const int64_t first = (int64_t)blockIdx.x * block_tokens;
   const int64_t last = first + block_tokens < T ? first + block_tokens : T;
   const bool sorted = offsets != nullptr;
   if (sorted) {
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+    for (int e = threadIdx.x; e < E; e += NT) {
       cnt[e] = 0;
       mark[e] = 0;
     }
     __syncthreads();
   }
   for (int64_t chunk = first; chunk < last; chunk += kChunk) {
-    for (int base = wave * PER; base < kChunk; base += kRouteThreads / 64 * PER) {
+    const int here = (int)(last - chunk < kChunk ? last - chunk : kChunk);  // tokens
+    for (int base = wave * PER; base < here; base += NT / 64 * PER) {
       const int ct = base + lane / G;
       const int64_t t = chunk + ct;
-      const bool live = t < last;
+      const bool live = ct < here;
       float l[V];
       load_logits<G, V, F32>(logits, t, E, g, live, vec != 0, l);
-      uint64_t key[V];
+      uint32_t key[V];
       float bad = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        key[v] = logit_key(l[v], expert_of<G>(g, v));
+        key[v] = logit_key(l[v]);
         if (l[v] != l[v]) bad = l[v];
       }
       bad = group_sum<G>(bad);  // 0, or NaN where a logit of the token is
       float top = 0.0f, zk = 0.0f;
       for (int j = 0; j < k; ++j) {
-        uint64_t m = key[0];
+        uint32_t m = key[0];
 #pragma unroll
         for (int v = 1; v < V; ++v) m = key[v] > m ? key[v] : m;
         m = group_max<G>(m);
+        uint32_t best = ~0u;  // the lowest expert with that key (m = 0: none, not used)
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = key[v] == m ? 0 : key[v];
+        for (int v = V - 1; v >= 0; --v) best = key[v] == m ? (uint32_t)expert_of<G>(g, v) : best;
+        best = group_min<G>(best);
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = best == (uint32_t)expert_of<G>(g, v) ? 0 : key[v];
         const float val = m ? key_logit(m) : -INFINITY;
         if (j == 0) top = val;
         zk += m ? expf(val - top) : 0.0f;
         if (g == 0 && live) {
-          const int e = m ? key_expert(m) : -1;
+          const int e = m ? (int)best : -1;
           cid[ct * k + j] = e;
           cval[ct * k + j] = val;
           if (sorted && e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mark[e]), 1ull << ct);
@@ -239,19 +246,19 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(const void* __restr
     }
     if (!sorted) continue;
     __syncthreads();
-    const int n = (int)(last - chunk < kChunk ? last - chunk : kChunk) * k;
+    const int n = here * k;
     if (gridDim.x == 1) {
       // the only block, and its only chunk (block_tokens == kChunk)
-      for (int e = threadIdx.x; e < E; e += kRouteThreads) cnt[e] = __popcll(mark[e]);
+      for (int e = threadIdx.x; e < E; e += NT) cnt[e] = __popcll(mark[e]);
       __syncthreads();
       if (wave == 0) {
         const uint32_t sum = wave_scan(cnt, E);
         if (lane == 0) total = sum;
       }
       __syncthreads();
-      for (int e = threadIdx.x; e <= E; e += kRouteThreads) offsets[e] = (int32_t)(e < E ? cnt[e] : total);
+      for (int e = threadIdx.x; e <= E; e += NT) offsets[e] = (int32_t)(e < E ? cnt[e] : total);
     }
-    for (int i = threadIdx.x; i < n; i += kRouteThreads) {
+    for (int i = threadIdx.x; i < n; i += NT) {
       const int e = cid[i];
       const int at = e >= 0 ? (int)cnt[e] + __popcll(mark[e] & ((1ull << (i / k)) - 1)) : -1;
       slot[chunk * k + i] = at;
@@ -262,19 +269,19 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(const void* __restr
     }
     if (gridDim.x == 1) return;
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+    for (int e = threadIdx.x; e < E; e += NT) {
       cnt[e] += __popcll(mark[e]);
       mark[e] = 0;
     }
     __syncthreads();
   }
   if (sorted)
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) counts[(int64_t)blockIdx.x * E + e] = cnt[e];
+    for (int e = threadIdx.x; e < E; e += NT) counts[(int64_t)blockIdx.x * E + e] = cnt[e];
 }
 
 // Second launch, for more than one block: block b's pairs of expert e begin at
 // offsets[e] + (the counts of e in the blocks before b).
-__global__ __launch_bounds__(256) void k_moe_route_place(const uint32_t* __restrict__ counts, int64_t T, int E, int k,
+__global__ __launch_bounds__(kPlaceThreads) void k_moe_route_place(const uint32_t* __restrict__ counts, int64_t T, int E, int k,
                                                          int64_t block_tokens, const int32_t* __restrict__ ids,
                                                          int32_t* __restrict__ offsets, int32_t* __restrict__ order,
                                                          int32_t* __restrict__ slot) {
@@ -283,16 +290,16 @@ __global__ __launch_bounds__(256) void k_moe_route_place(const uint32_t* __restr
   uint32_t* total = lds + E;  // [E] of all blocks, then the offsets
   __shared__ uint32_t all;
   const int b = blockIdx.x, nb = gridDim.x;
-  for (int e = threadIdx.x; e < 2 * E; e += 256) lds[e] = 0;
+  for (int e = threadIdx.x; e < 2 * E; e += kPlaceThreads) lds[e] = 0;
   __syncthreads();
   // threads share an expert's column of counts where there are fewer experts
   // than threads: integer additions, whose order changes nothing
-  const int parts = E < 256 ? 256 / E : 1;
-  const int part = E < 256 ? threadIdx.x / E : 0;
+  const int parts = E < kPlaceThreads ? kPlaceThreads / E : 1;
+  const int part = E < kPlaceThreads ? threadIdx.x / E : 0;
   if (part < parts) {
-    for (int e = E < 256 ? threadIdx.x % E : threadIdx.x; e < E; e += 256) {
+    for (int e = threadIdx.x % E; e < E; e += kPlaceThreads) {
       uint32_t before = 0, sum = 0;
-#pragma unroll 8
+#pragma unroll 16
       for (int i = part; i < nb; i += parts) {
         const uint32_t c = counts[(int64_t)i * E + e];
         sum += c;
@@ -308,13 +315,13 @@ __global__ __launch_bounds__(256) void k_moe_route_place(const uint32_t* __restr
     if (threadIdx.x == 0) all = sum;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += 256) base[e] += total[e];
+  for (int e = threadIdx.x; e < E; e += kPlaceThreads) base[e] += total[e];
   if (b == 0)
-    for (int e = threadIdx.x; e <= E; e += 256) offsets[e] = (int32_t)(e < E ? total[e] : all);
+    for (int e = threadIdx.x; e <= E; e += kPlaceThreads) offsets[e] = (int32_t)(e < E ? total[e] : all);
   __syncthreads();
   const int64_t first = (int64_t)b * block_tokens * k;
   const int64_t last = first + block_tokens * k < T * k ? first + block_tokens * k : T * k;
-  for (int64_t i = first + threadIdx.x; i < last; i += 256) {
+  for (int64_t i = first + threadIdx.x; i < last; i += kPlaceThreads) {
     const int e = ids[i];
     if (e >= 0) {
       const int32_t at = (int32_t)base[e] + slot[i];
@@ -362,12 +369,13 @@ hipError_t launch_moe_route(const RouteArgs& a) {
   const int vec = rows_aligned(a.logits, a.E, a.f32);
   by_experts(a.E, [&](auto G, auto V) {
     auto kern = a.f32 ? k_moe_route<G.value, V.value, true> : k_moe_route<G.value, V.value, false>;
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kRouteThreads), lds, a.stream, a.logits, a.T, a.E, a.k,
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kRouteThreads<G.value>), lds, a.stream, a.logits, a.T, a.E, a.k,
                        a.gate, vec, bt, a.ids, a.weights, a.offsets, a.order, a.slot, a.ws);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || blocks == 1 || !a.offsets) return e;
-  hipLaunchKernelGGL(k_moe_route_place, dim3((unsigned)blocks), dim3(256), 8 * (size_t)a.E, a.stream, a.ws, a.T, a.E,
+  hipLaunchKernelGGL(k_moe_route_place, dim3((unsigned)blocks), dim3(kPlaceThreads), 8 * (size_t)a.E, a.stream,
+                     a.ws, a.T, a.E,
                      a.k, bt, a.ids, a.offsets, a.order, a.slot);
   return hipGetLastError();
 }
@@ -391,9 +399,12 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, int64
   if (gate == kGateSoftmax) load_logits<G, V, F32>(logits, t, E, g, live, (vec & 1) != 0, l);
 #pragma unroll
   for (int v = 0; v < V; ++v) d[v] = 0.0f;
+  // the pairs are shared by the group's lanes
   float dot = 0.0f;
-  for (int j = g; live && j < k; j += G)
-    dot += ids[t * k + j] >= 0 ? weights[t * k + j] * dweights[t * k + j] : 0.0f;
+  for (int j = g; live && j < k; j += G) {
+    const float wd = weights[t * k + j] * dweights[t * k + j];
+    dot += ids[t * k + j] >= 0 ? wd : 0.0f;
+  }
   dot = group_sum<G>(dot);
   if (gate == kGateSoftmax) {
     float top = -INFINITY, z = 0.0f;
@@ -410,14 +421,23 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, int64
 #pragma unroll
     for (int v = 0; v < V; ++v) d[v] = z == 0.0f ? 0.0f : -l[v] / z * dot;
   }
-  if (!live) return;
-  for (int j = 0; j < k; ++j) {
-    const int e = ids[t * k + j];
-    const float w = weights[t * k + j], dw = dweights[t * k + j];
-    const float c = gate == kGateSigmoid ? w * (1.0f - w) * dw : gate == kGateSoftmaxTopk ? w * (dw - dot) : w * dw;
+  const int base = (threadIdx.x & 63) - g;  // the group's first lane
+  for (int j0 = 0; j0 < k; j0 += G) {
+    int e = -1;
+    float c = 0.0f;
+    if (live && j0 + g < k) {
+      e = ids[t * k + j0 + g];
+      const float w = weights[t * k + j0 + g], dw = dweights[t * k + j0 + g];
+      c = gate == kGateSigmoid ? w * (1.0f - w) * dw : gate == kGateSoftmaxTopk ? w * (dw - dot) : w * dw;
+    }
+    for (int i = 0; i < G && j0 + i < k; ++i) {
+      const int ei = __shfl(e, base + i, 64);
+      const float ci = __shfl(c, base + i, 64);
 #pragma unroll
-    for (int v = 0; v < V; ++v) d[v] += e == expert_of<G>(g, v) ? c : 0.0f;
+      for (int v = 0; v < V; ++v) d[v] += ei == expert_of<G>(g, v) ? ci : 0.0f;
+    }
   }
+  if (!live) return;
 #pragma unroll
   for (int v = 0; v < V; v += 4) {
     const int e = expert_of<G>(g, v);
