@@ -1,6 +1,8 @@
-"""Float8Linear: a Linear layer whose GEMMs run in FP8 on the library's kernels.
+"""Autograd layers over the library's kernels: Float8Linear, a Linear layer whose GEMMs
+run in FP8; AddNorm, the normalization of a residual stream with the addition into it;
+route, an expert router whose sorted rows and offsets the grouped GEMMs take.
 
-The layer is one autograd node with a hand-written backward, as in "FP8
+Float8Linear is one autograd node with a hand-written backward, as in "FP8
 Training: Quantization, Autograd, Torchao", section 6: the quantization and
 the scaled GEMMs are not recorded op by op. Forward and backward are single
 calls of the C ABI (fp8_linear_fwd / fp8_linear_bwd), so every step of the
@@ -19,16 +21,26 @@ What the backward keeps: the bf16 input and weight (references, no copy).
 The kernels write every FP8 operand in the layout its GEMM reads straight
 from bf16, so the backward re-quantizes instead of transposing FP8 copies
 saved by the forward; a deterministic quantizer gives the forward's bytes.
+
+AddNorm and route are one node each as well (fp8_add_norm_quant_row / fp8_add_norm_bwd,
+fp8_moe_route / fp8_moe_route_bwd). As for any node, a backward pass captured into a
+graph needs leaves whose gradients were not accumulated on another stream: capture
+forward and backward together, with torch.autograd.grad or fresh gradients.
 """
 from __future__ import annotations
 
 import math
+from typing import NamedTuple
 
 import torch
 
-from . import (OUT_BF16, RECIPE_ROWWISE_BF16_WGRAD, RECIPE_TENSORWISE, fp8_linear_bwd, fp8_linear_fwd,
-               fp8_linear_ws_bytes, load)
+from . import (E4M3_NATIVE, GATE_SIGMOID, GATE_SOFTMAX, GATE_SOFTMAX_TOPK, NORM_LAYER, NORM_RMS, OUT_BF16,
+               RECIPE_ROWWISE_BF16_WGRAD, RECIPE_TENSORWISE, fp8_add_norm_bwd, fp8_add_norm_bwd_ws_bytes,
+               fp8_add_norm_quant_row, fp8_linear_bwd, fp8_linear_fwd, fp8_linear_ws_bytes, fp8_moe_route,
+               fp8_moe_route_bwd, fp8_moe_route_ws_bytes, load)
 
+_NORMS = {"rms": NORM_RMS, "layer": NORM_LAYER}
+_GATES = {"softmax": GATE_SOFTMAX, "softmax_topk": GATE_SOFTMAX_TOPK, "sigmoid": GATE_SIGMOID}
 _RECIPES = {"rowwise": RECIPE_ROWWISE_BF16_WGRAD, "tensorwise": RECIPE_TENSORWISE}
 
 
@@ -123,3 +135,132 @@ class Float8Linear(torch.nn.Module):
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
                 f"bias={self.bias is not None}, recipe={self.recipe}")
+
+
+class AddNormFunction(torch.autograd.Function):
+    """h = x + res (bf16) and y = norm(h) through fp8_add_norm_quant_row, both differentiable; the
+    gradients of x, res, gamma and beta through fp8_add_norm_bwd. res None: y alone, h = x."""
+
+    @staticmethod
+    def forward(ctx, x, res, gamma, beta, kind: int, norm_eps: float):
+        for t, name in ((x, "input"), (res, "residual"), (gamma, "weight"), (beta, "bias")):
+            if t is None:
+                continue
+            if t.device.type != "cuda":
+                raise RuntimeError(f"AddNorm: {name} must be on a ROCm GPU (got {t.device})")
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"AddNorm: {name} must be bfloat16 (got {t.dtype})")
+        if res is not None and res.shape != x.shape:
+            raise ValueError(f"AddNorm: input {tuple(x.shape)} and residual {tuple(res.shape)} differ in shape")
+        cols = x.shape[-1]
+        if gamma.shape != (cols,):
+            raise ValueError(f"AddNorm: input has {cols} features, weight has {tuple(gamma.shape)}")
+        x2 = x.reshape(-1, cols).contiguous()
+        rows = x2.shape[0]
+        r2 = None if res is None else res.reshape(-1, cols).contiguous()
+        h = x2 if res is None else torch.empty_like(x2)
+        y = torch.empty_like(x2)
+        stats = dict(dtype=torch.float32, device=x.device)
+        mean = torch.empty(rows, **stats) if kind == NORM_LAYER else None
+        rstd = torch.empty(rows, **stats)
+        g = gamma.contiguous()
+        fp8_add_norm_quant_row(x2, r2, g, None if beta is None else beta.contiguous(), kind, norm_eps, E4M3_NATIVE,
+                               1e-12, None if res is None else h, y, None, None, mean=mean, rstd=rstd)
+        ctx.save_for_backward(h, g, mean, rstd)
+        ctx.kind, ctx.shape = kind, x.shape
+        ctx.set_materialize_grads(False)
+        y = y.reshape(x.shape)
+        return y if res is None else (y, h.reshape(x.shape))
+
+    @staticmethod
+    def backward(ctx, dy, dh=None):
+        h, gamma, mean, rstd = ctx.saved_tensors
+        rows, cols = h.shape
+        flat = lambda g: None if g is None else g.to(torch.bfloat16).reshape(rows, cols).contiguous()  # noqa: E731
+        dy, dh = flat(dy), flat(dh)
+        if dy is None:  # only the stream behind h has a gradient
+            dx = None if dh is None else dh.reshape(ctx.shape)
+            return dx, dx, None, None, None, None
+        dx = torch.empty_like(h)
+        dgamma = torch.empty_like(gamma) if ctx.needs_input_grad[2] else None
+        dbeta = torch.empty_like(gamma) if ctx.needs_input_grad[3] else None
+        ws = None
+        if dgamma is not None or dbeta is not None:
+            ws = torch.empty(fp8_add_norm_bwd_ws_bytes(rows, cols, ctx.kind), dtype=torch.uint8, device=h.device)
+        fp8_add_norm_bwd(dy, dh, h, gamma, mean, rstd, ctx.kind, dx, dgamma, dbeta, ws)
+        dx = dx.reshape(ctx.shape)
+        return dx, dx if ctx.needs_input_grad[1] else None, dgamma, dbeta, None, None
+
+
+class AddNorm(torch.nn.Module):
+    """RMSNorm ("rms") or LayerNorm ("layer") of a residual stream with bf16 parameters:
+    forward(x, res) adds x into the stream and returns (norm(h), h) with h = x + res;
+    forward(x) returns (norm(x), x). features must be a multiple of 8, at most 16384."""
+
+    def __init__(self, features: int, kind: str = "rms", norm_eps: float = 1e-5, device=None):
+        super().__init__()
+        if kind not in _NORMS:
+            raise ValueError(f"kind must be one of {sorted(_NORMS)}")
+        self.features, self.kind, self.norm_eps = features, kind, float(norm_eps)
+        kw = dict(dtype=torch.bfloat16, device=device)
+        self.weight = torch.nn.Parameter(torch.ones(features, **kw))
+        self.bias = torch.nn.Parameter(torch.zeros(features, **kw)) if kind == "layer" else None
+
+    def forward(self, x: torch.Tensor, res: torch.Tensor | None = None):
+        load()
+        out = AddNormFunction.apply(x, res, self.weight, self.bias, _NORMS[self.kind], self.norm_eps)
+        return (out, x) if res is None else out
+
+    def extra_repr(self) -> str:
+        return f"features={self.features}, kind={self.kind}, norm_eps={self.norm_eps}"
+
+
+class Routing(NamedTuple):
+    """A router's answer for T tokens: ids and weights [T][k] (the weights differentiable), the grouped
+    GEMMs' offsets [E + 1], order [T * k] (the pair t * k + j of each sorted row, -1 behind the last)
+    and slot [T][k] (the sorted row of each pair, -1 for none)."""
+
+    ids: torch.Tensor
+    weights: torch.Tensor
+    offsets: torch.Tensor
+    order: torch.Tensor
+    slot: torch.Tensor
+
+
+class RouteFunction(torch.autograd.Function):
+    """fp8_moe_route on logits [T][E]; the gradient of the weights through fp8_moe_route_bwd."""
+
+    @staticmethod
+    def forward(ctx, logits, k: int, gate: int):
+        if logits.device.type != "cuda":
+            raise RuntimeError(f"route: logits must be on a ROCm GPU (got {logits.device})")
+        if logits.dim() != 2:
+            raise ValueError(f"route: logits must be [tokens][experts] (got {tuple(logits.shape)})")
+        l = logits.contiguous()
+        T, E = l.shape
+        i32 = dict(dtype=torch.int32, device=l.device)
+        ids, weights = torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=l.device)
+        offsets, order, slot = torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty((T, k), **i32)
+        ws = torch.empty(fp8_moe_route_ws_bytes(T, E, k), dtype=torch.uint8, device=l.device)
+        fp8_moe_route(l, gate, ids, weights, offsets, order, slot, ws)
+        ctx.save_for_backward(l, ids, weights)
+        ctx.gate = gate
+        ctx.mark_non_differentiable(ids, offsets, order, slot)
+        return ids, weights, offsets, order, slot
+
+    @staticmethod
+    def backward(ctx, _ids, dweights, _offsets, _order, _slot):
+        l, ids, weights = ctx.saved_tensors
+        dlogits = torch.empty_like(l)
+        fp8_moe_route_bwd(l, ctx.gate, ids, weights, dweights.float().contiguous(), dlogits)
+        return dlogits, None, None
+
+
+def route(logits: torch.Tensor, k: int, gate: str = "softmax") -> Routing:
+    """The k experts of each token with the largest logits ([T][E], bf16 or fp32), their gate weights
+    ("softmax" over all experts, "softmax_topk" over the chosen, "sigmoid") and the rows sorted by
+    expert, as fp8_moe_route defines them."""
+    if gate not in _GATES:
+        raise ValueError(f"gate must be one of {sorted(_GATES)}")
+    load()
+    return Routing(*RouteFunction.apply(logits, int(k), _GATES[gate]))
