@@ -329,6 +329,21 @@ def test_few(f, T, E, k, D, F, packed):
     check_few(f, Layer(E, D, F, 100 + D, packed), *_tokens(T, E, k, D, T))
 
 
+# many units of F an output tile: the down product's tiles are shared by workgroups and
+# their sums joined; tiles that begin and end inside a workgroup's share, a tile of half
+# the rows, every number of loads for an expert's tokens
+@pytest.mark.parametrize("packed", [False, True], ids=["rows", "packed"])
+@pytest.mark.parametrize("T,E,k,D,F", [(1, 8, 8, 64, 8192), (4, 8, 8, 64, 8256), (7, 40, 8, 576, 1088),
+                                       (33, 40, 8, 192, 1024), (64, 6, 6, 128, 5632), (24, 3, 2, 448, 12800)])
+def test_few_with_tiles_shared_by_workgroups(f, T, E, k, D, F, packed):
+    check_few(f, Layer(E, D, F, 400 + D, packed), *_tokens(T, E, k, D, T))
+
+
+@pytest.mark.parametrize("D,F", [(80, 8192), (1040, 5136), (16, 12816)])
+def test_few_with_shared_tiles_row_major_odd_sizes(f, D, F):
+    check_few(f, Layer(9, D, F, 450 + D, False), *_tokens(5, 9, 8, D, 6))
+
+
 @pytest.mark.parametrize("D,F", [(16, 16), (48, 16), (16, 176), (1040, 720), (208, 144)])
 def test_few_row_major_odd_sizes(f, D, F):
     check_few(f, Layer(5, D, F, 200 + D, False), *_tokens(9, 5, 3, D, 4))
