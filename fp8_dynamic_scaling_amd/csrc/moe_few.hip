@@ -271,23 +271,18 @@ __device__ __forceinline__ int few_count(uint32_t w) {
   return upto;
 }
 
-// The s-th named expert in order, s below their number (the same in every lane).
-__device__ __forceinline__ int few_expert(const uint32_t* bits, int s) {
+// The s-th named expert in order, s below their number (the same in every lane);
+// w and upto: the bits and their counts in lanes 0 to 31.
+__device__ __forceinline__ int few_expert(uint32_t w, int upto, int s) {
   const int lane = threadIdx.x & 63;
-  const uint32_t w = lane < 32 ? bits[lane] : 0;
-  const int upto = few_count(w);
   const int before = upto - __popc(w);
   const uint64_t hit = __ballot(lane < 32 && s >= before && s < upto);
-  const int word = __ffsll((unsigned long long)hit) - 1;
-  uint32_t v = __shfl(w, word, 64);
-  for (int r = s - __shfl(before, word, 64); r > 0; --r) v &= v - 1;
-  return __builtin_amdgcn_readfirstlane(32 * word + __ffs(v) - 1);
+  const int word = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+  uint32_t v = __builtin_amdgcn_readlane(w, word);
+  for (int r = s - __builtin_amdgcn_readlane(before, word); r > 0; --r) v &= v - 1;
+  return 32 * word + __ffs(v) - 1;
 }
 
-// Tiles [0, nt) of 16 gate and 16 up rows of one expert from row f0 on. The
-// units of a wave follow each other across the tiles' borders: the next one is
-// loaded as soon as one has been multiplied, and is in flight while the waves'
-// sums are added.
 // Calls go with the loads of four tokens for m tokens, at most 16 NTM.
 template <int NTM, class F>
 __device__ __forceinline__ void by_tokens(int m, F&& go) {
@@ -429,21 +424,24 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeFewArgs p) {
   __shared__ UpShared sh;
   const int lane = threadIdx.x & 63;
   const int n = (int)p.T * p.k;
+  // the first pairs' weights, under way while the ids are looked at
+  const float weight0 = threadIdx.x < 64 && lane < n ? p.weights[lane] : 0.0f;
   few_ids(p.ids, n, p.E, sh.sid, sh.bits);
-  const int nact = __builtin_amdgcn_readlane(few_count(lane < 32 ? sh.bits[lane] : 0), 31);
+  const uint32_t named = lane < 32 ? sh.bits[lane] : 0;
+  const int upto = few_count(named), nact = __builtin_amdgcn_readlane(upto, 31);
   const FewMeta meta = few_meta(p.act, p.T, p.k, p.F);
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0) meta.head[0] = nact;
     for (int i = threadIdx.x; i < kDownBlocks; i += 64 * kUpWaves) meta.done[i] = 0;
   }
-  const int per = (int)(p.F / 16);
-  const int64_t all = (int64_t)nact * per;
-  int64_t tile = all * blockIdx.x / gridDim.x;
-  const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
+  // at most 2^10 experts of 2^16 tiles
+  const uint32_t per = (uint32_t)(p.F / 16), all = nact * per, each = all / gridDim.x, rest = all % gridDim.x;
+  uint32_t tile = each * blockIdx.x + (blockIdx.x < rest ? blockIdx.x : rest);
+  const uint32_t end = tile + each + (blockIdx.x < rest);
   while (tile < end) {
     const int a = (int)(tile / per), first = (int)(tile % per);
     const int nt = (int)(end - tile < per - first ? end - tile : per - first);
-    const int e = few_expert(sh.bits, a);
+    const int e = few_expert(named, upto, a);
     // the expert's pairs in order, the first of each token's only, with the
     // weights of all the token's slots that name e, and the number of pairs of
     // the experts before it
@@ -458,8 +456,9 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeFewArgs p) {
         const uint64_t b = __ballot(head && id == e);
         if (head && id == e) {
           const int at = m + __popcll(b & ((1ull << lane) - 1));
-          float gate = 0.0f;
-          for (int j = i; j < i - i % p.k + p.k; ++j) gate += sh.sid[j] == e ? p.weights[j] : 0.0f;
+          float gate = i0 == 0 ? weight0 : p.weights[i];
+          for (int j = i + 1; j < i - i % p.k + p.k; ++j)
+            if (sh.sid[j] == e) gate += p.weights[j];
           sh.list[at] = i;
           sh.gate[at] = gate;
         }
@@ -655,9 +654,15 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeFewArgs p) {
       reinterpret_cast<uint4*>(p.out)[i] = make_uint4(0, 0, 0, 0);
     return;
   }
-  int64_t share = (all + gridDim.x - 1) / gridDim.x;
-  if (share < kDownWaves * 4) share = kDownWaves * 4;
-  if (share < per && per <= kDownWaves * 32) share = per;
+  int64_t share = (all + kDownBlocks - 1) / kDownBlocks;
+  if (share < per) {
+    // a joined tile costs some 2 us, so none with less than 32 units a wave is split,
+    // and no part has less than 4
+    if (per <= kDownWaves * 32)
+      share = per;
+    else if (share < kDownWaves * 4)
+      share = kDownWaves * 4;
+  }
   int64_t i = share * blockIdx.x;
   const int64_t end = i + share < all ? i + share : all;
   while (i < end) {
