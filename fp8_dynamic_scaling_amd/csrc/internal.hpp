@@ -124,7 +124,7 @@ struct MoeFewArgs {
   int64_t D, F;           // % 16 == 0 (packed: % 64 == 0), < 2^20: 32-bit byte offsets in x and act
   bool packed;
   uint16_t* out;          // [T][D]
-  uint16_t* act;          // workspace, moe_few_ws_bytes(): [T * k][F] bf16 and the experts' tokens
+  uint16_t* act;          // workspace, moe_few_ws_bytes(): the activations and the experts' tokens
   hipStream_t stream;
 };
 hipError_t launch_moe_few(const MoeFewArgs& a);  // F > 0

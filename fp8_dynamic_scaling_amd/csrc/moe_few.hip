@@ -9,7 +9,7 @@
 // straight from HBM to registers, 16 bytes a lane, are decoded to bf16 (exact)
 // and multiplied by 16 tokens at a time with the BF16 matrix-core instruction,
 // which sums at fp32 precision; x and a are bf16 and come from the caches.
-//  - k_moe_up: two workgroups a CU share the named experts' tiles of 16 gate and
+//  - k_moe_up: four workgroups a CU share the named experts' tiles of 16 gate and
 //    16 up rows evenly; a workgroup's waves share D among them. The waves'
 //    partial sums meet in LDS, in a fixed order.
 //  - k_moe_down: the workgroups share the tiles of rows of D, each for all
@@ -30,9 +30,18 @@
 // k_moe_down reads it, and tokens are loaded by fours: one load of a unit
 // for up to 4 tokens of an expert, two up to 8.
 //
-// The rounding of a to bf16 (with its gate weight, half a step: 2^-8 relative)
-// is that of the activations the grouped GEMMs take; everything else is fp32
-// up to the one rounding of the output.
+// a is kept as the sum of two bf16 values (some 16 bits of its fp32 value), each
+// multiplied by the codes: one bf16 value alone would add as large an error to the
+// output as the output's own rounding. The second one costs 2 to 3% of the call with
+// few tokens (63.2 -> 64.5 us with one, 333 -> 343 with 64 that take one of 16 experts
+// each) and up to 14% where an expert has many (293 -> 334 us, 64 tokens that take 8 of
+// 32). Everything else is fp32 up to the one rounding of the output.
+//
+// Measured, both launches, bytes of codes read: one token, 8 of 32 experts of D 7168 and
+// F 2048, packed: 352 MB in 64.5 us (5.5 TB/s); 16 tokens of the same, 31 experts named:
+// 1.38 GB in 228 us (6.0 TB/s); 64 tokens, 16 experts of D 5120, F 8192, row-major: 2.0 GB
+// in 343 us (5.9 TB/s), packed 340. A kernel that only reads such an amount reaches 5.7
+// to 6.3 TB/s with these loads.
 //
 // A token may name an expert twice: its first slot carries the sum of the
 // weights. Ids outside [0, E) name none.
@@ -43,6 +52,11 @@
 namespace fp8dyn {
 
 namespace {
+// One token (8 of 32 experts, D 7168, F 2048), 16 tokens of the same and 64 tokens (1 of
+// 16 experts, D 5120, F 8192): with 512 workgroups k_moe_up takes 58, 223 and 311 us,
+// with 1024 39, 147 and 221, with 2048, which take turns on the CUs, 39, 186 and 232.
+// k_moe_down with one tile of 16 rows a unit takes 36, 115 and 158 us, with two, which
+// share a load of the tokens, 23, 78 and 115.
 constexpr int kUpWaves = 2;
 constexpr int kUpBlocks = 1024;  // four a CU
 constexpr int kDownWaves = 8;
@@ -52,9 +66,11 @@ constexpr int kDownRows = 16 * kDownTiles;
 constexpr int kFewT = 64;
 constexpr int kFewK = 32;
 
-// What k_moe_up leaves in the workspace for k_moe_down: a, an expert's part at
-// 4 start F (room for m tokens, rounded up to a multiple mp of four), in it value
-// f of its i-th token at ((f / 8) mp + i) 8 + f % 8; the number of named experts; each one's id, in order, where its pairs begin,
+// What k_moe_up leaves in the workspace for k_moe_down: a, in units of 128 values
+// of F, the last one with room for as many; an expert's units are at pair 4 start
+// (room for m tokens, rounded up to a multiple mp of four), in a unit the first
+// parts [16 groups of 8 values][mp tokens][8], then the second parts alike; the
+// number of named experts; each one's id, in order, where its pairs begin,
 // and the tokens of the pairs. k_moe_down joins split sums by `done` (counters
 // that k_moe_up clears) and `part` ([workgroup][first or last tile][T][rows]).
 struct FewMeta {
@@ -65,9 +81,10 @@ struct FewMeta {
   uint16_t* start;   // [T * k + 1]
   uint16_t* token;   // [T * k]
 };
+__host__ __device__ inline int64_t act_pair(int64_t F) { return (F + 127) / 128 * 256; }  // bf16 values a pair
 __host__ __device__ inline FewMeta few_meta(uint16_t* act, int64_t T, int k, int64_t F) {
   FewMeta m;
-  m.part = reinterpret_cast<float*>(act + 4 * T * k * F);
+  m.part = reinterpret_cast<float*>(act + 4 * T * k * act_pair(F));
   m.done = reinterpret_cast<uint32_t*>(m.part + kDownBlocks * 2 * T * kDownRows);
   m.head = reinterpret_cast<int32_t*>(m.done + kDownBlocks);
   m.expert = reinterpret_cast<uint16_t*>(m.head + 1);
@@ -78,7 +95,7 @@ __host__ __device__ inline FewMeta few_meta(uint16_t* act, int64_t T, int k, int
 }  // namespace
 
 size_t moe_few_ws_bytes(int64_t T, int k, int64_t F) {
-  return (size_t)(T * k) * (8 * F + 6) + 8 + kDownBlocks * (size_t)(4 + 8 * T * kDownRows);
+  return (size_t)(T * k) * (8 * act_pair(F) + 6) + 8 + kDownBlocks * (size_t)(4 + 8 * T * kDownRows);
 }
 
 // Eight e4m3 codes -> eight bf16 (every e4m3 value is a bf16 value).
@@ -198,8 +215,8 @@ __device__ __forceinline__ void turn_rows(const v8bf (&x)[G], Tokens (&t)[NT], u
 }
 
 // Zeros for the values of the last unit that lie behind K.
-template <int R, int NT>
-__device__ __forceinline__ void mask_unit(uint4 (&w)[R][2], Tokens (&x)[NT], int u, int K) {
+template <int R, int NT, int S>
+__device__ __forceinline__ void mask_unit(uint4 (&w)[R][2], Tokens (&x)[S][NT], int u, int K) {
   if (128 * (u + 1) <= K) return;
   const int kg = (threadIdx.x & 63) >> 4;
 #pragma unroll
@@ -208,13 +225,16 @@ __device__ __forceinline__ void mask_unit(uint4 (&w)[R][2], Tokens (&x)[NT], int
 #pragma unroll
     for (int r = 0; r < R; ++r) w[r][h] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) x[n].v[2 * h] = x[n].v[2 * h + 1] = (v8bf){};
+    for (int z = 0; z < S; ++z)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) x[z][n].v[2 * h] = x[z][n].v[2 * h + 1] = (v8bf){};
   }
 }
 
-// The products of R tiles of codes with NT tiles of tokens.
-template <int R, int NT>
-__device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const Tokens (&x)[NT], v4f (&acc)[R][NT]) {
+// The products of R tiles of codes with NT tiles of tokens, whose values are the sums of S
+// parts.
+template <int R, int NT, int S>
+__device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const Tokens (&x)[S][NT], v4f (&acc)[R][NT]) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     v8bf a[4];
@@ -228,10 +248,13 @@ __device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const Tokens (&
     asm volatile("s_nop 1" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int z = 0; z < S; ++z) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], x[n].v[q], acc[r][n], 0, 0, 0);
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q], x[z][n].v[q], acc[r][n], 0, 0, 0);
+      }
     }
     // the operands stay live past the matrix instructions, which nothing may
     // move behind this point: no destination shares a source's registers
@@ -240,7 +263,9 @@ __device__ __forceinline__ void multiply(const uint4 (&w)[R][2], const Tokens (&
     for (int q = 0; q < 4; ++q) {
       keep_live(a[q]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) keep_live(x[n].v[q]);
+      for (int z = 0; z < S; ++z)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) keep_live(x[z][n].v[q]);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -344,8 +369,8 @@ __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, 
   auto finish = [&]() {
     // The waves' partial sums (and the rows' scales), in one of two buffers: a
     // wave writes it again two tiles on, behind a barrier that the reader
-    // reaches after reading. Four token tiles have one buffer, which lets two
-    // workgroups share a CU's LDS, and a barrier before it is written again.
+    // reaches after reading. Four token tiles have one buffer, which lets
+    // four workgroups share a CU's LDS, and a barrier before it is written again.
     if (NT == 4 && tile > 0) __syncthreads();
     float4* r = red + (NT < 4 ? tile & 1 : 0) * (NT * 2 * kUpWaves * 64);
 #pragma unroll
@@ -387,10 +412,21 @@ __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, 
         const float gv = g[i] * sh.scale[tile & 1][4 * kg + i], uv = uu[i] * sh.scale[tile & 1][16 + 4 * kg + i];
         v[i] = gate * (gv / (1.0f + expf(-gv)) * uv);
       }
-      const v2bf lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
-      const int64_t f = f0 + 16 * tile + 4 * kg;
-      *reinterpret_cast<uint2*>(p.act + 4 * act0 * p.F + ((f >> 3) * mp + item) * 8 + (f & 7)) =
-          make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+      // v as a bf16 value and the bf16 value of what is left, nothing beside an infinity
+      v2bf hi[2], lo[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __bf16 h = (__bf16)v[i];
+        hi[i >> 1][i & 1] = h;
+        lo[i >> 1][i & 1] = (__bf16)(isinf((float)h) ? 0.0f : v[i] - (float)h);
+      }
+      const int f = (int)f0 + 16 * tile + 4 * kg;
+      uint16_t* d = p.act + 4 * act0 * act_pair(p.F) + (int64_t)(f >> 7) * 256 * mp +
+                    ((f >> 3 & 15) * mp + item) * 8 + (f & 7);
+      *reinterpret_cast<uint2*>(d) =
+          make_uint2(__builtin_bit_cast(uint32_t, hi[0]), __builtin_bit_cast(uint32_t, hi[1]));
+      *reinterpret_cast<uint2*>(d + 128 * mp) =
+          make_uint2(__builtin_bit_cast(uint32_t, lo[0]), __builtin_bit_cast(uint32_t, lo[1]));
     }
     ++tile;
   };
@@ -403,10 +439,10 @@ __device__ __forceinline__ void moe_up_tiles(const MoeFewArgs& p, int e, int m, 
     for (int u = 0; u < nu; ++u) {
       turn_codes<PACKED>(w[0], mine);
       turn_codes<PACKED>(w[1], mine);
-      Tokens t[NT];
-      turn_rows<G, NT>(x, t, mine);
-      mask_unit<2, NT>(w, t, u0 + u, D);
-      multiply<2, NT>(w, t, acc);
+      Tokens t[1][NT];
+      turn_rows<G, NT>(x, t[0], mine);
+      mask_unit<2, NT, 1>(w, t, u0 + u, D);
+      multiply<2, NT, 1>(w, t, acc);
       const bool here = u + 1 < nu;
       load(here || tile + 1 == nt ? tile : tile + 1, here ? u + 1 : 0);  // behind the last unit one that nobody uses
     }
@@ -501,7 +537,7 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
   constexpr int NT = (G + 3) / 4, R = kDownTiles;
   const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4, F = (int)p.F;
   uint4 w[R][2];
-  v8bf x[G];
+  v8bf x[2][G];
   const Codes<PACKED> codes(F);
   // the first row of tile r; behind D the first tile again, whose sums are not written
   auto row_of = [&](int r) { return d0 + 16 * r < p.D ? d0 + 16 * r : d0; };
@@ -509,7 +545,7 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
   int a = i / units, u = i % units, mp = 0;
   const uint8_t* wp[R];
   const uint8_t* ap = nullptr;
-  // Up to 8 tokens: a unit's 256 mp bytes in a row, mp / 4 loads (with fewer than
+  // Up to 8 tokens: a part's 256 mp bytes in a row, mp / 4 loads (with fewer than
   // G, the first again), turned in LDS. More: the lanes' own operands.
   uint32_t aoff[G];
   auto point = [&]() {
@@ -519,7 +555,7 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
     mp = (m + 3) & ~3;
 #pragma unroll
     for (int r = 0; r < R; ++r) wp[r] = p.w2 + (e * p.D + row_of(r)) * p.F;
-    ap = reinterpret_cast<const uint8_t*>(p.act + 4 * (int64_t)b * p.F);
+    ap = reinterpret_cast<const uint8_t*>(p.act + 4 * (int64_t)b * act_pair(p.F));
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       if constexpr (G <= 2) {
@@ -534,21 +570,14 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
   auto load = [&]() {
 #pragma unroll
     for (int r = 0; r < R; ++r) codes.load(w[r], wp[r], u, F);
-    const uint8_t* at = ap + (int64_t)u * 256 * mp;
-    const int rest = F - 128 * u;  // below 128: the part behind F is not there to be read
+    const uint8_t* at = ap + (int64_t)u * 512 * mp;
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      uint32_t o = aoff[j];
-      if (rest < 128) {
-        if constexpr (G <= 2)
-          o = o < (uint32_t)(2 * rest * mp) ? o : 0;
-        else
-          o = 64 * (j % 4 >> 1) + 16 * kg < rest ? o : 0;
-      }
-      x[j] = *reinterpret_cast<const v8bf*>(at + o);
+    for (int z = 0; z < 2; ++z) {
+#pragma unroll
+      for (int j = 0; j < G; ++j) x[z][j] = *reinterpret_cast<const v8bf*>(at + 256 * z * mp + aoff[j]);
     }
   };
-  auto operands = [&](Tokens (&t)[NT]) {
+  auto operands = [&](const v8bf (&x)[G], Tokens (&t)[NT]) {
     if constexpr (G <= 2) {
 #pragma unroll
       for (int j = 0; j < G; ++j) *reinterpret_cast<v8bf*>(turn + 1024 * j + 16 * lane) = x[j];
@@ -573,10 +602,11 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
   for (; i < end; ++i) {
 #pragma unroll
     for (int r = 0; r < R; ++r) turn_codes<PACKED>(w[r], turn);
-    Tokens t[NT];
-    operands(t);
-    mask_unit<R, NT>(w, t, u, F);
-    multiply<R, NT>(w, t, acc);
+    Tokens t[2][NT];
+    operands(x[0], t[0]);
+    operands(x[1], t[1]);
+    mask_unit<R, NT, 2>(w, t, u, F);
+    multiply<R, NT, 2>(w, t, acc);
     const int of = a;
     if (i + 1 < end) {
       if (++u == units) {
@@ -656,8 +686,9 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeFewArgs p) {
   }
   int64_t share = (all + kDownBlocks - 1) / kDownBlocks;
   if (share < per) {
-    // a joined tile costs some 2 us, so none with less than 32 units a wave is split,
-    // and no part has less than 4
+    // a joined tile costs some 2 us, so none with less than 32 units a wave is split
+    // (128 units a tile: 22.9 us unsplit, 25.9 split; 1024 units: 155 us unsplit, 115
+    // split), and no part has less than 4
     if (per <= kDownWaves * 32)
       share = per;
     else if (share < kDownWaves * 4)

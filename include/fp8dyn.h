@@ -478,14 +478,15 @@ FP8DYN_API fp8_status fp8_moe_route_bwd(const void* logits, fp8_out logits_type,
  * writes them, or with packed nonzero as fp8_quant_row_kpacked does, the
  * operands of fp8_grouped_mm(_kpacked). Only the named experts' codes are read,
  * once. x is not quantized: the products are bf16 (codes decoded exactly) with
- * fp32 sums; a is rounded to bf16 once, out [T][D] to bf16 once. An id outside
+ * fp32 sums; a is kept to 16 bits, as two bf16 values; out [T][D] is rounded to
+ * bf16 once. An id outside
  * [0, E) names no expert; one that a token names twice counts with the sum of
  * its weights; a token that names none gets zeros. The order of all sums is
  * fixed. D % 16 == 0 and F % 16 == 0 (packed: % 64), 16-byte aligned x, w13, w2,
  * out, ws (else FP8_ERR_ALIGNMENT); k <= 32, E <= 1024, D, F < 2^20 (else
  * FP8_ERR_UNSUPPORTED); fmt the native e4m3. F = 0 writes zeros. ws:
- * fp8_moe_few_ws_bytes(T, k, F) bytes (2 * T * k * F and some), content on
- * entry of no matter; calls that may run at the same time need one each. */
+ * fp8_moe_few_ws_bytes(T, k, F) bytes (some 16 * T * k * F), content on entry
+ * of no matter; calls that may run at the same time need one each. */
 FP8DYN_API fp8_status fp8_moe_few(const uint16_t* x, const int32_t* ids, const float* weights, int64_t T, int32_t k,
                                   const uint8_t* w13, const float* w13_inv, const uint8_t* w2, const float* w2_inv,
                                   fp8_format fmt, int32_t E, int64_t D, int64_t F, int packed, uint16_t* out,

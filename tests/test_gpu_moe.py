@@ -280,7 +280,7 @@ def few_reference(layer, x, ids, w):
         # at most 1.1, a few roundings and expf (relative to its argument) for the rest
         dg, du = (D + 4) * U * sg, (D + 4) * U * su
         da = sh.abs() * (1.1 * dg * u.abs() + silu.abs() * du + dg * du) + (32 + 4 * g.abs()) * U * a.abs()
-        da = da + 2.0 ** -8 * (a.abs() + da)  # stored as bf16
+        da = da + 2.0 ** -16 * (a.abs() + da)  # stored as a bf16 value and that of what is left
         out[t] += a @ m2.t()
         err[t] += da @ m2.abs().t() + (F + 64) * U * ((a.abs() + da) @ m2.abs().t())
     return out, err + 2.0 ** -8 * (out.abs() + err)
@@ -379,6 +379,25 @@ def test_few_a_nan_stays_with_its_token(f, T):
     got = run_few(f, layer, x, ids, w)
     assert bool(got[1].isnan().all()) and bool(got[2, 11].isnan())
     keep = [t for t in range(T) if t not in (1, 2)]
+    assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_few_an_infinite_activation_is_the_formulas(f, T):
+    """Activations that overflow with codes of one sign behind them: an infinity, not a NaN."""
+    import torch
+    layer = Layer(4, 128, 128, 312, False)
+    x, ids, w = _tokens(T, 3, 1, 128, 313)  # expert 3 unused
+    clean = run_few(f, layer, x, ids, w)
+    layer.c13[3], layer.c2[3] = 0x38, 0x38  # ones
+    layer.i13[3], layer.i2[3] = 1.0, 1.0
+    layer.c2[3, 5] = 0xB8
+    ids[1], w[1], x[1] = 3, 0.5, 1e30  # 128e30 squared
+    got = run_few(f, layer, x, ids, w)
+    want = torch.full((128,), float("inf"), device="cuda:0")
+    want[5] = -want[5]
+    assert torch.equal(got[1].float(), want)
+    keep = [t for t in range(T) if t != 1]
     assert torch.equal(got[keep], clean[keep])
 
 
