@@ -33,6 +33,7 @@ import math
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (E4M3_NATIVE, GATE_SIGMOID, GATE_SOFTMAX, GATE_SOFTMAX_TOPK, NORM_LAYER, NORM_RMS, OUT_BF16,
                RECIPE_ROWWISE_BF16_WGRAD, RECIPE_TENSORWISE, fp8_add_norm_bwd, fp8_add_norm_bwd_ws_bytes,
@@ -158,24 +159,28 @@ class AddNormFunction(torch.autograd.Function):
         x2 = x.reshape(-1, cols).contiguous()
         rows = x2.shape[0]
         r2 = None if res is None else res.reshape(-1, cols).contiguous()
-        h = x2 if res is None else torch.empty_like(x2)
-        y = torch.empty_like(x2)
+        # the outputs have their own shape, not a view's: they may be changed in place
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        h = x2 if res is None else torch.empty_like(y)
         stats = dict(dtype=torch.float32, device=x.device)
         mean = torch.empty(rows, **stats) if kind == NORM_LAYER else None
         rstd = torch.empty(rows, **stats)
         g = gamma.contiguous()
         fp8_add_norm_quant_row(x2, r2, g, None if beta is None else beta.contiguous(), kind, norm_eps, E4M3_NATIVE,
-                               1e-12, None if res is None else h, y, None, None, mean=mean, rstd=rstd)
+                               1e-12, None if res is None else h.view(rows, cols), y.view(rows, cols), None, None,
+                               mean=mean, rstd=rstd)
         ctx.save_for_backward(h, g, mean, rstd)
         ctx.kind, ctx.shape = kind, x.shape
         ctx.set_materialize_grads(False)
-        y = y.reshape(x.shape)
-        return y if res is None else (y, h.reshape(x.shape))
+        return y if res is None else (y, h)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, gamma, mean, rstd = ctx.saved_tensors
-        rows, cols = h.shape
+        cols = h.shape[-1]
+        h = h.view(-1, cols)
+        rows = h.shape[0]
         flat = lambda g: None if g is None else g.to(torch.bfloat16).reshape(rows, cols).contiguous()  # noqa: E731
         dy, dh = flat(dy), flat(dh)
         if dy is None:  # only the stream behind h has a gradient
@@ -249,6 +254,7 @@ class RouteFunction(torch.autograd.Function):
         return ids, weights, offsets, order, slot
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _ids, dweights, _offsets, _order, _slot):
         l, ids, weights = ctx.saved_tensors
         dlogits = torch.empty_like(l)

@@ -78,6 +78,44 @@ def test_add_norm_with_one_output_used(f):
     assert torch.equal(both, gy)
 
 
+def test_add_norm_outputs_changed_in_place(f):
+    """y may be changed in place (its values are not kept); a changed stream, whose values are,
+    is refused by the backward pass."""
+    import torch
+    from fp8_dynamic_scaling_amd.nn import AddNorm
+    m = AddNorm(64, device="cuda:0")
+    x, res = (_randn(2, 3, 64, seed=s).requires_grad_(True) for s in (1, 2))
+    g = _randn(2, 3, 64, seed=3)
+    y, h = m(x, res)
+    want, = torch.autograd.grad(y, x, 2 * g)
+    y, h = m(x, res)
+    y.mul_(2)
+    got, = torch.autograd.grad(y, x, g)
+    assert torch.equal(got, want)
+    y, h = m(x, res)
+    h.add_(1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        torch.autograd.grad(y, x, g)
+
+
+def test_no_rows_and_no_second_derivatives(f):
+    import torch
+    from fp8_dynamic_scaling_amd.nn import AddNorm, route
+    m = AddNorm(64, device="cuda:0")
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda:0", requires_grad=True)
+    y, h = m(x, x)
+    (y.sum() + h.sum()).backward()
+    assert y.shape == h.shape == x.grad.shape == (0, 64) and not bool(m.weight.grad.any())
+    x = _randn(4, 64, seed=1).requires_grad_(True)
+    dx, = torch.autograd.grad(m(x)[0].float().pow(2).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiat"):
+        dx.sum().backward()
+    l = torch.randn(4, 8, device="cuda:0", requires_grad=True)
+    dl, = torch.autograd.grad(route(l, 2).weights.pow(2).sum(), l, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiat"):
+        dl.sum().backward()
+
+
 @pytest.mark.parametrize("gate", ["softmax", "softmax_topk", "sigmoid"])
 def test_route(f, gate):
     import torch
