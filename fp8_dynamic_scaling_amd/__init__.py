@@ -158,11 +158,14 @@ def _args(fn, *operands):
             if nbytes:
                 raise ValueError(f"{fn}: {name} is required")
             continue
-        if not t.is_cuda:
+        at = t.get_device()
+        if at == dev and (t.dtype is dtype or dtype is None) and t.is_contiguous() and (not nbytes or t.nbytes >= nbytes):
+            continue  # all in order; below, the first operand, or what is wrong
+        if at < 0 or not t.is_cuda:
             raise ValueError(f"{fn}: {name} must be on the GPU")
         if dev is None:
-            dev = t.get_device()
-        elif t.get_device() != dev:
+            dev = at
+        elif at != dev:
             raise ValueError(f"{fn}: {name} is on another GPU than the operands before it")
         if dtype is not None and t.dtype != dtype:
             raise ValueError(f"{fn}: {name} must be {dtype} (got {t.dtype})")
