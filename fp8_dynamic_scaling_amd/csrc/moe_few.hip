@@ -61,7 +61,7 @@ constexpr int kUpWaves = 2;
 constexpr int kUpBlocks = 1024;  // four a CU
 constexpr int kDownWaves = 8;
 constexpr int kDownBlocks = 256;  // one a CU
-constexpr int kDownTiles = 2;     // tiles of 16 rows a unit has
+constexpr int kDownTiles = 2;     // tiles of 16 rows a unit has at most
 constexpr int kDownRows = 16 * kDownTiles;
 constexpr int kFewT = 64;
 constexpr int kFewK = 32;
@@ -528,13 +528,13 @@ struct DownShared {
   int count;
 };
 
-// A wave's run [i, end) of the (expert, unit) pairs of kDownRows rows, the next one
+// A wave's run [i, end) of the (expert, unit) pairs of R tiles of 16 rows, the next one
 // loaded as soon as one has been multiplied. At an expert's last unit its sums,
 // times the rows' scales, are added to the wave's sums [token][row].
-template <int G, bool PACKED>
+template <int G, bool PACKED, int R>
 __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShared& sh, int64_t d0, int units, int i,
                                              int end, float* sum, uint8_t* turn) {
-  constexpr int NT = (G + 3) / 4, R = kDownTiles;
+  constexpr int NT = (G + 3) / 4;
   const int lane = threadIdx.x & 63, lr = lane & 15, kg = lane >> 4, F = (int)p.F;
   uint4 w[R][2];
   v8bf x[2][G];
@@ -635,7 +635,7 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
       for (int n = 0; n < NT; ++n) {
         // an expert's tokens differ, so no two lanes meet
         if (16 * n + lr < mc) {
-          float4* d = reinterpret_cast<float4*>(sum + sh.token[b + 16 * n + lr] * kDownRows + 16 * r + 4 * kg);
+          float4* d = reinterpret_cast<float4*>(sum + sh.token[b + 16 * n + lr] * (16 * R) + 16 * r + 4 * kg);
           float4 v = *d;
           v.x += acc[r][n][0] * c[0];
           v.y += acc[r][n][1] * c[1];
@@ -653,9 +653,9 @@ __device__ __forceinline__ void moe_down_run(const MoeFewArgs& p, const DownShar
 // workgroup has an end of a tile of rows, whole ones, and a beginning. The sums
 // of a tile that several share meet in memory, and the one that comes last adds
 // them, in the workgroups' order. Where a tile has few units it is not split.
-template <int NTM, bool PACKED>
+template <int NTM, bool PACKED, int R>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeFewArgs p) {
-  constexpr int kQuads = 16 * NTM * kDownRows / 4;  // a wave's sums, by fours
+  constexpr int kRows = 16 * R, kQuads = 16 * NTM * kRows / 4;  // a tile's rows; a wave's sums, by fours
   __shared__ float4 sums[kDownWaves * kQuads];  // [wave][token][row]
   __shared__ __align__(16) uint8_t turn[kDownWaves * 2048];
   __shared__ DownShared sh;
@@ -677,7 +677,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeFewArgs p) {
   for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o, 64));
   most = __builtin_amdgcn_readfirstlane(most);
   const int units = (int)((p.F + 127) / 128);
-  const int64_t tiles = (p.D + kDownRows - 1) / kDownRows, per = (int64_t)nact * units, all = tiles * per;
+  const int64_t tiles = (p.D + kRows - 1) / kRows, per = (int64_t)nact * units, all = tiles * per;
   if (nact == 0) {  // no token has an expert: zeros
     for (int64_t i = (int64_t)blockIdx.x * 64 * kDownWaves + threadIdx.x; i < p.T * p.D / 8;
          i += (int64_t)gridDim.x * 64 * kDownWaves)
@@ -697,7 +697,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeFewArgs p) {
   int64_t i = share * blockIdx.x;
   const int64_t end = i + share < all ? i + share : all;
   while (i < end) {
-    const int64_t tile = i / per, d0 = kDownRows * tile;
+    const int64_t tile = i / per, d0 = kRows * tile;
     const int from = (int)(i - tile * per);
     const int to = (int)(end - tile * per < per ? end - tile * per : per);
     float* sum = reinterpret_cast<float*>(&sums[wave * kQuads]);
@@ -707,13 +707,13 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeFewArgs p) {
     const int i1 = from + (int)((int64_t)(to - from) * (wave + 1) / kDownWaves);
     uint8_t* mine = turn + wave * 2048;
     if (i0 < i1) {
-      auto run = [&](auto loads) { moe_down_run<loads.value, PACKED>(p, sh, d0, units, i0, i1, sum, mine); };
+      auto run = [&](auto loads) { moe_down_run<loads.value, PACKED, R>(p, sh, d0, units, i0, i1, sum, mine); };
       by_tokens<NTM>(most, run);
     }
     __syncthreads();
     // each thread adds up the waves' sums of up to two fours of rows of a token
     constexpr int kMine = (kQuads + 64 * kDownWaves - 1) / (64 * kDownWaves);
-    const int quads = (int)p.T * (kDownRows / 4);
+    const int quads = (int)p.T * (kRows / 4);
     float r[kMine][4];
 #pragma unroll
     for (int y = 0; y < kMine; ++y) {
@@ -772,8 +772,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeFewArgs p) {
     if (write) {
 #pragma unroll
       for (int y = 0; y < kMine; ++y) {
-        const int z = threadIdx.x + y * 64 * kDownWaves, t = z / (kDownRows / 4);
-        const int64_t d = d0 + 4 * (z % (kDownRows / 4));
+        const int z = threadIdx.x + y * 64 * kDownWaves, t = z / (kRows / 4);
+        const int64_t d = d0 + 4 * (z % (kRows / 4));
         if (z >= quads || d >= p.D) continue;
         const v2bf lo = {(__bf16)r[y][0], (__bf16)r[y][1]}, hi = {(__bf16)r[y][2], (__bf16)r[y][3]};
         *reinterpret_cast<uint2*>(p.out + (int64_t)t * p.D + d) =
@@ -787,7 +787,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_down(MoeFewArgs p) {
 
 template <bool PACKED>
 static hipError_t launch_few_t(const MoeFewArgs& a) {
-  const int64_t pairs = a.T * a.k, most = (pairs < a.E ? pairs : a.E) * (a.F / 16);
+  const int64_t pairs = a.T * a.k, experts = pairs < a.E ? pairs : a.E, most = experts * (a.F / 16);
   const dim3 gu((unsigned)(most < kUpBlocks ? most : kUpBlocks)), gd(kDownBlocks);
   const dim3 bu(64 * kUpWaves), bd(64 * kDownWaves);
   auto go = [&](auto up, auto down) {
@@ -797,9 +797,15 @@ static hipError_t launch_few_t(const MoeFewArgs& a) {
     hipLaunchKernelGGL(down, gd, bd, 0, a.stream, a);
     return hipGetLastError();
   };
-  if (a.T <= 16) return go(k_moe_up<1, PACKED>, k_moe_down<1, PACKED>);
-  if (a.T <= 32) return go(k_moe_up<2, PACKED>, k_moe_down<2, PACKED>);
-  return go(k_moe_up<4, PACKED>, k_moe_down<4, PACKED>);
+  // One tile of 16 rows a unit where two would leave half of the CUs without work
+  // and a tile is too short to be split (k_moe_down, with one and with two: 5 tokens,
+  // 8 experts, D 1040, F 720: 7.2 and 8.9 us; 32 tokens, 16 experts, D 4096, F 2048: 37.9
+  // and 42.7 us).
+  const bool narrow = a.D <= 16 * kDownBlocks && experts * ((a.F + 127) / 128) <= kDownWaves * 32;
+  auto by_rows = [&](auto up, auto one, auto two) { return narrow ? go(up, one) : go(up, two); };
+  if (a.T <= 16) return by_rows(k_moe_up<1, PACKED>, k_moe_down<1, PACKED, 1>, k_moe_down<1, PACKED, kDownTiles>);
+  if (a.T <= 32) return by_rows(k_moe_up<2, PACKED>, k_moe_down<2, PACKED, 1>, k_moe_down<2, PACKED, kDownTiles>);
+  return by_rows(k_moe_up<4, PACKED>, k_moe_down<4, PACKED, 1>, k_moe_down<4, PACKED, kDownTiles>);
 }
 
 hipError_t launch_moe_few(const MoeFewArgs& a) {

@@ -349,6 +349,13 @@ def test_few_row_major_odd_sizes(f, D, F):
     check_few(f, Layer(5, D, F, 200 + D, False), *_tokens(9, 5, 3, D, 4))
 
 
+@pytest.mark.parametrize("T,D,F,packed", [(1, 4096, 128, True), (1, 4112, 128, False), (20, 4112, 272, False),
+                                          (20, 4160, 320, True), (50, 4160, 64, True), (50, 4096, 144, False)])
+def test_few_either_side_of_narrow_tiles(f, T, D, F, packed):
+    """Whole tiles of 16 rows up to 4096 rows of few units, of 32 above."""
+    check_few(f, Layer(6, D, F, 460 + T, packed), *_tokens(T, 6, 2, D, T))
+
+
 def test_few_tokens_without_experts_and_repeated_ids(f):
     import torch
     layer = Layer(6, 256, 192, 300, True)
