@@ -4,7 +4,8 @@
 //
 // Choosing compares and never computes, so it is exact: a logit's 32-bit
 // pattern is mapped to an unsigned integer of the same order, and k times the
-// largest is found, then the lowest expert that has it, which is taken out.
+// largest is found, then the lowest expert that has it, which is taken out (bf16
+// logits leave room for the expert in the integer, so that one search finds both).
 // -inf and NaN have key 0, below every other, and are never chosen; a token with
 // fewer than k other logits gets id -1 and weight 0 in the slots left.
 //
@@ -20,9 +21,9 @@
 // works on 64 / G tokens at once: a maximum is V - 1 comparisons and log2 G
 // exchanges between lanes, up to 16 lanes within the vector unit. What remains is
 // latency: the exchanges, k rounds of them, and two to three trips to memory.
-// Measured, choosing + placing: 64 tokens x 32 experts, k 8: 5.0 us; 16384 x 32, k 8:
-// 6.3 + 4.5 us (2 MB of logits); 4096 x 256: 8.2 + 8.5; 65536 x 128, k 8, bf16: 30 + 9 us,
-// bound by the vector instructions of the choices.
+// Measured, choosing + placing: 64 tokens x 32 experts, k 8: 4.3 us; 16384 x 32, k 8:
+// 5.9 + 6.0 us (2 MB of logits); 4096 x 256: 7.3 + 8.5; 65536 x 128, k 8: 24 + 9 us with bf16
+// logits, 26 + 9 with fp32, bound by the vector instructions of the choices.
 #include <type_traits>
 
 #include "common.hpp"
@@ -38,7 +39,7 @@ constexpr int kMaxRouteBlocks = 256;
 
 // Tokens a block: all of them up to kChunk; else so that at most kMaxRouteBlocks
 // (one a CU) count, for the second launch reads all their counts in every block
-// (4096 x 256, 64 tokens a block: 13 + 5 us, 16 tokens: 8.2 + 8.5, 8 tokens: 13 + 16).
+// (4096 x 256, 64 tokens a block: 12 + 5 us, 16 tokens: 7.3 + 8.5, 8 tokens: 12 + 16).
 int64_t route_block_tokens(int64_t T) {
   if (T <= kChunk) return kChunk;
   const int64_t per = (T + kMaxRouteBlocks - 1) / kMaxRouteBlocks;
@@ -47,7 +48,7 @@ int64_t route_block_tokens(int64_t T) {
 }  // namespace
 
 // Threads of a block: what counts is the number of rounds over a chunk (65536 x 128
-// experts with 512: 38 us, with 1024: 30), and in the second launch over the counts
+// experts with 512: 29 us, with 1024: 24), and in the second launch over the counts
 // (256 threads: 12 us, 1024: 8.5); small blocks take the same time with either.
 constexpr int kRouteThreads = 1024;
 constexpr int kPlaceThreads = 1024;
@@ -140,8 +141,16 @@ __device__ __forceinline__ uint32_t logit_key(float f) {
   const uint32_t u = __float_as_uint(f + 0.0f);  // -0 as +0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+// A bf16 logit's order is in the upper half of its key. The lower half holds how far
+// the expert is from the last one, so that one maximum gives the largest logit and
+// the lowest expert that has it, and no two experts' keys are equal.
+__device__ __forceinline__ uint32_t expert_key(uint32_t key, int e) {
+  return key ? (key & 0xffff0000u) | (0xffffu - (uint32_t)e) : 0;
+}
+template <bool F32>
 __device__ __forceinline__ float key_logit(uint32_t o) {
-  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+  const uint32_t u = o & 0x80000000u ? o & 0x7fffffffu : ~o;
+  return o ? __uint_as_float(F32 ? u : u & 0xffff0000u) : -INFINITY;
 }
 
 // Exclusive sums of n words in LDS, by the first wavefront; returns the total.
@@ -174,7 +183,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(const void* __restr
   uint64_t* mark = lds64;                                      // [E] the tokens of the chunk that chose e
   uint32_t* cnt = reinterpret_cast<uint32_t*>(lds64 + E);      // [E] the pairs of the chunks before
   int32_t* cid = reinterpret_cast<int32_t*>(cnt + E);          // [kChunk * k]
-  float* cval = reinterpret_cast<float*>(cid + kChunk * k);    // [kChunk * k]
+  uint32_t* ckey = reinterpret_cast<uint32_t*>(cid + kChunk * k);  // [kChunk * k]
   __shared__ uint32_t total;
   constexpr int PER = 64 / G;  // tokens a wavefront works on at once
   constexpr int NT = kRouteThreads;
@@ -190,6 +199,13 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(const void* __restr
     }
     __syncthreads();
   }
+  // the logits of the wavefront's next tokens, on their way while the present ones are chosen for
+  float ahead[V];
+  auto load = [&](int64_t chunk, int base) {
+    const int64_t t = chunk + base + lane / G;
+    load_logits<G, V, F32>(logits, t, E, g, base + lane / G < kChunk && t < last, vec != 0, ahead);
+  };
+  load(first, wave * PER);
   for (int64_t chunk = first; chunk < last; chunk += kChunk) {
     const int here = (int)(last - chunk < kChunk ? last - chunk : kChunk);  // tokens
     for (int base = wave * PER; base < here; base += NT / 64 * PER) {
@@ -197,51 +213,67 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(const void* __restr
       const int64_t t = chunk + ct;
       const bool live = ct < here;
       float l[V];
-      load_logits<G, V, F32>(logits, t, E, g, live, vec != 0, l);
+#pragma unroll
+      for (int v = 0; v < V; ++v) l[v] = ahead[v];
+      if (base + NT / 64 * PER < kChunk)
+        load(chunk, base + NT / 64 * PER);
+      else
+        load(chunk + kChunk, wave * PER);
       uint32_t key[V];
       float bad = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         key[v] = logit_key(l[v]);
+        if constexpr (!F32) key[v] = expert_key(key[v], expert_of<G>(g, v));
         if (l[v] != l[v]) bad = l[v];
       }
       bad = group_sum<G>(bad);  // 0, or NaN where a logit of the token is
-      float top = 0.0f, zk = 0.0f;
+      float top = 0.0f;
       for (int j = 0; j < k; ++j) {
         uint32_t m = key[0];
 #pragma unroll
         for (int v = 1; v < V; ++v) m = key[v] > m ? key[v] : m;
         m = group_max<G>(m);
-        uint32_t best = ~0u;  // the lowest expert with that key (m = 0: none, not used)
+        uint32_t best;  // m = 0: none, not used
+        if constexpr (F32) {
+          best = ~0u;  // the lowest expert with that key
 #pragma unroll
-        for (int v = V - 1; v >= 0; --v) best = key[v] == m ? (uint32_t)expert_of<G>(g, v) : best;
-        best = group_min<G>(best);
+          for (int v = V - 1; v >= 0; --v) best = key[v] == m ? (uint32_t)expert_of<G>(g, v) : best;
+          best = group_min<G>(best);
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = best == (uint32_t)expert_of<G>(g, v) ? 0 : key[v];
-        const float val = m ? key_logit(m) : -INFINITY;
-        if (j == 0) top = val;
-        zk += m ? expf(val - top) : 0.0f;
+          for (int v = 0; v < V; ++v) key[v] = best == (uint32_t)expert_of<G>(g, v) ? 0 : key[v];
+        } else {
+          best = 0xffffu - (m & 0xffffu);
+#pragma unroll
+          for (int v = 0; v < V; ++v) key[v] = key[v] == m ? 0 : key[v];
+        }
+        if (j == 0) top = key_logit<F32>(m);
         if (g == 0 && live) {
           const int e = m ? (int)best : -1;
           cid[ct * k + j] = e;
-          cval[ct * k + j] = val;
+          ckey[ct * k + j] = m;
           if (sorted && e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mark[e]), 1ull << ct);
         }
-      }
-      float z = zk;
-      if (gate == kGateSoftmax) {
-        z = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) z += l[v] > -INFINITY ? expf(l[v] - top) : 0.0f;
-        z = group_sum<G>(z);
       }
       // the group's own writes to LDS, read back by its other lanes
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
+      float z = 0.0f;
+      if (gate == kGateSoftmax) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) z += l[v] > -INFINITY ? expf(l[v] - top) : 0.0f;
+        z = group_sum<G>(z);
+      } else if (gate == kGateSoftmaxTopk) {
+        for (int j = g; live && j < k; j += G) {
+          const uint32_t m = ckey[ct * k + j];
+          z += m ? expf(key_logit<F32>(m) - top) : 0.0f;
+        }
+        z = group_sum<G>(z);
+      }
       if (live) {
         for (int j = g; j < k; j += G) {
           const int e = cid[ct * k + j];
-          const float val = cval[ct * k + j];
+          const float val = key_logit<F32>(ckey[ct * k + j]);
           const float w = gate == kGateSigmoid ? 1.0f / (1.0f + expf(-val)) : expf(val - top) / z;
           ids[t * k + j] = e;
           weights[t * k + j] = e >= 0 ? w + bad : 0.0f;
@@ -343,7 +375,8 @@ int64_t route_ws_words(int64_t T, int32_t E) {
 }
 
 // Lanes a token and logits a lane: the smallest group whose lanes hold at most
-// 8 logits each up to 128 experts, then 16.
+// 8 logits each up to 128 experts, then 16 (32768 x 512: 34 us with 32 lanes a
+// token, 60 with 64, half of them without experts).
 template <class F>
 static void by_experts(int E, F&& go) {
   if (E <= 16)
@@ -356,6 +389,8 @@ static void by_experts(int E, F&& go) {
     go(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
   else if (E <= 256)
     go(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
+  else if (E <= 512)
+    go(std::integral_constant<int, 32>{}, std::integral_constant<int, 16>{});
   else
     go(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
 }

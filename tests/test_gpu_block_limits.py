@@ -115,11 +115,13 @@ def test_few_every_token_on_one_expert(f, T):
     check_few(f, layer, x, ids, w)
 
 
-@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (700, 1, 1), (3, 1024, 32), (130, 33, 32)])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (700, 1, 1), (3, 1024, 32), (130, 33, 32), (70, 257, 8), (333, 512, 32),
+                                   (150, 513, 5)])
 def test_route_ends_of_the_range(f, T, E, k):
     import torch
     g = torch.Generator(device="cuda:0").manual_seed(T)
     l = torch.randn(T, E, generator=g, device="cuda:0")
+    check_route(f, l.to(torch.bfloat16), k, "softmax_topk")  # many equal logits
     for gate in ("softmax", "softmax_topk", "sigmoid"):
         check_route(f, l, k, gate)
 

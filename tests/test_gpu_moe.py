@@ -185,7 +185,8 @@ def bwd_reference(l, ids, w, dw, gate):
     return out, mag
 
 
-@pytest.mark.parametrize("T,E,k", [(1, 32, 8), (5, 1, 1), (130, 17, 3), (300, 100, 8), (77, 256, 8), (40, 1000, 32)])
+@pytest.mark.parametrize("T,E,k", [(1, 32, 8), (5, 1, 1), (130, 17, 3), (300, 100, 8), (77, 256, 8), (90, 257, 8),
+                                   (33, 512, 8), (40, 1000, 32)])
 @pytest.mark.parametrize("gate", GATES)
 def test_route_backward(f, T, E, k, gate):
     import torch
