@@ -38,8 +38,8 @@
 // 32). Everything else is fp32 up to the one rounding of the output.
 //
 // Measured, both launches, bytes of codes read: one token, 8 of 32 experts of D 7168 and
-// F 2048, packed: 352 MB in 64.5 us (5.5 TB/s); 16 tokens of the same, 31 experts named:
-// 1.38 GB in 228 us (6.0 TB/s); 64 tokens, 16 experts of D 5120, F 8192, row-major: 2.0 GB
+// F 2048, packed: 352 MB in 63.5 us (5.5 TB/s); 16 tokens of the same, 31 experts named:
+// 1.38 GB in 225 us (6.1 TB/s); 64 tokens, 16 experts of D 5120, F 8192, row-major: 2.0 GB
 // in 343 us (5.9 TB/s), packed 340. A kernel that only reads such an amount reaches 5.7
 // to 6.3 TB/s with these loads.
 //
