@@ -446,7 +446,9 @@ FP8DYN_API fp8_status fp8_grouped_wgrad_bf16(const uint16_t* gy, const uint16_t*
  * within one (a stable sort, the same on every run): offsets [E + 1], as
  * fp8_grouped_mm takes them (offsets[E] pairs in all); order [T * k]: the pair
  * t * k + j of each sorted row, -1 behind the last; slot [T][k]: the sorted row
- * of each pair, -1 where there is none. T = 0 writes zeros to offsets. E <= 1024,
+ * of each pair, -1 where there is none. With slots left empty offsets[E] is less
+ * than T * k, and the grouped GEMMs with Mtot = T * k neither use nor write the
+ * rows behind offsets[E]. T = 0 writes zeros to offsets. E <= 1024,
  * k <= 32, T * k < 2^31 (else FP8_ERR_UNSUPPORTED); k <= E. ws:
  * fp8_moe_route_ws_bytes(T, E, k) bytes (0 up to 64 tokens, or without
  * offsets), 4-byte aligned, content on entry of no matter; calls that may run

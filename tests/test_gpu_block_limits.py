@@ -4,7 +4,7 @@ calls captured into graphs that replay at the same time."""
 import pytest
 
 from tests.gpu_util import gpu, have_gpu, lib
-from tests.test_gpu_moe import Layer, _tokens, check_few, check_route, few_reference, run_few
+from tests.test_gpu_moe import Layer, _tokens, check_few, check_route, few_reference, run_few, run_route
 
 pytestmark = [gpu, pytest.mark.skipif(not have_gpu(), reason="needs an MI355X")]
 EPS = 1e-12
@@ -124,6 +124,45 @@ def test_route_ends_of_the_range(f, T, E, k):
     check_route(f, l.to(torch.bfloat16), k, "softmax_topk")  # many equal logits
     for gate in ("softmax", "softmax_topk", "sigmoid"):
         check_route(f, l, k, gate)
+
+
+@pytest.mark.parametrize("T,pad", [(48, 7), (300, 111)])
+def test_a_padded_batch_in_the_grouped_gemms(f, T, pad):
+    """Tokens without an expert leave rows behind the last pair: the grouped GEMMs over all T k
+    rows neither use what is there (NaN) nor write it."""
+    import torch
+    E, k, K, N = 8, 2, 256, 192
+    g = torch.Generator(device="cuda:0").manual_seed(740 + T)
+    l = torch.randn(T, E, generator=g, device="cuda:0")
+    l[T - pad:] = -float("inf")
+    ids, w, offsets, order, slot = run_route(f, l, k, "softmax")
+    M, used = T * k, (T - pad) * k
+    assert int(offsets[E]) == used and bool((order[used:] == -1).all()) and bool((slot[T - pad:] == -1).all())
+    assert f.fp8_validate_offsets(offsets.cpu().numpy(), M) != f.OK  # the strict check of a full batch
+    layer = Layer(E, N, K, 741, True)  # w2 codes [E][N][K]
+    codes = torch.randint(0, 0x7f, (M, K), generator=g, device="cuda:0", dtype=torch.int32).to(torch.uint8)
+    codes[used:] = 0x7F
+    inv = torch.rand(M, generator=g, device="cuda:0") * 1e-2
+    inv[used:] = float("nan")
+    paired = codes.reshape(M // 2, 2, K // 64, 64).transpose(1, 2).contiguous().reshape(M, K)
+
+    def gemm(call, a, b, rows, **shape):
+        out = torch.full((rows, N), 9.0, dtype=torch.bfloat16, device="cuda:0")
+        call(a[:rows], f.E4M3_NATIVE, b, f.E4M3_NATIVE, f.SCALE_ROW, inv[:rows], layer.i2, offsets, f.OUT_BF16, out,
+             use_fast_accum=False, **shape)
+        return out
+
+    for call, a, b, shape in ((f.fp8_grouped_mm, codes, layer.w2, {}),
+                              (f.fp8_grouped_mm_kpacked, paired, layer.c2, dict(N=N))):
+        out = gemm(call, a, b, M, **shape)
+        assert bool((out[used:] == 9.0).all())
+        assert torch.equal(out[:used], gemm(call, a, b, used, **shape))
+    gy, x = (torch.randn(M, n, generator=g, device="cuda:0").to(torch.bfloat16) for n in (N, K))
+    gy[used:] = x[used:] = float("nan")
+    gw = [torch.empty(E, N, K, dtype=torch.bfloat16, device="cuda:0") for _ in range(2)]
+    f.fp8_grouped_wgrad_bf16(gy, x, offsets, gw[0])
+    f.fp8_grouped_wgrad_bf16(gy[:used], x[:used], offsets, gw[1])
+    assert torch.equal(*gw) and not bool(gw[0].isnan().any())
 
 
 def test_split_tiles_and_placed_rows_captured(f):
