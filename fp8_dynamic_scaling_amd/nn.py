@@ -138,6 +138,13 @@ class Float8Linear(torch.nn.Module):
                 f"bias={self.bias is not None}, recipe={self.recipe}")
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t contiguous and from 16 bytes on, as the norm's kernels read it: a gradient may be a
+    contiguous piece of a longer tensor, at any offset."""
+    c = t.contiguous()
+    return c if c.data_ptr() % 16 == 0 else c.clone()
+
+
 class AddNormFunction(torch.autograd.Function):
     """h = x + res (bf16) and y = norm(h) through fp8_add_norm_quant_row, both differentiable; the
     gradients of x, res, gamma and beta through fp8_add_norm_bwd. res None: y alone, h = x."""
@@ -156,17 +163,17 @@ class AddNormFunction(torch.autograd.Function):
         cols = x.shape[-1]
         if gamma.shape != (cols,):
             raise ValueError(f"AddNorm: input has {cols} features, weight has {tuple(gamma.shape)}")
-        x2 = x.reshape(-1, cols).contiguous()
+        x2 = _dense(x.reshape(-1, cols))
         rows = x2.shape[0]
-        r2 = None if res is None else res.reshape(-1, cols).contiguous()
+        r2 = None if res is None else _dense(res.reshape(-1, cols))
         # the outputs have their own shape, not a view's: they may be changed in place
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         h = x2 if res is None else torch.empty_like(y)
         stats = dict(dtype=torch.float32, device=x.device)
         mean = torch.empty(rows, **stats) if kind == NORM_LAYER else None
         rstd = torch.empty(rows, **stats)
-        g = gamma.contiguous()
-        fp8_add_norm_quant_row(x2, r2, g, None if beta is None else beta.contiguous(), kind, norm_eps, E4M3_NATIVE,
+        g = _dense(gamma)
+        fp8_add_norm_quant_row(x2, r2, g, None if beta is None else _dense(beta), kind, norm_eps, E4M3_NATIVE,
                                1e-12, None if res is None else h.view(rows, cols), y.view(rows, cols), None, None,
                                mean=mean, rstd=rstd)
         ctx.save_for_backward(h, g, mean, rstd)
@@ -181,7 +188,7 @@ class AddNormFunction(torch.autograd.Function):
         cols = h.shape[-1]
         h = h.view(-1, cols)
         rows = h.shape[0]
-        flat = lambda g: None if g is None else g.to(torch.bfloat16).reshape(rows, cols).contiguous()  # noqa: E731
+        flat = lambda g: None if g is None else _dense(g.to(torch.bfloat16).reshape(rows, cols))  # noqa: E731
         dy, dh = flat(dy), flat(dh)
         if dy is None:  # only the stream behind h has a gradient
             dx = None if dh is None else dh.reshape(ctx.shape)
