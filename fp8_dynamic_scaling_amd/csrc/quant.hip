@@ -17,6 +17,7 @@
 namespace fp8dyn {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------------------
 // Row groups. One workgroup of 256 threads per row; the row (up to
@@ -1267,7 +1268,9 @@ __device__ __forceinline__ void exact_add(uint32_t b, long long* L1, long long* 
 // res may be null (h = x). h is written where asked, and mean32 and rstd32 for
 // the backward. Each lane writes just the elements of h it has read, after it
 // read them, so h may be x or res itself. h and y are stored past the caches,
-// as q is (8192 x 4096: 59.4 -> 55.5 us).
+// as q is (8192 x 4096: 59.4 -> 55.5 us). A value that is not finite is not hidden:
+// such a row has the IEEE formula's statistics, and a NaN in y makes the row's
+// scale and inverse scale NaN, so that its codes stand for NaN.
 struct NormAdd {
   const uint16_t* res;
   uint16_t* h;
@@ -1289,6 +1292,7 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const
   __shared__ double red_d[2][4];
   __shared__ uint32_t red_e[4];
   __shared__ float red[4];
+  __shared__ uint32_t red_b[4];  // ADD, in the place of red
   __shared__ long long s_limbs[TPR == 64 ? 4 : 1][kS1Limbs + kS2Limbs];
   __shared__ double s_exact[TPR == 64 ? 4 : 1][2];
   const int tid = threadIdx.x;
@@ -1403,30 +1407,34 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const
     rstd32 = r_small;
   }
   if (!settled) {
-    long long* L1 = s_limbs[slot];
-    long long* L2 = s_limbs[slot] + kS1Limbs;
-    if (t < kS1Limbs + kS2Limbs) s_limbs[slot][t] = 0;
-    if constexpr (TPR == 256) __syncthreads();
-    else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    // ADD: a row with a NaN or an infinity, whose s2 is one (finite squares stay below
+    // 2^270), keeps its IEEE sums: as integers they would look like finite values
+    if (!ADD || s2 < __builtin_inf()) {
+      long long* L1 = s_limbs[slot];
+      long long* L2 = s_limbs[slot] + kS1Limbs;
+      if (t < kS1Limbs + kS2Limbs) s_limbs[slot][t] = 0;
+      if constexpr (TPR == 256) __syncthreads();
+      else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+      for (int j = 0; j < J; ++j) {
+        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        exact_add<LAYER>(w[k] & 0xffffu, L1, L2);
-        exact_add<LAYER>(w[k] >> 16, L1, L2);
+        for (int k = 0; k < 4; ++k) {
+          exact_add<LAYER>(w[k] & 0xffffu, L1, L2);
+          exact_add<LAYER>(w[k] >> 16, L1, L2);
+        }
       }
+      if constexpr (TPR == 256) __syncthreads();
+      else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (t == 0) {
+        s_exact[slot][0] = LAYER ? limbs_to_double(L1, kS1Limbs, -133) : 0.0;
+        s_exact[slot][1] = limbs_to_double(L2, kS2Limbs, -266);
+      }
+      if constexpr (TPR == 256) __syncthreads();
+      else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      s1 = s_exact[slot][0];
+      s2 = s_exact[slot][1];
     }
-    if constexpr (TPR == 256) __syncthreads();
-    else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (t == 0) {
-      s_exact[slot][0] = LAYER ? limbs_to_double(L1, kS1Limbs, -133) : 0.0;
-      s_exact[slot][1] = limbs_to_double(L2, kS2Limbs, -266);
-    }
-    if constexpr (TPR == 256) __syncthreads();
-    else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    s1 = s_exact[slot][0];
-    s2 = s_exact[slot][1];
     const double mean = __ddiv_rn(s1, n), ms = __ddiv_rn(s2, n);
     const double var = LAYER ? __dsub_rn(ms, __dmul_rn(mean, mean)) : ms;
     const double rstd = __ddiv_rn(1.0, __dsqrt_rn(__dadd_rn(var, norm_eps)));
@@ -1442,6 +1450,7 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const
   }
   // normalize, keep as bf16 in registers (and store to y)
   float m = 0.0f;
+  u16x2_t mag = {0, 0};  // ADD: the magnitudes' bits, in whose order a NaN is above all
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int64_t c = 8 * (t + TPR * j);
@@ -1471,7 +1480,13 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const
       o[k] = __builtin_bit_cast(uint32_t, h);
     }
     v[j] = make_uint4(o[0], o[1], o[2], o[3]);
-    m = amax8(v[j], m);
+    if constexpr (ADD) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        mag = __builtin_elementwise_max(mag, __builtin_bit_cast(u16x2_t, o[k] & 0x7fff7fffu));
+    } else {
+      m = amax8(v[j], m);
+    }
     if (y) {
       if constexpr (ADD)
         st_nt16(y + row * cols + c, v[j]);
@@ -1480,10 +1495,22 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const
     }
   }
   if (!q) return;
-  if constexpr (TPR == 64)
+  if constexpr (ADD) {
+    // a row with a NaN has it as its maximum, and with it as its scale and inverse scale
+    uint32_t b = (uint32_t)(mag[0] > mag[1] ? mag[0] : mag[1]) << 16;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) b = max(b, (uint32_t)__shfl_xor((int)b, o, 64));
+    if constexpr (TPR == 256) {
+      if ((tid & 63) == 0) red_b[tid >> 6] = b;
+      __syncthreads();
+      b = max(max(red_b[0], red_b[1]), max(red_b[2], red_b[3]));
+    }
+    m = __uint_as_float(b);
+  } else if constexpr (TPR == 64) {
     m = wave_max(m);
-  else
+  } else {
     m = block_max<256>(m, red);
+  }
   float s, iv;
   scale_from_amax(m, fmax, eps, s, iv);
   if (t == 0) {

@@ -247,13 +247,16 @@ FP8DYN_API fp8_status fp8_norm_quant_row(const uint16_t* x, const uint16_t* gamm
 
 /* fp8_norm_quant_row of the residual stream, with the residual's addition in
  * the same pass: per row, h = bf16(x + res) (one fp32 addition, RNE), then y, q,
- * scale and inv_scale as fp8_norm_quant_row(h) writes them, bit for bit. h
- * [rows][cols] is written if non-NULL (the stream that the next addition
- * takes) and may be x or res itself; res may be NULL (then h = x, and h must be
- * NULL). mean [rows] (LAYER only) and rstd [rows] are mean32 and rstd32,
- * written if non-NULL, for fp8_add_norm_bwd. y or q (or both) must be given; y
- * and q overlap no input. Limits, alignment and formats as for
- * fp8_norm_quant_row; rows < 2^31. */
+ * scale and inv_scale as fp8_norm_quant_row(h) writes them, bit for bit, for
+ * rows of finite values. h [rows][cols] is written if non-NULL (the stream that
+ * the next addition takes) and may be x or res itself; res may be NULL (then
+ * h = x, and h must be NULL). mean [rows] (LAYER only) and rstd [rows] are
+ * mean32 and rstd32, written if non-NULL, for fp8_add_norm_bwd. y or q (or
+ * both) must be given; y and q overlap no input. Unlike there, a row of h with
+ * a NaN or an infinity (a sum past bf16's range is one) has the statistics and
+ * y of the IEEE formula, and a row of y with a NaN has NaN as its scale and
+ * inv_scale, so that its codes stand for NaN. Limits, alignment and formats as
+ * for fp8_norm_quant_row; rows < 2^31. */
 FP8DYN_API fp8_status fp8_add_norm_quant_row(const uint16_t* x, const uint16_t* res, const uint16_t* gamma,
                                              const uint16_t* beta, int64_t rows, int64_t cols, fp8_norm kind,
                                              double norm_eps, fp8_format fmt, double eps, uint16_t* h, uint16_t* y,

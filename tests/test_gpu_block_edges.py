@@ -5,7 +5,7 @@ import pytest
 
 import oracle
 import synth
-from tests.gpu_util import gpu, have_gpu, lib, to_dev_bf16
+from tests.gpu_util import gpu, have_gpu, lib
 from tests.test_gpu_add_norm import EPS, NEPS, _bits, _forward, _inputs, _sum_bits
 
 pytestmark = [gpu, pytest.mark.skipif(not have_gpu(), reason="needs an MI355X")]
@@ -57,3 +57,106 @@ def test_add_norm_operands_at_any_offset(f, kind, with_res):
     got = step(lambda at, size: flat[at:at + size].detach())
     want = step(lambda at, size: flat[at:at + size].detach().clone())
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---- rows that are not finite ---------------------------------------------------------------
+
+NAN, PINF, NINF, MAX = 0x7FC0, 0x7F80, 0xFF80, 0x7F7F
+# rows of inputs that are not finite, and sums of finite ones that pass bf16's range: in the
+# addition, and in its rounding (the largest value and half a step more, a tie)
+BAD = {1: (0, NAN, 0), 2: (5, PINF, 0), 3: (7, NINF, 0), 5: (0, MAX, MAX), 6: (3, 0, NAN), 8: (2, MAX, 0x7B00),
+       10: (1, 0xFFC0, PINF)}
+
+
+def _bad_inputs(cols, layer):
+    x, r, g, b = _inputs(12, cols, 4990 + cols, layer)
+    for row, (at, xv, rv) in BAD.items():
+        x[row, at - cols // 2], r[row, at - cols // 2] = xv, rv
+    x[9, 0], r[9, 0], x[9, cols - 1], r[9, cols - 1] = PINF, 0, NINF, 0  # both infinities
+    return x, r, g, b, sorted([*BAD, 9])
+
+
+def _formula(h, g, b, layer):
+    """y (fp32, before its rounding), mean and rstd of rows of h by IEEE arithmetic."""
+    with np.errstate(all="ignore"):
+        v = oracle.bf16_to_f32(h)
+        n = v.shape[1]
+        mean = v.astype(np.float64).sum(1) / n if layer else np.zeros(len(v))
+        rstd = 1.0 / np.sqrt((v.astype(np.float64) ** 2).sum(1) / n - mean * mean + NEPS)
+        y = (v - mean.astype(np.float32)[:, None]) * rstd.astype(np.float32)[:, None] * oracle.bf16_to_f32(g)
+        if layer:
+            y = y + oracle.bf16_to_f32(b)
+    return y.astype(np.float32), mean.astype(np.float32), rstd.astype(np.float32)
+
+
+# both numbers of threads a row, one and several pieces a lane
+@pytest.mark.parametrize("cols", [64, 1032, 2056, 6000])
+@pytest.mark.parametrize("layer", [False, True], ids=["rms", "layer"])
+def test_norm_rows_that_are_not_finite(f, layer, cols):
+    """A row whose h has a NaN or an infinity has the formula's statistics and outputs (all NaN,
+    or with an infinity under RMS zeros beside the NaN), and an inverse scale of NaN, whether y
+    is written or not; the rows beside it have their own bits."""
+    x, r, g, b, bad = _bad_inputs(cols, layer)
+    good = [i for i in range(len(x)) if i not in bad]
+    with np.errstate(all="ignore"):
+        h = _bits(oracle.bf16_to_f32(x) + oracle.bf16_to_f32(r))
+    for fmt, name in ((f.E4M3_NATIVE, "e4m3fn"), (f.E5M2_NATIVE, "e5m2")):
+        got = _forward(f, x, r, g, b, layer, fmt)
+        ry, rq, rs, ri = oracle.norm_quant_row(h[good], g, b, layer, NEPS, name, EPS)
+        assert np.array_equal(got["h"][good], h[good])
+        assert np.array_equal(got["y"][good], ry) and np.array_equal(got["q"][good], rq)
+        assert np.array_equal(got["scale"][good], rs) and np.array_equal(got["inv"][good], ri)
+        v = oracle.bf16_to_f32(got["h"][bad])
+        assert not np.isfinite(v).all(1).any()
+        y, mean, rstd = _formula(got["h"][bad], g, b, layer)
+        assert np.array_equal(got["rstd"][bad], rstd, equal_nan=True)
+        assert not layer or np.array_equal(got["mean"][bad], mean, equal_nan=True)
+        gy = oracle.bf16_to_f32(got["y"][bad])
+        assert np.array_equal(gy, y, equal_nan=True) and np.isnan(gy).any(1).all()  # 0 and NaN: exact in bf16
+        assert np.isnan(got["inv"][bad]).all() and np.isnan(got["scale"][bad]).all()
+        codes = _forward(f, x, r, g, b, layer, fmt, want_y=False)
+        for part in ("q", "scale", "inv", "rstd"):
+            assert np.array_equal(got[part], codes[part], equal_nan=part != "q"), part
+
+
+@pytest.mark.parametrize("cols", [264, 6000])
+def test_norm_outputs_that_are_not_finite(f, cols):
+    """Finite rows with a weight that is not, and a row of zeros without a norm_eps (0 times
+    infinity): y is the formula's, an inverse scale is NaN where y has a NaN, else infinite."""
+    x, r, g, _ = _inputs(6, cols, 4995, False)
+    h = _sum_bits(x, r)
+    ry = oracle.norm_quant_row(h, g, None, False, NEPS, "e4m3fn", EPS)[0]
+    for bits, test in ((NAN, np.isnan), (PINF, np.isinf)):
+        bad = g.copy()
+        bad[5] = bits
+        got = _forward(f, x, r, bad, None, False, f.E4M3_NATIVE)
+        y = oracle.bf16_to_f32(got["y"])
+        assert test(y[:, 5]).all() and test(got["inv"]).all()
+        keep = [c for c in range(cols) if c != 5]
+        assert np.array_equal(got["y"][:, keep], ry[:, keep])
+    r[2] = x[2] ^ 0x8000
+    got = _forward(f, x, r, g, None, False, f.E4M3_NATIVE, neps=0.0)
+    assert np.isnan(oracle.bf16_to_f32(got["y"][2])).all() and np.isnan(got["inv"][2])
+    assert np.isfinite(got["inv"][[0, 1, 3, 4, 5]]).all()
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_add_norm_hides_no_fault(f, kind):
+    """A NaN in one row of the stream: the row's y and gradient and the weight's gradient are
+    NaN, the other rows' as without it."""
+    import torch
+    from fp8_dynamic_scaling_amd.nn import AddNorm
+    m = AddNorm(264, kind, device="cuda:0")
+    x, res, dy, dh = (_randn(6, 264, seed=s) for s in (1, 2, 3, 4))
+    keep = [0, 1, 2, 4, 5]
+
+    def step(x):
+        x = x.clone().requires_grad_(True)
+        y, h = m(x, res)
+        return (y, *torch.autograd.grad([y, h], [x, m.weight], [dy, dh]))
+
+    clean = step(x)
+    x[3, 100] = float("nan")
+    y, dx, dw = step(x)
+    assert bool(y[3].isnan().all()) and bool(dx[3].isnan().all()) and bool(dw.isnan().all())
+    assert torch.equal(y[keep], clean[0][keep]) and torch.equal(dx[keep], clean[1][keep])
