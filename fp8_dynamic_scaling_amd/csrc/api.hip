@@ -325,11 +325,12 @@ fp8_status fp8_add_norm_quant_row(const uint16_t* x, const uint16_t* res, const 
   if (kind != FP8_NORM_RMS && kind != FP8_NORM_LAYER) return FP8_ERR_INVALID_ARGUMENT;
   if (kind == FP8_NORM_RMS && (beta || mean)) return FP8_ERR_INVALID_ARGUMENT;
   if (h && !res) return FP8_ERR_INVALID_ARGUMENT;  // without a residual h is x itself
+  if (rows >= ((int64_t)1 << 31)) return FP8_ERR_UNSUPPORTED;
   if (rows == 0) return FP8_OK;
   if (cols == 0) return empty_group_scales(fmt, false, eps, scale, inv_scale, scale ? rows : 0, stream);
   if (!x || !gamma || (!y && !q) || (q && !scale)) return FP8_ERR_INVALID_ARGUMENT;
   if (cols % 8 != 0) return FP8_ERR_ALIGNMENT;
-  if (cols > 16384 || rows >= ((int64_t)1 << 31)) return FP8_ERR_UNSUPPORTED;  // the row lives in registers
+  if (cols > 16384) return FP8_ERR_UNSUPPORTED;  // the row lives in registers
   if (!aligned(x, 16) || !aligned(gamma, 16) || (res && !aligned(res, 16)) || (beta && !aligned(beta, 16)) ||
       (h && !aligned(h, 16)) || (y && !aligned(y, 16)) || (q && !aligned(q, 8)) || (scale && !aligned(scale, 4)) ||
       (inv_scale && !aligned(inv_scale, 4)) || (mean && !aligned(mean, 4)) || (rstd && !aligned(rstd, 4)))

@@ -58,6 +58,9 @@ struct NormQuantArgs {
 hipError_t launch_norm_quant_row(const NormQuantArgs& a);
 hipError_t launch_add_norm_quant_row(const NormQuantArgs& a);
 
+// Workgroups of 256 threads a launch has at most: a grid has fewer than 2^32 threads.
+constexpr int64_t kMaxGrid256 = (int64_t)1 << 23;
+
 // Backward of the row normalization, with the residual stream's gradient.
 struct NormBwdArgs {
   const uint16_t* dy;     // [rows][cols]

@@ -512,8 +512,15 @@ hipError_t launch_moe_route_bwd(const RouteBwdArgs& a) {
   by_experts(a.E, [&](auto G, auto V) {
     auto kern = a.f32 ? k_moe_route_bwd<G.value, V.value, true> : k_moe_route_bwd<G.value, V.value, false>;
     const int64_t per = 256 / G.value;
-    hipLaunchKernelGGL(kern, dim3((unsigned)((a.T + per - 1) / per)), dim3(256), 0, a.stream, a.logits, a.T, a.E, a.k,
-                       a.gate, vec, a.ids, a.weights, a.dweights, a.dlogits);
+    // one launch unless the tokens pass what a grid holds; a later one's rows are as aligned
+    // as the first's, for their number is a multiple of 16
+    for (int64_t t = 0; t < a.T; t += kMaxGrid256 * per) {
+      const int64_t n = a.T - t < kMaxGrid256 * per ? a.T - t : kMaxGrid256 * per;
+      const int64_t at = t * a.E * (a.f32 ? 4 : 2);
+      hipLaunchKernelGGL(kern, dim3((unsigned)((n + per - 1) / per)), dim3(256), 0, a.stream,
+                         static_cast<const uint8_t*>(a.logits) + at, n, a.E, a.k, a.gate, vec, a.ids + t * a.k,
+                         a.weights + t * a.k, a.dweights + t * a.k, static_cast<uint8_t*>(a.dlogits) + at);
+    }
   });
   return hipGetLastError();
 }

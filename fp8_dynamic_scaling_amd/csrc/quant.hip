@@ -1527,32 +1527,37 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const
 
 template <bool E5, bool LAYER, bool ADD>
 static void launch_norm_quant_t(const NormQuantArgs& a) {
-  const dim3 block(256);
-  const NormAdd add{a.res, a.h, a.mean, a.rstd};
-  auto go = [&](auto kern, int64_t blocks) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), block, 0, a.stream, a.x, a.gamma, a.beta, a.rows, a.cols,
-                       a.norm_eps, a.y, a.q, a.scale, a.inv, a.fmax, a.eps, add);
+  // each workgroup has `per` rows; one launch unless the rows pass what a grid holds
+  auto go = [&](auto kern, int64_t per) {
+    for (int64_t r = 0; r < a.rows; r += kMaxGrid256 * per) {
+      const int64_t n = a.rows - r < kMaxGrid256 * per ? a.rows - r : kMaxGrid256 * per;
+      auto el = [&](auto* p) { return p ? p + r * a.cols : p; };
+      auto one = [&](auto* p) { return p ? p + r : p; };
+      const NormAdd add{el(a.res), el(a.h), one(a.mean), one(a.rstd)};
+      hipLaunchKernelGGL(kern, dim3((unsigned)((n + per - 1) / per)), dim3(256), 0, a.stream, el(a.x), a.gamma, a.beta,
+                         n, a.cols, a.norm_eps, el(a.y), el(a.q), one(a.scale), one(a.inv), a.fmax, a.eps, add);
+    }
   };
   if (ADD && a.cols <= 4096 && a.cols > (a.rows <= 1024 ? 1024 : 2048)) {
     // With two inputs and three outputs a row of over 2048 elements is better
     // shared by four wavefronts (8192 x 4096 with all outputs: 53.7 us, 55.5 us
     // with one; 16384 x 2048: 57.9 and 52.9 us); so are fewer rows than SIMDs
     // (1 x 4096: 3.5 and 6.0 us).
-    go(k_norm_quant_row<256, 2, E5, LAYER, ADD>, a.rows);
+    go(k_norm_quant_row<256, 2, E5, LAYER, ADD>, 1);
   } else if (a.cols <= 512 * 8) {  // one wavefront per row
-    const int64_t J = (a.cols + 511) / 512, blocks = (a.rows + 3) / 4;
+    const int64_t J = (a.cols + 511) / 512;
     if (J <= 2)
-      go(k_norm_quant_row<64, 2, E5, LAYER, ADD>, blocks);
+      go(k_norm_quant_row<64, 2, E5, LAYER, ADD>, 4);
     else if (J <= 4)
-      go(k_norm_quant_row<64, 4, E5, LAYER, ADD>, blocks);
+      go(k_norm_quant_row<64, 4, E5, LAYER, ADD>, 4);
     else
-      go(k_norm_quant_row<64, 8, E5, LAYER, ADD>, blocks);
+      go(k_norm_quant_row<64, 8, E5, LAYER, ADD>, 4);
   } else {
     const int64_t J = (a.cols + 2047) / 2048;
     if (J <= 4)
-      go(k_norm_quant_row<256, 4, E5, LAYER, ADD>, a.rows);
+      go(k_norm_quant_row<256, 4, E5, LAYER, ADD>, 1);
     else
-      go(k_norm_quant_row<256, 8, E5, LAYER, ADD>, a.rows);
+      go(k_norm_quant_row<256, 8, E5, LAYER, ADD>, 1);
   }
 }
 

@@ -160,3 +160,55 @@ def test_add_norm_hides_no_fault(f, kind):
     y, dx, dw = step(x)
     assert bool(y[3].isnan().all()) and bool(dx[3].isnan().all()) and bool(dw.isnan().all())
     assert torch.equal(y[keep], clean[0][keep]) and torch.equal(dx[keep], clean[1][keep])
+
+
+# ---- more rows than a launch holds ----------------------------------------------------------
+
+
+@pytest.mark.parametrize("rows,cols", [((1 << 26) + 5, 8), ((1 << 23) + 3, 2056)], ids=["wave", "workgroup"])
+def test_norm_rows_past_a_grid(f, rows, cols):
+    """A grid has fewer than 2^32 threads, 64 or 256 of them a row. Rows do not depend on each
+    other, so those at both ends and where a second launch begins are those of calls alone."""
+    import torch
+    bf = dict(dtype=torch.bfloat16, device="cuda:0")
+    x, gamma, beta = torch.empty(rows, cols, **bf).normal_(), _randn(cols, seed=5), _randn(cols, seed=6)
+
+    def forward(x):
+        n = len(x)
+        q = torch.full((n, cols), 0xA5, dtype=torch.uint8, device="cuda:0")
+        s = [torch.full((n,), -7.0, device="cuda:0") for _ in range(4)]
+        f.fp8_add_norm_quant_row(x, None, gamma, beta, f.NORM_LAYER, NEPS, f.E4M3_NATIVE, EPS, None, None, q, *s[:2],
+                                 mean=s[2], rstd=s[3])
+        return q, *s
+
+    whole = forward(x)
+    assert bool((whole[1] > 0).all()) and bool((whole[4] > 0).all())
+    for at in (0, 1 << 23, 1 << 24, 1 << 25, 1 << 26, rows):
+        lo, hi = max(0, at - 9), min(rows, at + 9)
+        if lo < hi:
+            for a, b in zip(whole, forward(x[lo:hi].clone())):
+                assert torch.equal(a[lo:hi], b), at
+
+
+@pytest.mark.parametrize("T,E,k", [((1 << 30) + 70, 1, 1), ((1 << 25) + 5, 520, 2)])
+def test_route_backward_tokens_past_a_grid(f, T, E, k):
+    import torch
+    l = torch.empty(T, E, dtype=torch.bfloat16, device="cuda:0").normal_()
+    ids, w = torch.empty(T, k, dtype=torch.int32, device="cuda:0"), torch.empty(T, k, device="cuda:0")
+    f.fp8_moe_route(l, f.GATE_SIGMOID, ids, w)
+    dw = torch.empty(T, k, device="cuda:0").normal_()
+    alone = {}
+    for at in (0, 1 << 25, 1 << 29, 1 << 30, T):
+        lo, hi = max(0, at - 70), min(T, at + 70)
+        if lo < hi:
+            part = [t[lo:hi].clone() for t in (l, ids, w, dw)]
+            alone[lo, hi] = torch.full_like(part[0], 7.0)
+            f.fp8_moe_route_bwd(part[0], f.GATE_SIGMOID, *part[1:], alone[lo, hi])
+    f.fp8_moe_route_bwd(l, f.GATE_SIGMOID, ids, w, dw, l)  # in place
+    for (lo, hi), b in alone.items():
+        assert torch.equal(l[lo:hi], b), (lo, hi)
+    # every token: w (1 - w) <= 1/4, so |dl| <= |dw| / 4, half a step of bf16 (2^-8 of it) and a few of
+    # fp32 above that: 0.25 (1 + 2^-8) = 0.25098
+    n = 1 << 22
+    for a, d in zip(l.split(n), dw.split(n)):
+        assert bool((a.abs().amax(1) <= 0.251 * d.abs().amax(1)).all())

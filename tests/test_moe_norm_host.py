@@ -191,3 +191,8 @@ def test_few_token_kernels_keep_the_matrix_core_rules(tmp_path):
     asm = out.read_text()
     assert "v_mfma" in asm
     assert not mfma_overlaps(asm) and not mfma_raw_hazards(asm)
+
+
+def test_add_norm_row_limit_holds_for_empty_rows(lib):
+    assert _norm(lib, rows=1 << 31, cols=0) == f.ERR_UNSUPPORTED
+    assert _norm(lib, rows=1 << 40, cols=0, q=None, scale=None) == f.ERR_UNSUPPORTED
