@@ -258,11 +258,14 @@ class RouteFunction(torch.autograd.Function):
         ctx.save_for_backward(l, ids, weights)
         ctx.gate = gate
         ctx.mark_non_differentiable(ids, offsets, order, slot)
+        ctx.set_materialize_grads(False)
         return ids, weights, offsets, order, slot
 
     @staticmethod
     @once_differentiable
     def backward(ctx, _ids, dweights, _offsets, _order, _slot):
+        if dweights is None:
+            return None, None, None
         l, ids, weights = ctx.saved_tensors
         dlogits = torch.empty_like(l)
         fp8_moe_route_bwd(l, ctx.gate, ids, weights, dweights.float().contiguous(), dlogits)
