@@ -150,8 +150,9 @@ def _arg(fn, name, t, nbytes, esize=None):
 
 
 def _args(fn, *operands):
-    """_arg for each (name, tensor, nbytes, dtype): contiguous, of exactly that dtype, at least
-    nbytes long and on one device, which is returned. A tensor may be None where nbytes is None."""
+    """_arg for each (name, tensor, nbytes, dtype): contiguous, of exactly that dtype (1: of any with
+    one-byte elements, as codes are), at least nbytes long and on one device, which is returned. A
+    tensor may be None where nbytes is None or False."""
     dev = None
     for name, t, nbytes, dtype in operands:
         if t is None:
@@ -159,7 +160,8 @@ def _args(fn, *operands):
                 raise ValueError(f"{fn}: {name} is required")
             continue
         at = t.get_device()
-        if at == dev and (t.dtype is dtype or dtype is None) and t.is_contiguous() and (not nbytes or t.nbytes >= nbytes):
+        kind = t.dtype is dtype or dtype is None or dtype == 1 and t.element_size() == 1
+        if at == dev and kind and t.is_contiguous() and (not nbytes or t.nbytes >= nbytes):
             continue  # all in order; below, the first operand, or what is wrong
         if at < 0 or not t.is_cuda:
             raise ValueError(f"{fn}: {name} must be on the GPU")
@@ -167,8 +169,8 @@ def _args(fn, *operands):
             dev = at
         elif at != dev:
             raise ValueError(f"{fn}: {name} is on another GPU than the operands before it")
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError(f"{fn}: {name} must be {dtype} (got {t.dtype})")
+        if not kind:
+            raise ValueError(f"{fn}: {name} must {'have 1-byte elements' if dtype == 1 else f'be {dtype}'} (got {t.dtype})")
         if not t.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous")
         if nbytes and t.nbytes < nbytes:
@@ -511,7 +513,7 @@ def fp8_add_norm_quant_row(x, res, gamma, beta, kind, norm_eps, fmt, eps, h, y, 
     q_rows = 0 if q is None else 4 * rows
     dev = _args(fn, ("x", x, n, bf), ("res", res, res is not None and n, bf), ("gamma", gamma, 2 * cols, bf),
                 ("beta", beta, beta is not None and 2 * cols, bf), ("h", h, h is not None and n, bf),
-                ("y", y, y is not None and n, bf), ("q", q, q is not None and n // 2, torch.uint8),
+                ("y", y, y is not None and n, bf), ("q", q, q is not None and n // 2, 1),
                 ("scale", scale, q_rows or (scale is not None and 4 * rows), f32),
                 ("inv_scale", inv_scale, inv_scale is not None and 4 * rows, f32),
                 ("mean", mean, mean is not None and 4 * rows, f32), ("rstd", rstd, rstd is not None and 4 * rows, f32))
@@ -593,7 +595,7 @@ def fp8_moe_few(x, ids, weights, w13, w13_inv, w2, w2_inv, fmt, out, ws, packed=
     out [T][D] bf16. w13 holds the e4m3 codes of [E][2F][D] (gate rows, then up rows), w2 those of
     [E][D][F], with w13_inv [E][2F] and w2_inv [E][D]; packed: k-packed codes."""
     import torch
-    fn, f32, u8 = "fp8_moe_few", torch.float32, torch.uint8
+    fn, f32 = "fp8_moe_few", torch.float32
     T, D = x.shape
     if ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError(f"{fn}: ids must be [T][k]")
@@ -602,8 +604,8 @@ def fp8_moe_few(x, ids, weights, w13, w13_inv, w2, w2_inv, fmt, out, ws, packed=
     k = ids.shape[1]
     E, F = w13_inv.shape[0], w13_inv.shape[1] // 2
     dev = _args(fn, ("x", x, 2 * T * D, torch.bfloat16), ("ids", ids, 4 * T * k, torch.int32),
-                ("weights", weights, 4 * T * k, f32), ("w13", w13, 2 * E * F * D, u8),
-                ("w13_inv", w13_inv, 8 * E * F, f32), ("w2", w2, E * F * D, u8), ("w2_inv", w2_inv, 4 * E * D, f32),
+                ("weights", weights, 4 * T * k, f32), ("w13", w13, 2 * E * F * D, 1),
+                ("w13_inv", w13_inv, 8 * E * F, f32), ("w2", w2, E * F * D, 1), ("w2_inv", w2_inv, 4 * E * D, f32),
                 ("out", out, 2 * T * D, torch.bfloat16), ("ws", ws, None, None))
     _launch(fn, dev, stream, _ptr(x), _ptr(ids), _ptr(weights), T, k, _ptr(w13), _ptr(w13_inv), _ptr(w2),
             _ptr(w2_inv), fmt, E, D, F, 1 if packed else 0, _ptr(out), _ptr(ws), 0 if ws is None else ws.nbytes)

@@ -212,3 +212,28 @@ def test_route_backward_tokens_past_a_grid(f, T, E, k):
     n = 1 << 22
     for a, d in zip(l.split(n), dw.split(n)):
         assert bool((a.abs().amax(1) <= 0.251 * d.abs().amax(1)).all())
+
+
+# ---- codes in torch's float8 tensors ----------------------------------------------------------
+
+
+def test_codes_in_float8_tensors(f):
+    """The norm's codes and the expert layer's weights as torch.float8_e4m3fn: the same bytes."""
+    import torch
+    from tests.test_gpu_moe import Layer, _tokens
+    x, res, gamma = _randn(5, 264, seed=1), _randn(5, 264, seed=2), _randn(264, seed=3)
+    got = []
+    for dtype in (torch.uint8, torch.float8_e4m3fn):
+        q, s = torch.empty(5, 264, dtype=dtype, device="cuda:0"), torch.empty(5, device="cuda:0")
+        f.fp8_add_norm_quant_row(x, res, gamma, None, f.NORM_RMS, NEPS, f.E4M3_NATIVE, EPS, None, None, q, s)
+        got.append(q.view(torch.uint8))
+    assert torch.equal(*got)
+    layer = Layer(4, 128, 64, 800, False)
+    x, ids, w = _tokens(3, 4, 2, 128, 801)
+    ws = torch.empty(f.fp8_moe_few_ws_bytes(3, 2, 64), dtype=torch.uint8, device="cuda:0")
+    out = []
+    for view in (torch.uint8, torch.float8_e4m3fn):
+        out.append(torch.empty_like(x))
+        f.fp8_moe_few(x, ids, w, layer.w13.view(view), layer.i13, layer.w2.view(view), layer.i2, f.E4M3_NATIVE, out[-1],
+                      ws)
+    assert torch.equal(*out)

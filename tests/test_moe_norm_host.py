@@ -196,3 +196,18 @@ def test_few_token_kernels_keep_the_matrix_core_rules(tmp_path):
 def test_add_norm_row_limit_holds_for_empty_rows(lib):
     assert _norm(lib, rows=1 << 31, cols=0) == f.ERR_UNSUPPORTED
     assert _norm(lib, rows=1 << 40, cols=0, q=None, scale=None) == f.ERR_UNSUPPORTED
+
+
+def test_binding_takes_codes_of_any_one_byte_type():
+    """As the quantizers and the GEMMs do: codes may be in torch's float8 tensors."""
+    class Codes(_Fake):
+        def element_size(self):
+            return self.dtype.itemsize
+
+    for dtype in (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2):
+        for first in ((), (("x", _Fake(64, torch.bfloat16), 64, torch.bfloat16),)):
+            assert f._args("fn", *first, ("q", Codes(64, dtype), 64, 1)) == 0
+            with pytest.raises(ValueError, match="needs 65"):
+                f._args("fn", *first, ("q", Codes(64, dtype), 65, 1))
+    with pytest.raises(ValueError, match=r"1-byte elements \(got torch.bfloat16\)"):
+        f._args("fn", ("q", Codes(64, torch.bfloat16), 64, 1))
