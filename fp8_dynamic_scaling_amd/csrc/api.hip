@@ -605,8 +605,8 @@ static fp8_status check_route(fp8_out logits_type, int64_t T, int32_t E, int32_t
   if (T < 0 || E < 1 || k < 1 || k > E) return FP8_ERR_INVALID_ARGUMENT;
   if (logits_type != FP8_OUT_BF16 && logits_type != FP8_OUT_F32) return FP8_ERR_INVALID_ARGUMENT;
   if ((int)gate < 0 || (int)gate > 2) return FP8_ERR_INVALID_ARGUMENT;
-  // an expert's logits live in registers; pairs are numbered in 32 bits
-  if (E > 1024 || k > 32 || T > INT32_MAX / k) return FP8_ERR_UNSUPPORTED;
+  // pairs are numbered in 32 bits
+  if (E > kMaxMoeE || k > kMaxMoeK || T > INT32_MAX / k) return FP8_ERR_UNSUPPORTED;
   return FP8_OK;
 }
 
@@ -651,7 +651,7 @@ fp8_status fp8_moe_route_bwd(const void* logits, fp8_out logits_type, int64_t T,
 }
 
 size_t fp8_moe_few_ws_bytes(int64_t T, int32_t k, int64_t F) {
-  if (T <= 0 || T > 64 || k <= 0 || k > 32 || F <= 0 || F >= (1 << 20)) return 0;
+  if (T <= 0 || T > kFewT || k <= 0 || k > kMaxMoeK || F <= 0 || F >= (1 << 20)) return 0;
   return moe_few_ws_bytes(T, k, F);
 }
 
@@ -660,7 +660,7 @@ fp8_status fp8_moe_few(const uint16_t* x, const int32_t* ids, const float* weigh
                        fp8_format fmt, int32_t E, int64_t D, int64_t F, int packed, uint16_t* out, void* ws,
                        size_t ws_bytes, void* stream) {
   if (T < 0 || k < 1 || E < 1 || D < 0 || F < 0) return FP8_ERR_INVALID_ARGUMENT;
-  if (T > 64 || k > 32 || E > 1024 || D >= (1 << 20) || F >= (1 << 20)) return FP8_ERR_UNSUPPORTED;
+  if (T > kFewT || k > kMaxMoeK || E > kMaxMoeE || D >= (1 << 20) || F >= (1 << 20)) return FP8_ERR_UNSUPPORTED;
   const int step = packed ? 64 : 16;
   if (D % step != 0 || F % step != 0) return FP8_ERR_ALIGNMENT;
   if (T == 0 || D == 0) return FP8_OK;

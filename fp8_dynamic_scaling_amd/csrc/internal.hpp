@@ -80,6 +80,12 @@ struct NormBwdArgs {
 hipError_t launch_norm_bwd(const NormBwdArgs& a);
 int64_t norm_bwd_ws_floats(int64_t rows, int64_t cols, bool layer);
 
+// Limits of the router and of the layer for a few tokens: experts (a token's logits live in
+// registers), choices, and the layer's tokens.
+constexpr int32_t kMaxMoeE = 1024;
+constexpr int32_t kMaxMoeK = 32;
+constexpr int kFewT = 64;
+
 // Expert router: the k largest logits of each token, gate weights, and the
 // rows sorted by expert.
 enum GateKind : int { kGateSoftmax = 0, kGateSoftmaxTopk = 1, kGateSigmoid = 2 };
@@ -87,7 +93,7 @@ struct RouteArgs {
   const void* logits;  // [T][E], bf16 or fp32
   bool f32;
   int64_t T;           // T * k < 2^31
-  int32_t E, k;        // E <= 1024, 1 <= k <= min(E, 32)
+  int32_t E, k;        // E <= kMaxMoeE, 1 <= k <= min(E, kMaxMoeK)
   int gate;
   int32_t* ids;        // [T][k]
   float* weights;      // [T][k]
@@ -122,8 +128,8 @@ struct MoeFewArgs {
   const float* inv13;     // [E][2F]
   const uint8_t* w2;      // [E][D][F] e4m3
   const float* inv2;      // [E][D]
-  int64_t T;              // <= 64
-  int32_t E, k;           // E <= 1024, k <= 32
+  int64_t T;              // <= kFewT
+  int32_t E, k;           // E <= kMaxMoeE, k <= kMaxMoeK
   int64_t D, F;           // % 16 == 0 (packed: % 64 == 0), < 2^20: 32-bit byte offsets in x and act
   bool packed;
   uint16_t* out;          // [T][D]

@@ -63,8 +63,6 @@ constexpr int kDownWaves = 8;
 constexpr int kDownBlocks = 256;  // one a CU
 constexpr int kDownTiles = 2;     // tiles of 16 rows a unit has at most
 constexpr int kDownRows = 16 * kDownTiles;
-constexpr int kFewT = 64;
-constexpr int kFewK = 32;
 
 // What k_moe_up leaves in the workspace for k_moe_down: a, in units of 128 values
 // of F, the last one with room for as many; an expert's units are at pair 4 start
@@ -324,11 +322,11 @@ __device__ __forceinline__ void by_tokens(int m, F&& go) {
 }
 
 struct UpShared {
-  int32_t sid[kFewT * kFewK];
+  int32_t sid[kFewT * kMaxMoeK];
   int32_t list[kFewT];
   float gate[kFewT];
   float scale[2][32];
-  uint32_t bits[32];
+  uint32_t bits[kMaxMoeE / 32];
   int count[2];
 };
 
@@ -524,7 +522,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeFewArgs p) {
 }
 
 struct DownShared {
-  uint16_t expert[kMaxExperts], start[kMaxExperts + 1], token[kFewT * kFewK];
+  uint16_t expert[kMaxMoeE], start[kMaxMoeE + 1], token[kFewT * kMaxMoeK];
   int count;
 };
 

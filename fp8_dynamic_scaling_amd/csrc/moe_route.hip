@@ -33,8 +33,6 @@ namespace fp8dyn {
 
 namespace {
 constexpr int kChunk = 64;         // tokens a workgroup chooses for at a time
-constexpr int kMaxRouteK = 32;
-constexpr int kMaxRouteE = 1024;
 constexpr int kMaxRouteBlocks = 256;
 
 // Tokens a block: all of them up to kChunk; else so that at most kMaxRouteBlocks

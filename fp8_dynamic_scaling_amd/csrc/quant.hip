@@ -1286,8 +1286,7 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const
                                                         float* __restrict__ inv, double fmax, double eps,
                                                         NormAdd add) {
   // TPR threads per row: 64 (one wavefront per row, 4 rows per workgroup, no
-  // barrier; LDS only in the exact-sum path) for rows up to 4096 elements,
-  // else 256
+  // barrier; LDS only in the exact-sum path) or 256; launch_norm_quant_t chooses
   static_assert(TPR == 64 || TPR == 256, "threads per row");
   __shared__ double red_d[2][4];
   __shared__ uint32_t red_e[4];
@@ -1446,7 +1445,6 @@ __global__ __launch_bounds__(256) void k_norm_quant_row(const uint16_t* x, const
       if (add.mean) add.mean[row] = mean32;
       if (add.rstd) add.rstd[row] = rstd32;
     }
-    if (!y && !q) return;
   }
   // normalize, keep as bf16 in registers (and store to y)
   float m = 0.0f;
