@@ -16,7 +16,8 @@
 //    experts, evenly; the waves share a tile's (expert, piece of F) units. A wave
 //    adds what it has of a token to its own fp32 sums in LDS, the waves' sums are
 //    added in order, and so are those of workgroups that share a tile: the same
-//    inputs give the same bits.
+//    inputs give the same bits. How tiles are shared goes by the experts that the
+//    batch names, so a token's sums may be taken in another order in another batch.
 // A wave's unit of work is twice 16 rows x 128 values of the
 // contraction and the same 128 values of its tokens. An expert's tokens are
 // compacted into tiles of 16.
@@ -35,7 +36,9 @@
 // output as the output's own rounding. The second one costs 2 to 3% of the call with
 // few tokens (63.2 -> 64.5 us with one, 333 -> 343 with 64 that take one of 16 experts
 // each) and up to 14% where an expert has many (293 -> 334 us, 64 tokens that take 8 of
-// 32). Everything else is fp32 up to the one rounding of the output.
+// 32). Some of the outputs are therefore rounded to the other neighbour than with an fp32 a
+// (1e-4 of the norm); their error against 64 bits is the same. Everything else is fp32 up to
+// the one rounding of the output.
 //
 // Measured, both launches, bytes of codes read: one token, 8 of 32 experts of D 7168 and
 // F 2048, packed: 352 MB in 63.5 us (5.5 TB/s); 16 tokens of the same, 31 experts named:
@@ -52,11 +55,11 @@
 namespace fp8dyn {
 
 namespace {
-// One token (8 of 32 experts, D 7168, F 2048), 16 tokens of the same and 64 tokens (1 of
-// 16 experts, D 5120, F 8192): with 512 workgroups k_moe_up takes 58, 223 and 311 us,
-// with 1024 39, 147 and 221, with 2048, which take turns on the CUs, 39, 186 and 232.
-// k_moe_down with one tile of 16 rows a unit takes 36, 115 and 158 us, with two, which
-// share a load of the tokens, 23, 78 and 115.
+// Medians of launches back to back, one token (8 of 32 experts, D 7168, F 2048), 16 tokens of
+// the same and 64 tokens (1 of 16 experts, D 5120, F 8192): with 512 workgroups k_moe_up
+// takes 59, 240 and 350 us, with 1024 40, 154 and 237, with 2048, which take turns on the
+// CUs, 40, 183 and 282. k_moe_down with one tile of 16 rows a unit takes 37, 128 and 189 us,
+// with two, which share a load of the tokens, 24, 84 and 129.
 constexpr int kUpWaves = 2;
 constexpr int kUpBlocks = 1024;  // four a CU
 constexpr int kDownWaves = 8;
@@ -796,9 +799,9 @@ static hipError_t launch_few_t(const MoeFewArgs& a) {
     return hipGetLastError();
   };
   // One tile of 16 rows a unit where two would leave half of the CUs without work
-  // and a tile is too short to be split (k_moe_down, with one and with two: 5 tokens,
-  // 8 experts, D 1040, F 720: 7.2 and 8.9 us; 32 tokens, 16 experts, D 4096, F 2048: 37.9
-  // and 42.7 us).
+  // and a tile is too short to be split (k_moe_down, with one and with two: 5 tokens, 2 of
+  // 8 experts, D 1040, F 720: 8.1 and 9.7 us; 32 tokens, 2 of 16 experts, D 4096, F 2048: 40.1
+  // and 40.7 us).
   const bool narrow = a.D <= 16 * kDownBlocks && experts * ((a.F + 127) / 128) <= kDownWaves * 32;
   auto by_rows = [&](auto up, auto one, auto two) { return narrow ? go(up, one) : go(up, two); };
   if (a.T <= 16) return by_rows(k_moe_up<1, PACKED>, k_moe_down<1, PACKED, 1>, k_moe_down<1, PACKED, kDownTiles>);

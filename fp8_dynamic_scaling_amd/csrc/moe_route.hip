@@ -22,8 +22,8 @@
 // exchanges between lanes, up to 16 lanes within the vector unit. What remains is
 // latency: the exchanges, k rounds of them, and two to three trips to memory.
 // Measured, choosing + placing: 64 tokens x 32 experts, k 8: 4.3 us; 16384 x 32, k 8:
-// 5.9 + 6.0 us (2 MB of logits); 4096 x 256: 7.3 + 8.5; 65536 x 128, k 8: 24 + 9 us with bf16
-// logits, 26 + 9 with fp32, bound by the vector instructions of the choices.
+// 5.9 + 6.0 us (2 MB of logits); 4096 x 256: 7.9 + 8.1; 65536 x 128, k 8: 25 + 9 us with bf16
+// logits, 29 + 9 with fp32, bound by the vector instructions of the choices.
 #include <type_traits>
 
 #include "common.hpp"
@@ -37,7 +37,7 @@ constexpr int kMaxRouteBlocks = 256;
 
 // Tokens a block: all of them up to kChunk; else so that at most kMaxRouteBlocks
 // (one a CU) count, for the second launch reads all their counts in every block
-// (4096 x 256, 64 tokens a block: 12 + 5 us, 16 tokens: 7.3 + 8.5, 8 tokens: 12 + 16).
+// (4096 x 256, 64 tokens a block: 13 + 5 us, 16 tokens: 7.9 + 8.1, 8 tokens: 13 + 23).
 int64_t route_block_tokens(int64_t T) {
   if (T <= kChunk) return kChunk;
   const int64_t per = (T + kMaxRouteBlocks - 1) / kMaxRouteBlocks;
@@ -46,8 +46,8 @@ int64_t route_block_tokens(int64_t T) {
 }  // namespace
 
 // Threads of a block: what counts is the number of rounds over a chunk (65536 x 128
-// experts with 512: 29 us, with 1024: 24), and in the second launch over the counts
-// (256 threads: 12 us, 1024: 8.5); small blocks take the same time with either.
+// experts with 512: 30 us, with 1024: 25), and in the second launch over the counts
+// (4096 x 256 with 256: 12 us, with 1024: 8.1); small blocks take the same time with either.
 constexpr int kRouteThreads = 1024;
 constexpr int kPlaceThreads = 1024;
 
@@ -423,7 +423,7 @@ hipError_t launch_moe_route(const RouteArgs& a) {
 //   SOFTMAX_TOPK  the same over the chosen experts (p = w, 0 elsewhere)
 //   SIGMOID       dl_s = w_s (1 - w_s) dw_s, 0 elsewhere
 // p is computed again from the logits; -inf and a token of -inf alone get 0. Reads and
-// writes a logit once; measured 7.6 us for 8192 x 256 fp32 logits, k 8 (17 MB), of which
+// writes a logit once; measured 8.3 us for 8192 x 256 fp32 logits, k 8 (17 MB), of which
 // an empty launch is 3.5: one trip to memory, the exchanges, the stores.
 template <int G, int V, bool F32>
 __global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, int64_t T, int E, int k, int gate, int vec,

@@ -255,8 +255,9 @@ FP8DYN_API fp8_status fp8_norm_quant_row(const uint16_t* x, const uint16_t* gamm
  * both) must be given; y and q overlap no input. Unlike there, a row of h with
  * a NaN or an infinity (a sum past bf16's range is one) has the statistics and
  * y of the IEEE formula, and a row of y with a NaN has NaN as its scale and
- * inv_scale, so that its codes stand for NaN. Limits, alignment and formats as
- * for fp8_norm_quant_row; rows < 2^31. */
+ * inv_scale, so that its codes stand for NaN. cols = 0 writes the scales of
+ * empty rows and no statistics. Limits, alignment and formats as for
+ * fp8_norm_quant_row; rows < 2^31. */
 FP8DYN_API fp8_status fp8_add_norm_quant_row(const uint16_t* x, const uint16_t* res, const uint16_t* gamma,
                                              const uint16_t* beta, int64_t rows, int64_t cols, fp8_norm kind,
                                              double norm_eps, fp8_format fmt, double eps, uint16_t* h, uint16_t* y,
@@ -484,14 +485,15 @@ FP8DYN_API fp8_status fp8_moe_route_bwd(const void* logits, fp8_out logits_type,
  * operands of fp8_grouped_mm(_kpacked). Only the named experts' codes are read,
  * once. x is not quantized: the products are bf16 (codes decoded exactly) with
  * fp32 sums; a is kept to 16 bits, as two bf16 values; out [T][D] is rounded to
- * bf16 once. An id outside
- * [0, E) names no expert; one that a token names twice counts with the sum of
- * its weights; a token that names none gets zeros. The order of all sums is
- * fixed. D % 16 == 0 and F % 16 == 0 (packed: % 64), 16-byte aligned x, w13, w2,
- * out, ws (else FP8_ERR_ALIGNMENT); k <= 32, E <= 1024, D, F < 2^20 (else
- * FP8_ERR_UNSUPPORTED); fmt the native e4m3. F = 0 writes zeros. ws:
- * fp8_moe_few_ws_bytes(T, k, F) bytes (some 16 * T * k * F), content on entry
- * of no matter; calls that may run at the same time need one each. */
+ * bf16 once. An id outside [0, E) names no expert; one that a token names twice
+ * counts with the sum of its weights; a token that names none gets zeros. The
+ * same inputs give the same bits on every run; the order of a token's sums goes
+ * by the experts that the whole batch names, so its bits may change with the
+ * tokens beside it. D % 16 == 0 and F % 16 == 0 (packed: % 64), 16-byte aligned
+ * x, w13, w2, out, ws (else FP8_ERR_ALIGNMENT); k <= 32, E <= 1024, D, F < 2^20
+ * (else FP8_ERR_UNSUPPORTED); fmt the native e4m3. F = 0 writes zeros. ws:
+ * fp8_moe_few_ws_bytes(T, k, F) bytes (some 16 * T * k * F), content on entry of
+ * no matter; calls that may run at the same time need one each. */
 FP8DYN_API fp8_status fp8_moe_few(const uint16_t* x, const int32_t* ids, const float* weights, int64_t T, int32_t k,
                                   const uint8_t* w13, const float* w13_inv, const uint8_t* w2, const float* w2_inv,
                                   fp8_format fmt, int32_t E, int64_t D, int64_t F, int packed, uint16_t* out,
