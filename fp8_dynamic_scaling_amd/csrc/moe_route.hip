@@ -57,7 +57,9 @@ __device__ __forceinline__ int expert_of(int g, int v) {
 }
 
 // A token's logits in its lanes; -inf behind E and where the token is not live.
-// vec: rows are 16-byte (bf16: 8-byte) aligned and E % 4 == 0.
+// vec: rows are 16-byte (bf16: 8-byte) aligned and E % 4 == 0. Else element by element: 65536
+// tokens, 126 instead of 128 experts: 31 and 28 us with fp32 logits, 26 and 24 with bf16; the
+// backward, whose stores are single too, 27 and 19, 20 and 18.
 template <int G, int V, bool F32>
 __device__ __forceinline__ void load_logits(const void* p, int64_t t, int E, int g, bool live, bool vec,
                                             float (&l)[V]) {
