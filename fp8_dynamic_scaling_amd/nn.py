@@ -161,8 +161,9 @@ class AddNormFunction(torch.autograd.Function):
         if res is not None and res.shape != x.shape:
             raise ValueError(f"AddNorm: input {tuple(x.shape)} and residual {tuple(res.shape)} differ in shape")
         cols = x.shape[-1]
-        if gamma.shape != (cols,):
-            raise ValueError(f"AddNorm: input has {cols} features, weight has {tuple(gamma.shape)}")
+        for t, name in ((gamma, "weight"), (beta, "bias")):
+            if t is not None and t.shape != (cols,):
+                raise ValueError(f"AddNorm: input has {cols} features, {name} has {tuple(t.shape)}")
         x2 = _dense(x.reshape(-1, cols))
         rows = x2.shape[0]
         r2 = None if res is None else _dense(res.reshape(-1, cols))

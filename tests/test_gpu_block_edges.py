@@ -237,3 +237,15 @@ def test_codes_in_float8_tensors(f):
         f.fp8_moe_few(x, ids, w, layer.w13.view(view), layer.i13, layer.w2.view(view), layer.i2, f.E4M3_NATIVE, out[-1],
                       ws)
     assert torch.equal(*out)
+
+
+def test_add_norm_refuses_parameters_of_another_size(f):
+    import torch
+    from fp8_dynamic_scaling_amd.nn import AddNorm
+    x = _randn(3, 64, seed=1)
+    for name in ("weight", "bias"):
+        for size in (56, 72):
+            m = AddNorm(64, "layer", device="cuda:0")
+            setattr(m, name, torch.nn.Parameter(_randn(size, seed=2)))
+            with torch.no_grad(), pytest.raises(ValueError, match="64 features, " + name):
+                m(x)
