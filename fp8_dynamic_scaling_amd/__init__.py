@@ -22,6 +22,8 @@ OUT_BF16, OUT_F32 = range(2)
 MX_POW2_FLOOR, MX_OCP = range(2)
 RECIPE_TENSORWISE, RECIPE_ROWWISE_BF16_WGRAD = range(2)
 GATE_SOFTMAX, GATE_SOFTMAX_TOPK, GATE_SIGMOID = range(3)
+ACT_SILU, ACT_GELU_TANH = range(2)
+STATE_F32, STATE_MX8 = range(2)
 
 EXPORTS = [
     "fp8_probe", "fp8_status_string", "fp8_last_device_error", "fp8_format_max",
@@ -34,6 +36,8 @@ EXPORTS = [
     "fp8_linear_ws_bytes", "fp8_validate_offsets",
     "fp8_add_norm_quant_row", "fp8_add_norm_bwd", "fp8_add_norm_bwd_ws_bytes",
     "fp8_moe_route", "fp8_moe_route_ws_bytes", "fp8_moe_route_bwd", "fp8_moe_few", "fp8_moe_few_ws_bytes",
+    "fp8_gated_mm", "fp8_grouped_gated_mm", "fp8_gated_bwd",
+    "fp8_adamw", "fp8_grad_norm", "fp8_grad_norm_ws_bytes",
 ]
 
 
@@ -97,6 +101,12 @@ def load(path: str = LIB_PATH):
         "fp8_moe_route_bwd": (I, [P, I, I64, I32, I32, I, P, P, P, P, P]),
         "fp8_moe_few": (I, [P, P, P, I64, I32, P, P, P, P, I, I32, I64, I64, I, P, P, SZ, P]),
         "fp8_moe_few_ws_bytes": (SZ, [I64, I32, I64]),
+        "fp8_gated_mm": (I, [P, P, I, I, P, P, I64, I64, I64, I, I, P, P, I, P]),
+        "fp8_grouped_gated_mm": (I, [P, P, I, P, P, P, I32, I64, I64, I64, I, I, P, P, I, P]),
+        "fp8_gated_bwd": (I, [P, P, I64, I64, I, I, D, P, P, P, P, P, P]),
+        "fp8_adamw": (I, [P, I32, I, I, I, D, D, D, D, D, I64, ctypes.c_uint64, P, P, P, P]),
+        "fp8_grad_norm": (I, [P, I32, D, D, P, P, P, P, SZ, P]),
+        "fp8_grad_norm_ws_bytes": (SZ, [P, I32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -609,6 +619,161 @@ def fp8_moe_few(x, ids, weights, w13, w13_inv, w2, w2_inv, fmt, out, ws, packed=
                 ("out", out, 2 * T * D, torch.bfloat16), ("ws", ws, None, None))
     _launch(fn, dev, stream, _ptr(x), _ptr(ids), _ptr(weights), T, k, _ptr(w13), _ptr(w13_inv), _ptr(w2),
             _ptr(w2_inv), fmt, E, D, F, 1 if packed else 0, _ptr(out), _ptr(ws), 0 if ws is None else ws.nbytes)
+
+
+# ---- gated feed-forward block ---------------------------------------------------------
+
+def fp8_gated_mm(a, b, fmt, scaling, a_inv, b_inv, act, gu, out, packed=False, use_fast_accum=True, stream=None):
+    """out [M][F] = act(g) * u in bf16 for the projections [g | u] = a b^T of a [M][K] and b (the codes of
+    [2F][K], gate rows first); gu [M][2F]: the projections in bf16, or None. packed: b k-packed."""
+    import torch
+    fn, bf, f32 = "fp8_gated_mm", torch.bfloat16, torch.float32
+    M, K = a.shape
+    if out.dim() != 2 or out.shape[0] != M:
+        raise ValueError(f"{fn}: out must be [M][F]")
+    F = out.shape[1]
+    row = scaling == SCALE_ROW
+    dev = _args(fn, ("a", a, M * K, 1), ("b", b, 2 * F * K, 1), ("a_inv", a_inv, K and 4 * (M if row else 1), f32),
+                ("b_inv", b_inv, K and 4 * (2 * F if row else 1), f32), ("gu", gu, gu is not None and 4 * M * F, bf),
+                ("out", out, 2 * M * F, bf))
+    _launch(fn, dev, stream, _ptr(a), _ptr(b), fmt, scaling, _ptr(a_inv), _ptr(b_inv), M, F, K, act,
+            1 if packed else 0, _ptr(gu), _ptr(out), 1 if use_fast_accum else 0)
+
+
+def fp8_grouped_gated_mm(a, b, fmt, a_inv, b_inv, offsets, act, gu, out, packed=False, use_fast_accum=True,
+                         stream=None):
+    """fp8_gated_mm of the rows [offsets[e], offsets[e + 1]) of a with expert e of b (the codes of [E][2F][K],
+    b_inv [E][2F]); packed: a pair-interleaved, b k-packed. Rows behind offsets[E] stay as they were."""
+    import torch
+    fn, bf, f32 = "fp8_grouped_gated_mm", torch.bfloat16, torch.float32
+    M, K = a.shape
+    if out.dim() != 2 or out.shape[0] != M:
+        raise ValueError(f"{fn}: out must be [Mtot][F]")
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError(f"{fn}: offsets must hold E + 1 entries")
+    F, E = out.shape[1], offsets.numel() - 1
+    dev = _args(fn, ("a", a, M * K, 1), ("b", b, 2 * E * F * K, 1), ("a_inv", a_inv, K and 4 * M, f32),
+                ("b_inv", b_inv, K and 8 * E * F, f32), ("offsets", offsets, 4 * (E + 1), torch.int32),
+                ("gu", gu, gu is not None and 4 * M * F, bf), ("out", out, 2 * M * F, bf))
+    _launch(fn, dev, stream, _ptr(a), _ptr(b), fmt, _ptr(a_inv), _ptr(b_inv), _ptr(offsets), E, M, F, K, act,
+            1 if packed else 0, _ptr(gu), _ptr(out), 1 if use_fast_accum else 0)
+
+
+def fp8_gated_bwd(dh, gu, act, fmt, eps, dgu, q, scale, inv_scale=None, h=None, stream=None):
+    """dh [M][F] and the forward's gu [M][2F] -> dgu [M][2F] (bf16, or None), q/scale/inv (rowwise FP8 of the
+    gradient, or None) and h [M][F] (the forward's product again, or None)."""
+    import torch
+    fn, bf, f32 = "fp8_gated_bwd", torch.bfloat16, torch.float32
+    M, F = dh.shape
+    n = 2 * M * F
+    dev = _args(fn, ("dh", dh, n, bf), ("gu", gu, 2 * n, bf), ("dgu", dgu, dgu is not None and 2 * n, bf),
+                ("q", q, q is not None and n, 1), ("scale", scale, (q is not None or scale is not None) and 4 * M, f32),
+                ("inv_scale", inv_scale, inv_scale is not None and 4 * M, f32), ("h", h, h is not None and n, bf))
+    _launch(fn, dev, stream, _ptr(dh), _ptr(gu), M, F, act, fmt, eps, _ptr(dgu), _ptr(q), _ptr(scale),
+            _ptr(inv_scale), _ptr(h))
+
+
+# ---- optimizer --------------------------------------------------------------------------
+
+def _float_type(fn, name, t):
+    import torch
+    if t.dtype is torch.bfloat16:
+        return OUT_BF16
+    if t.dtype is torch.float32:
+        return OUT_F32
+    raise ValueError(f"{fn}: {name} must be bfloat16 or float32 (got {t.dtype})")
+
+
+def _scalar(fn, name, t, dtype, dev):
+    """Pointer of a one-element tensor of dtype on the device that the others are on, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() < 1 or not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be a {dtype} tensor of one element on the GPU")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on another GPU than the tensors")
+    return t.data_ptr()
+
+
+def fp8_adamw(params, grads, exp_avgs, exp_avg_sqs, lr, beta1, beta2, eps, weight_decay, step, exp_avg_scales=None,
+              exp_avg_sq_scales=None, masters=None, seed=0, grad_mul=None, step_dev=None, lr_dev=None, stream=None):
+    """One AdamW step over lists of tensors, changed in place: params and grads bf16 or fp32, exp_avgs and
+    exp_avg_sqs fp32, or e4m3 codes of the moments and of the second's square roots with exp_avg_scales and
+    exp_avg_sq_scales (uint8, one byte for 32 elements); masters: fp32 copies of bf16 params. step: this
+    step's number, from 1; seed: 0 rounds to nearest, else stochastically. grad_mul, lr_dev (fp32) and
+    step_dev (int32): one-element tensors on the device, or None. Elements go by their place in memory:
+    every tensor must be contiguous."""
+    import torch
+    fn, f32 = "fp8_adamw", torch.float32
+    count = len(params)
+    if count == 0:
+        return
+    first, g0 = params[0], grads[0]
+    p_type, g_type = _float_type(fn, "params", first), _float_type(fn, "grads", g0)
+    mx = exp_avgs[0].dtype is not f32
+    if mx and (exp_avg_scales is None or exp_avg_sq_scales is None):
+        raise ValueError(f"{fn}: 8-bit states need exp_avg_scales and exp_avg_sq_scales")
+    sdt = (1 if mx else f32)
+    lists = [("params", params, first.dtype, 1, 0), ("grads", grads, g0.dtype, 1, 0),
+             ("exp_avgs", exp_avgs, sdt, 1, 0), ("exp_avg_sqs", exp_avg_sqs, sdt, 1, 0)]
+    if mx:
+        lists += [("exp_avg_scales", exp_avg_scales, 1, 32, 31), ("exp_avg_sq_scales", exp_avg_sq_scales, 1, 32, 31)]
+    if masters is not None:
+        lists.append(("masters", masters, f32, 1, 0))
+    dev = first.get_device()
+    sizes = [p.numel() for p in params]
+    columns = []
+    for name, ts, dtype, per, up in lists:
+        if len(ts) != count:
+            raise ValueError(f"{fn}: {name} holds {len(ts)} tensors, params {count}")
+        for t, n in zip(ts, sizes):
+            kind = t.dtype is dtype or dtype == 1 and t.element_size() == 1
+            if not (kind and t.get_device() == dev >= 0 and t.numel() == (n + up) // per and t.is_contiguous()):
+                _args(fn, (name, t, None, dtype), (name, first, None, None))  # raises if it is one of these
+                raise ValueError(f"{fn}: {name} holds {t.numel()} elements for a parameter of {n}")
+        columns.append([t.data_ptr() for t in ts])
+    none = [0] * count
+    p, g, m, v = columns[:4]
+    ms, vs = columns[4:6] if mx else (none, none)
+    w = columns[-1] if masters is not None else none
+    table = (ctypes.c_int64 * (8 * count))(*[x for row in zip(p, g, m, v, ms, vs, w, sizes) for x in row])
+    _launch(fn, dev, stream, table, count, p_type, g_type, STATE_MX8 if mx else STATE_F32, lr, beta1, beta2, eps,
+            weight_decay, step, seed, _scalar(fn, "grad_mul", grad_mul, f32, dev),
+            _scalar(fn, "step_dev", step_dev, torch.int32, dev), _scalar(fn, "lr_dev", lr_dev, f32, dev))
+
+
+def _grad_table(fn, grads):
+    import torch
+    dev, rows = None, []
+    for g in grads:
+        if not g.is_contiguous() or not g.is_cuda or dev is not None and g.get_device() != dev:
+            raise ValueError(f"{fn}: grads must be contiguous tensors on one GPU")
+        dev = g.get_device()
+        rows += (g.data_ptr(), g.numel(), OUT_F32 if g.dtype is torch.float32 else _float_type(fn, "grads", g))
+    return (ctypes.c_int64 * max(1, len(rows)))(*rows), len(grads), dev
+
+
+def fp8_grad_norm_ws_bytes(grads) -> int:
+    table, count, _ = _grad_table("fp8_grad_norm_ws_bytes", grads)
+    return load().fp8_grad_norm_ws_bytes(table, count)
+
+
+def fp8_grad_norm(grads, norm, mul, ws, grad_scale=1.0, max_norm=float("inf"), step=None, stream=None):
+    """The 2-norm of a list of bf16 and fp32 tensors into norm [1], and into mul [1] the factor that clips them to
+    max_norm (fp8_adamw's grad_mul; NaN where the norm is not finite); step [1] int32 is increased by one where
+    it is finite. norm, mul and step may be None."""
+    import torch
+    fn = "fp8_grad_norm"
+    table, count, dev = _grad_table(fn, grads)
+    for t in (norm, mul, step):
+        dev = t.get_device() if dev is None and t is not None else dev
+    if ws is not None:
+        _args(fn, ("ws", ws, None, None))
+        if dev is not None and ws.get_device() != dev:
+            raise ValueError(f"{fn}: ws is on another GPU than the tensors")
+    _launch(fn, dev, stream, table, count, grad_scale, max_norm, _scalar(fn, "norm", norm, torch.float32, dev),
+            _scalar(fn, "mul", mul, torch.float32, dev), _scalar(fn, "step", step, torch.int32, dev), _ptr(ws),
+            0 if ws is None else ws.nbytes)
 
 
 # ---- Linear layer -----------------------------------------------------------------

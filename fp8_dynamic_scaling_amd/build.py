@@ -27,8 +27,9 @@ COMMON = [
 
 
 # Sources whose arithmetic is defined operation by operation (the quantizers and
-# the fused normalization): no multiply-add contraction, so a * b + c rounds twice.
-NO_CONTRACT = {"quant.hip": ["-ffp-contract=off"]}
+# the fused normalization, and the optimizer whose 8-bit states they round): no
+# multiply-add contraction, so a * b + c rounds twice.
+NO_CONTRACT = {"quant.hip": ["-ffp-contract=off"], "adamw.hip": ["-ffp-contract=off"]}
 
 
 def sources():

@@ -1,0 +1,518 @@
+// adamw.hip -- one AdamW step over many tensors, with 32-bit or 8-bit states, and the
+// gradients' norm with the factor that clips them.
+//
+// Per element, in fp32, each operation rounded by itself (this file is built without
+// multiply-add contraction, so that the 8-bit states' codes and scales are those of the
+// definition, bit for bit):
+//   g = g mul;  m = m b1 + g (1 - b1);  v = v b2 + (g g) (1 - b2);  r = sqrt(v)
+//   p = p (1 - lr wd) - (m / (r c2 + eps)) step
+//   step = lr / (1 - b1^t), c2 = 1 / sqrt(1 - b2^t), formed in 64 bits.
+// The quotient alone is a product with the reciprocal instruction (1 ulp).
+//
+// 8-bit states: m and r are kept as MXFP8, e4m3 codes with one power of two (E8M0) for
+// each 32 elements, the smallest with which the largest is at most 448. r and not v: its
+// codes span 2^18 in a group, which is 2^36 in v. A value of r above zero keeps a code
+// above zero, since m / (0 c2 + eps) would be a step of any size.
+// To nearest, a code of three mantissa bits stands still when a step changes its value by
+// less than 1/32 to 1/16 of it: with b2 = 0.999 r would never decay, and stop to grow
+// after some ten steps. Stochastic rounding (a seed other than 0) moves it by the right
+// amount in the mean: 16 random bits below the code's last place, from Wellons' 32-bit
+// integer hash "lowbias32" of (seed, tensor, step, element).
+#include <cmath>
+
+#include "../../include/fp8dyn.h"
+#include "common.hpp"
+#include "internal.hpp"
+
+namespace fp8dyn {
+
+namespace {
+
+typedef __bf16 aw_bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kTensorsALaunch = 48;  // their table travels in the kernel's arguments (4 KB)
+constexpr int kNormTensorsALaunch = 128;
+constexpr int kStepV4 = 256 * 4 * 2;      // elements of a workgroup, 32-bit states
+constexpr int kStepV8 = 256 * 8;          // and 8-bit states
+constexpr int64_t kNormChunk = 32768;     // elements of a workgroup of the norm
+
+struct StepTensor {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  uint8_t* ms;
+  uint8_t* vs;
+  float* master;
+  int64_t n;
+  uint32_t key;
+  uint32_t vec;  // every pointer allows the wide loads
+};
+struct StepArgs {
+  StepTensor t[kTensorsALaunch];
+  int32_t first[kTensorsALaunch + 1];  // chunks before each tensor
+  int32_t count;
+  float b1, c1, b2, c2m;  // c1 = 1 - b1, c2m = 1 - b2
+  float eps, decay, step, c2;
+  uint32_t now;  // the step's number for the random bits
+  const float* mul;
+  // where given: the step's number and rate on the device, from which the factors are formed there
+  const int32_t* step_dev;
+  const float* lr_dev;
+  double lr, wd, log_b1, log_b2;
+};
+static_assert(sizeof(StepArgs) <= 4096, "kernel arguments");
+
+struct NormArgs {
+  const void* g[kNormTensorsALaunch];
+  int64_t n[kNormTensorsALaunch];
+  int32_t first[kNormTensorsALaunch + 1];
+  uint32_t f32[(kNormTensorsALaunch + 31) / 32];
+  int32_t count;
+  double* part;
+};
+static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
+
+__host__ __device__ __forceinline__ uint32_t lowbias32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x7feb352du;
+  x ^= x >> 15;
+  x *= 0x846ca68bu;
+  x ^= x >> 16;
+  return x;
+}
+
+// the tensor of a chunk: the last one whose first chunk is not behind it
+template <class A>
+__device__ __forceinline__ int tensor_of(const A& a, int32_t chunk) {
+  int lo = 0, hi = a.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.first[mid] <= chunk) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// V consecutive values of an fp32 or bf16 array as fp32; `left` of them exist
+template <bool F32, int V>
+__device__ __forceinline__ void load_v(const void* base, int64_t i, bool wide, int left, float* x) {
+  if (wide) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const uint4 w = ld_nt16(reinterpret_cast<const float*>(base) + i + j);
+        x[j] = __uint_as_float(w.x), x[j + 1] = __uint_as_float(w.y);
+        x[j + 2] = __uint_as_float(w.z), x[j + 3] = __uint_as_float(w.w);
+      }
+    } else if constexpr (V == 8) {
+      const uint4 w = ld_nt16(reinterpret_cast<const uint16_t*>(base) + i);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[2 * j] = bf16_lo(u[j]), x[2 * j + 1] = bf16_hi(u[j]);
+    } else {
+      const u32x2 w =
+          __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(base) + i));
+      x[0] = bf16_lo(w[0]), x[1] = bf16_hi(w[0]), x[2] = bf16_lo(w[1]), x[3] = bf16_hi(w[1]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    x[j] = j >= left ? 0.0f
+           : F32     ? reinterpret_cast<const float*>(base)[i + j]
+                     : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(base)[i + j] << 16);
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const aw_bf16x2 h = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+template <bool F32, int V>
+__device__ __forceinline__ void store_v(void* base, int64_t i, bool wide, int left, const float* x) {
+  if (wide) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4)
+        st_nt16(reinterpret_cast<float*>(base) + i + j,
+                make_uint4(__float_as_uint(x[j]), __float_as_uint(x[j + 1]), __float_as_uint(x[j + 2]),
+                           __float_as_uint(x[j + 3])));
+    } else if constexpr (V == 8) {
+      st_nt16(reinterpret_cast<uint16_t*>(base) + i, make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]),
+                                                                bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])));
+    } else {
+      st_nt8(reinterpret_cast<uint16_t*>(base) + i, make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])));
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (j < left) {
+      if constexpr (F32)
+        reinterpret_cast<float*>(base)[i + j] = x[j];
+      else
+        reinterpret_cast<uint16_t*>(base)[i + j] = (uint16_t)bf16_pair(x[j], 0.0f);
+    }
+}
+
+// eight e4m3 codes times their group's power of two
+__device__ __forceinline__ void decode8(uint2 c, uint32_t e8, float* x) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  const float s = __uint_as_float(e8 << 23);
+  const v2f a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
+  const v2f d = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false), e = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
+  x[0] = a[0] * s, x[1] = a[1] * s, x[2] = b[0] * s, x[3] = b[1] * s;
+  x[4] = d[0] * s, x[5] = d[1] * s, x[6] = e[0] * s, x[7] = e[1] * s;
+}
+
+// the largest of a group's 32 magnitudes as bits (those of a NaN are above all others): a lane
+// holds 8, four neighbouring lanes the group
+__device__ __forceinline__ uint32_t group_top(const float* x) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = __float_as_uint(x[j]) & 0x7fffffffu;
+    t = b > t ? b : t;
+  }
+  uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)t, 0xB1, 0xf, 0xf, true);  // lanes 1 0 3 2
+  t = o > t ? o : t;
+  o = (uint32_t)__builtin_amdgcn_mov_dpp((int)t, 0x4E, 0xf, 0xf, true);  // lanes 2 3 0 1
+  return o > t ? o : t;
+}
+
+// MXFP8 of eight values of a group: codes and the group's E8M0 byte. SR: bits[j] holds 16 random
+// bits. LIFT: values are not negative, and one above zero keeps a code above zero.
+template <bool SR, bool LIFT>
+__device__ __forceinline__ uint2 encode8(const float* x, const uint32_t* bits, uint32_t& e8) {
+  const uint32_t top = group_top(x);
+  int e = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = e < 12 ? 12 : e;
+  const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    y[j] = x[j] * inv;
+    if constexpr (SR) {
+      // codes below 2^-6 are 2^-9 apart, as they are in the binade above it: 2^-6 is added there
+      const float a = fabsf(y[j]);
+      const float shift = a < 0x1p-6f ? 0x1p-6f : 0.0f;
+      const uint32_t t = (__float_as_uint(a + shift) + bits[j] * 16u + 8u) & ~0xfffffu;
+      y[j] = copysignf(__uint_as_float(t) - shift, y[j]);
+    }
+    if constexpr (LIFT) y[j] = x[j] > 0.0f && y[j] < 0x1p-9f ? 0x1p-9f : y[j];
+  }
+  uint2 c = make_uint2(cvt4<false>(y[0], y[1], y[2], y[3]), cvt4<false>(y[4], y[5], y[6], y[7]));
+  e8 = (uint32_t)e;
+  if (top >= 0x7f800000u) {  // not finite: the whole group stands for NaN
+    e8 = 255u;
+    c = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+  return c;
+}
+
+template <bool P32, bool G32, bool MASTER, bool EIGHT, bool SR>
+__global__ __launch_bounds__(256) void k_adamw(const StepArgs a) {
+  constexpr int V = EIGHT ? 8 : 4, U = EIGHT ? 1 : 2;
+  constexpr int CH = 256 * V * U;
+  float mul = 1.0f;
+  if (a.mul) {
+    mul = *a.mul;
+    if (!(fabsf(mul) <= 3.402823466e38f)) return;  // gradients that are not finite: no step
+  }
+  float step = a.step, c2 = a.c2, decay = a.decay;
+  uint32_t now = a.now;
+  if (a.step_dev || a.lr_dev) {
+    const double t = (double)(a.step_dev ? *a.step_dev : (int32_t)now);
+    const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
+    now = (uint32_t)(int32_t)t;
+    step = (float)(lr / -expm1(t * a.log_b1));
+    c2 = (float)(1.0 / sqrt(-expm1(t * a.log_b2)));
+    decay = (float)(1.0 - lr * a.wd);
+  }
+  const int32_t chunks = a.first[a.count];
+  for (int32_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+    const int k = tensor_of(a, chunk);
+    const StepTensor& T = a.t[k];
+    const int64_t n = T.n, begin = (int64_t)(chunk - a.first[k]) * CH;
+    const uint32_t key = SR ? lowbias32(T.key + now) : 0u;
+    float p[U][V], g[U][V], m[U][V], v[U][V];
+    uint2 cm = make_uint2(0, 0), cv = cm;
+    uint32_t em = 0, ev = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = begin + (int64_t)(u * 256 + threadIdx.x) * V;
+      const int left = n - i < V ? (int)(n - i) : V;
+      const bool wide = T.vec && left == V;
+      load_v<G32, V>(T.g, i, wide, left, g[u]);
+      if constexpr (MASTER)
+        load_v<true, V>(T.master, i, wide, left, p[u]);
+      else
+        load_v<P32, V>(T.p, i, wide, left, p[u]);
+      if constexpr (EIGHT) {
+        const uint8_t *qm = reinterpret_cast<const uint8_t*>(T.m) + i, *qv = reinterpret_cast<const uint8_t*>(T.v) + i;
+        if (wide) {
+          const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(qm));
+          const u32x2 y = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(qv));
+          cm = make_uint2(x[0], x[1]), cv = make_uint2(y[0], y[1]);
+        } else {
+          uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < left) {
+              w[j >> 2] |= (uint32_t)qm[j] << (8 * (j & 3));
+              w[2 + (j >> 2)] |= (uint32_t)qv[j] << (8 * (j & 3));
+            }
+          cm = make_uint2(w[0], w[1]), cv = make_uint2(w[2], w[3]);
+        }
+        if (left > 0) em = T.ms[i >> 5], ev = T.vs[i >> 5];
+      } else {
+        load_v<true, V>(T.m, i, wide, left, m[u]);
+        load_v<true, V>(T.v, i, wide, left, v[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = begin + (int64_t)(u * 256 + threadIdx.x) * V;
+      const int left = n - i < V ? (int)(n - i) : V;
+      const bool wide = T.vec && left == V;
+      float r[V];
+      if constexpr (EIGHT) {
+        decode8(cm, em, m[u]);
+        decode8(cv, ev, v[u]);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if constexpr (EIGHT) v[u][j] = v[u][j] * v[u][j];
+        const float x = a.mul ? g[u][j] * mul : g[u][j];
+        m[u][j] = m[u][j] * a.b1 + x * a.c1;
+        v[u][j] = v[u][j] * a.b2 + (x * x) * a.c2m;
+        r[j] = sqrtf(v[u][j]);
+        p[u][j] = p[u][j] * decay - (m[u][j] * __builtin_amdgcn_rcpf(r[j] * c2 + a.eps)) * step;
+      }
+      uint32_t lo[V], hi[V];
+      if constexpr (SR) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const uint32_t b = lowbias32((uint32_t)i + (uint32_t)j + key);
+          lo[j] = b & 0xffffu, hi[j] = b >> 16;
+        }
+      }
+      if constexpr (EIGHT) {
+        // lanes past the end hold zeros, and take no part in a group's largest
+        if (left < V) {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (j >= left) m[u][j] = r[j] = 0.0f;
+        }
+        cm = encode8<SR, false>(m[u], lo, em);
+        cv = encode8<SR, true>(r, hi, ev);
+        uint8_t *qm = reinterpret_cast<uint8_t*>(T.m) + i, *qv = reinterpret_cast<uint8_t*>(T.v) + i;
+        if (wide) {
+          st_nt8(qm, cm);
+          st_nt8(qv, cv);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < left) {
+              qm[j] = (uint8_t)((j < 4 ? cm.x : cm.y) >> (8 * (j & 3)));
+              qv[j] = (uint8_t)((j < 4 ? cv.x : cv.y) >> (8 * (j & 3)));
+            }
+        }
+        if ((threadIdx.x & 3) == 0 && left > 0) T.ms[i >> 5] = (uint8_t)em, T.vs[i >> 5] = (uint8_t)ev;
+      } else {
+        store_v<true, V>(T.m, i, wide, left, m[u]);
+        store_v<true, V>(T.v, i, wide, left, v[u]);
+      }
+      if constexpr (MASTER) store_v<true, V>(T.master, i, wide, left, p[u]);
+      if constexpr (SR && !P32 && !MASTER) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {  // bf16 with 16 random bits below its last place
+          const uint32_t b = __float_as_uint(p[u][j]);
+          if ((b & 0x7fffffffu) <= 0x7f800000u) p[u][j] = __uint_as_float((b + (lo[j] ^ hi[j])) & 0xffff0000u);
+        }
+      }
+      store_v<P32, V>(T.p, i, wide, left, p[u]);
+    }
+  }
+}
+
+// One partial sum of squares a workgroup, in 64 bits: a thread's elements in order, then a tree.
+__global__ __launch_bounds__(256) void k_grad_sq(const NormArgs a) {
+  __shared__ double red[4];
+  const int32_t chunks = a.first[a.count];
+  for (int32_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+    const int t = tensor_of(a, chunk);
+    const int64_t n = a.n[t], begin = (int64_t)(chunk - a.first[t]) * kNormChunk;
+    const int64_t end = begin + kNormChunk < n ? begin + kNormChunk : n;
+    const bool f32 = (a.f32[t >> 5] >> (t & 31)) & 1u;
+    const bool vec = ((uintptr_t)a.g[t] & 15) == 0;
+    double s = 0.0;
+    const int64_t whole = vec ? begin + ((end - begin) & ~(int64_t)7) : begin;
+    if (f32) {
+      const float* g = reinterpret_cast<const float*>(a.g[t]);
+      for (int64_t i = begin + 4 * threadIdx.x; i < whole; i += 4 * 256) {
+        const uint4 w = ld_nt16(g + i);
+        const double x0 = __uint_as_float(w.x), x1 = __uint_as_float(w.y);
+        const double x2 = __uint_as_float(w.z), x3 = __uint_as_float(w.w);
+        s += x0 * x0 + x1 * x1 + x2 * x2 + x3 * x3;
+      }
+      for (int64_t i = whole + threadIdx.x; i < end; i += 256) s += (double)g[i] * (double)g[i];
+    } else {
+      const uint16_t* g = reinterpret_cast<const uint16_t*>(a.g[t]);
+      for (int64_t i = begin + 8 * threadIdx.x; i < whole; i += 8 * 256) {
+        const uint4 w = ld_nt16(g + i);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const double x = bf16_lo(u[j]), y = bf16_hi(u[j]);
+          s += x * x + y * y;
+        }
+      }
+      for (int64_t i = whole + threadIdx.x; i < end; i += 256) {
+        const double x = __uint_as_float((uint32_t)g[i] << 16);
+        s += x * x;
+      }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) a.part[chunk] = (red[0] + red[1]) + (red[2] + red[3]);
+    __syncthreads();
+  }
+}
+
+__global__ __launch_bounds__(1024) void k_grad_norm(const double* __restrict__ part, int64_t n, double grad_scale,
+                                                    double max_norm, float* norm, float* mul, int32_t* step) {
+  __shared__ double red[16];
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = red[0];
+    for (int w = 1; w < 16; ++w) s += red[w];
+    const double x = sqrt(s) * fabs(grad_scale);
+    const float xf = (float)x;
+    if (norm) *norm = xf;
+    const bool fine = fabsf(xf) <= 3.402823466e38f;  // not for NaN
+    const double clip = max_norm / (x + 1e-6);
+    if (mul) *mul = fine ? (float)(clip < 1.0 ? grad_scale * clip : grad_scale) : __uint_as_float(0x7fc00000u);
+    if (step && fine) *step += 1;
+  }
+}
+
+template <bool P32, bool G32, bool MASTER>
+hipError_t launch_step(const StepArgs& s, bool eight, bool sr, unsigned grid, hipStream_t stream) {
+  if (eight) {
+    if (sr) hipLaunchKernelGGL((k_adamw<P32, G32, MASTER, true, true>), dim3(grid), dim3(256), 0, stream, s);
+    else hipLaunchKernelGGL((k_adamw<P32, G32, MASTER, true, false>), dim3(grid), dim3(256), 0, stream, s);
+  } else if constexpr (!P32 && !MASTER) {
+    if (sr) hipLaunchKernelGGL((k_adamw<P32, G32, MASTER, false, true>), dim3(grid), dim3(256), 0, stream, s);
+    else hipLaunchKernelGGL((k_adamw<P32, G32, MASTER, false, false>), dim3(grid), dim3(256), 0, stream, s);
+  } else {
+    hipLaunchKernelGGL((k_adamw<P32, G32, MASTER, false, false>), dim3(grid), dim3(256), 0, stream, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamwArgs& a) {
+  const int64_t ch = a.eight ? kStepV8 : kStepV4;
+  StepArgs s;
+  s.b1 = (float)a.beta1, s.c1 = (float)(1.0 - a.beta1);
+  s.b2 = (float)a.beta2, s.c2m = (float)(1.0 - a.beta2);
+  s.eps = (float)a.eps;
+  s.decay = (float)(1.0 - a.lr * a.wd);
+  s.step = (float)(a.lr / (1.0 - std::pow(a.beta1, (double)a.step)));
+  s.c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(a.beta2, (double)a.step)));
+  s.now = (uint32_t)a.step;
+  s.mul = a.mul, s.step_dev = a.step_dev, s.lr_dev = a.lr_dev;
+  s.lr = a.lr, s.wd = a.wd, s.log_b1 = std::log(a.beta1), s.log_b2 = std::log(a.beta2);
+  const uint32_t lo = (uint32_t)a.seed, hi = (uint32_t)(a.seed >> 32);
+  int64_t chunks = 0;
+  s.count = 0;
+  auto flush = [&]() -> hipError_t {
+    if (s.count == 0) return hipSuccess;
+    s.first[s.count] = (int32_t)chunks;
+    const unsigned grid = (unsigned)(chunks < kMaxGrid256 ? chunks : kMaxGrid256);
+    const bool sr = a.seed != 0;
+    hipError_t e;
+    if (a.p_f32)
+      e = a.g_f32 ? launch_step<true, true, false>(s, a.eight, sr, grid, a.stream)
+                  : launch_step<true, false, false>(s, a.eight, sr, grid, a.stream);
+    else if (a.master)
+      e = a.g_f32 ? launch_step<false, true, true>(s, a.eight, sr, grid, a.stream)
+                  : launch_step<false, false, true>(s, a.eight, sr, grid, a.stream);
+    else
+      e = a.g_f32 ? launch_step<false, true, false>(s, a.eight, sr, grid, a.stream)
+                  : launch_step<false, false, false>(s, a.eight, sr, grid, a.stream);
+    s.count = 0;
+    chunks = 0;
+    return e;
+  };
+  for (int32_t i = 0; i < a.count; ++i) {
+    const fp8_adamw_tensor& t = a.tensors[i];
+    if (t.n == 0) continue;
+    const int64_t c = (t.n + ch - 1) / ch;
+    if (s.count == kTensorsALaunch || chunks + c > INT32_MAX) {
+      const hipError_t e = flush();
+      if (e != hipSuccess) return e;
+    }
+    const uintptr_t all = (uintptr_t)t.p | (uintptr_t)t.g | (uintptr_t)t.m | (uintptr_t)t.v | (uintptr_t)t.master;
+    s.first[s.count] = (int32_t)chunks;
+    s.t[s.count++] = {t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.master, t.n,
+                      lowbias32(hi ^ lowbias32(lo ^ lowbias32((uint32_t)i))),
+                      (all & 15) == 0 ? 1u : 0u};
+    chunks += c;
+  }
+  return flush();
+}
+
+int64_t grad_norm_partials(const fp8_grad_tensor* tensors, int32_t count) {
+  int64_t chunks = 0;
+  for (int32_t i = 0; i < count; ++i) chunks += (tensors[i].n + kNormChunk - 1) / kNormChunk;
+  return chunks;
+}
+
+hipError_t launch_grad_norm(const GradNormArgs& a) {
+  NormArgs s;
+  int64_t chunks = 0, before = 0;
+  s.count = 0;
+  auto flush = [&]() -> hipError_t {
+    if (s.count == 0) return hipSuccess;
+    s.first[s.count] = (int32_t)chunks;
+    s.part = a.ws + before;
+    const unsigned grid = (unsigned)(chunks < kMaxGrid256 ? chunks : kMaxGrid256);
+    hipLaunchKernelGGL(k_grad_sq, dim3(grid), dim3(256), 0, a.stream, s);
+    before += chunks;
+    s.count = 0;
+    chunks = 0;
+    return hipGetLastError();
+  };
+  for (int32_t i = 0; i < a.count; ++i) {
+    const fp8_grad_tensor& t = a.tensors[i];
+    if (t.n == 0) continue;
+    const int64_t c = (t.n + kNormChunk - 1) / kNormChunk;
+    if (s.count == kNormTensorsALaunch || chunks + c > INT32_MAX) {
+      const hipError_t e = flush();
+      if (e != hipSuccess) return e;
+    }
+    if (s.count % 32 == 0) s.f32[s.count / 32] = 0;
+    s.f32[s.count / 32] |= (t.type == FP8_OUT_F32 ? 1u : 0u) << (s.count % 32);
+    s.g[s.count] = t.g;
+    s.n[s.count] = t.n;
+    s.first[s.count++] = (int32_t)chunks;
+    chunks += c;
+  }
+  const hipError_t e = flush();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_grad_norm, dim3(1), dim3(1024), 0, a.stream, a.ws, before, a.grad_scale, a.max_norm, a.norm,
+                     a.mul, a.step);
+  return hipGetLastError();
+}
+
+}  // namespace fp8dyn

@@ -684,6 +684,159 @@ fp8_status fp8_moe_few(const uint16_t* x, const int32_t* ids, const float* weigh
   return dev_err(launch_moe_few(a));
 }
 
+static fp8_status check_gated(const void* a, const void* b, const void* sa, const void* sb, int64_t M, int64_t F,
+                              int64_t K, fp8_act act, int packed, const void* gu, const void* out) {
+  if (M < 0 || F < 0 || K < 0) return FP8_ERR_INVALID_ARGUMENT;
+  if (act != FP8_ACT_SILU && act != FP8_ACT_GELU_TANH) return FP8_ERR_INVALID_ARGUMENT;
+  if (M == 0 || F == 0) return FP8_OK;
+  if (M > INT32_MAX || F >= (1 << 30)) return FP8_ERR_UNSUPPORTED;
+  if (!out) return FP8_ERR_INVALID_ARGUMENT;
+  if (K > 0 && (!a || !b || !sa || !sb)) return FP8_ERR_INVALID_ARGUMENT;
+  if (K % 16 != 0 || (packed && (F % 16 != 0 || K % 128 != 0))) return FP8_ERR_ALIGNMENT;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sa, 4) || !aligned(sb, 4) || !aligned(gu, 2) || !aligned(out, 2))
+    return FP8_ERR_ALIGNMENT;
+  return FP8_OK;
+}
+
+// e4m3 of the native variant, as both operands of a gated product have it
+static fp8_status resolve_e4m3(fp8_format fmt) {
+  bool e5;
+  double fm;
+  const fp8_status st = resolve(fmt, &e5, &fm);
+  return st != FP8_OK ? st : e5 ? FP8_ERR_UNSUPPORTED : FP8_OK;
+}
+
+static fp8_status run_gated(const GatedMmArgs& g) {
+  if (g.K == 0) {  // no contraction terms: act(0) * 0
+    const fp8_status st = dev_err(launch_zero_fill(g.out, g.M * g.F * 2, g.stream));
+    return st != FP8_OK || !g.gu ? st : dev_err(launch_zero_fill(g.gu, g.M * g.F * 4, g.stream));
+  }
+  return dev_err(launch_gated_mm(g));
+}
+
+fp8_status fp8_gated_mm(const uint8_t* a, const uint8_t* b, fp8_format fmt, fp8_scaling scaling, const float* a_inv,
+                        const float* b_inv, int64_t M, int64_t F, int64_t K, fp8_act act, int packed, uint16_t* gu,
+                        uint16_t* out, int use_fast_accum, void* stream) {
+  if (scaling != FP8_SCALE_TENSOR && scaling != FP8_SCALE_ROW) return FP8_ERR_UNSUPPORTED;
+  fp8_status st = check_gated(a, b, a_inv, b_inv, M, F, K, act, packed, gu, out);
+  if (st != FP8_OK || M == 0 || F == 0) return st;
+  GatedMmArgs g{a, b, a_inv, b_inv, nullptr, 1, M, F, K, scaling == FP8_SCALE_ROW, packed != 0,
+                act == FP8_ACT_GELU_TANH, !use_fast_accum, gu, out, (hipStream_t)stream};
+  if (packed && K > 0 && !gated_mm_packed_ok(g)) return FP8_ERR_UNSUPPORTED;
+  if ((st = resolve_e4m3(fmt)) != FP8_OK) return st;
+  return run_gated(g);
+}
+
+fp8_status fp8_grouped_gated_mm(const uint8_t* a, const uint8_t* b, fp8_format fmt, const float* a_inv,
+                                const float* b_inv, const int32_t* offsets, int32_t E, int64_t Mtot, int64_t F,
+                                int64_t K, fp8_act act, int packed, uint16_t* gu, uint16_t* out, int use_fast_accum,
+                                void* stream) {
+  if (E < 1 || E > 1024) return FP8_ERR_INVALID_ARGUMENT;
+  fp8_status st = check_gated(a, b, a_inv, b_inv, Mtot, F, K, act, packed, gu, out);
+  if (st != FP8_OK || Mtot == 0 || F == 0) return st;
+  if (!offsets) return FP8_ERR_INVALID_ARGUMENT;
+  if (!aligned(offsets, 4) || (packed && Mtot % 2 != 0)) return FP8_ERR_ALIGNMENT;
+  GatedMmArgs g{a, b, a_inv, b_inv, offsets, E, Mtot, F, K, true, packed != 0, act == FP8_ACT_GELU_TANH,
+                !use_fast_accum, gu, out, (hipStream_t)stream};
+  if (packed && K > 0 && !gated_mm_packed_ok(g)) return FP8_ERR_UNSUPPORTED;
+  if ((st = resolve_e4m3(fmt)) != FP8_OK) return st;
+  return run_gated(g);
+}
+
+fp8_status fp8_gated_bwd(const uint16_t* dh, const uint16_t* gu, int64_t M, int64_t F, fp8_act act, fp8_format fmt,
+                         double eps, uint16_t* dgu, uint8_t* q, float* scale, float* inv_scale, uint16_t* h,
+                         void* stream) {
+  if (M < 0 || F < 0 || bad_eps(eps)) return FP8_ERR_INVALID_ARGUMENT;
+  if (act != FP8_ACT_SILU && act != FP8_ACT_GELU_TANH) return FP8_ERR_INVALID_ARGUMENT;
+  if (inv_scale && !scale) return FP8_ERR_INVALID_ARGUMENT;
+  if (!aligned(scale, 4) || !aligned(inv_scale, 4)) return FP8_ERR_ALIGNMENT;
+  if (M == 0) return FP8_OK;
+  if (F == 0) return empty_group_scales(fmt, false, eps, scale, inv_scale, scale ? M : 0, stream);
+  if (!dh || !gu || (!dgu && !q && !h) || (!q != !scale)) return FP8_ERR_INVALID_ARGUMENT;
+  if (F % 8 != 0) return FP8_ERR_ALIGNMENT;
+  if (F > kMaxGatedF) return FP8_ERR_UNSUPPORTED;
+  if (!aligned(dh, 16) || !aligned(gu, 16) || !aligned(dgu, 16) || !aligned(h, 16) || !aligned(q, 8))
+    return FP8_ERR_ALIGNMENT;
+  bool e5;
+  double fm;
+  fp8_status st;
+  if ((st = resolve(fmt, &e5, &fm)) != FP8_OK) return st;
+  GatedBwdArgs g{dh, gu, M, F, act == FP8_ACT_GELU_TANH, e5, fm, eps, dgu, q, scale, inv_scale, h,
+                 (hipStream_t)stream};
+  return dev_err(launch_gated_bwd(g));
+}
+
+static bool bad_factor(double x) { return !(std::isfinite(x) && x >= 0.0); }
+
+fp8_status fp8_adamw(const fp8_adamw_tensor* tensors, int32_t count, fp8_out param_type, fp8_out grad_type,
+                     fp8_adamw_state state, double lr, double beta1, double beta2, double eps, double weight_decay,
+                     int64_t step, uint64_t seed, const float* grad_mul, const int32_t* step_dev, const float* lr_dev,
+                     void* stream) {
+  if (count < 0 || (count > 0 && !tensors)) return FP8_ERR_INVALID_ARGUMENT;
+  if ((param_type != FP8_OUT_BF16 && param_type != FP8_OUT_F32) ||
+      (grad_type != FP8_OUT_BF16 && grad_type != FP8_OUT_F32) || (state != FP8_STATE_F32 && state != FP8_STATE_MX8))
+    return FP8_ERR_INVALID_ARGUMENT;
+  if ((!lr_dev && bad_factor(lr)) || bad_factor(beta1) || bad_factor(beta2) || bad_factor(eps) ||
+      bad_factor(weight_decay) || beta1 >= 1.0 || beta2 >= 1.0 || (!step_dev && step < 1))
+    return FP8_ERR_INVALID_ARGUMENT;
+  if (!aligned(grad_mul, 4) || !aligned(step_dev, 4) || !aligned(lr_dev, 4)) return FP8_ERR_ALIGNMENT;
+  const bool mx = state == FP8_STATE_MX8;
+  const size_t ps = param_type == FP8_OUT_F32 ? 4 : 2, gs = grad_type == FP8_OUT_F32 ? 4 : 2, ss = mx ? 1 : 4;
+  int master = -1;  // of all tensors with elements, or of none
+  for (int32_t i = 0; i < count; ++i) {
+    const fp8_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return FP8_ERR_INVALID_ARGUMENT;
+    if (t.n == 0) continue;
+    if (!t.p || !t.g || !t.m || !t.v || (mx && (!t.m_scale || !t.v_scale))) return FP8_ERR_INVALID_ARGUMENT;
+    if (master < 0) master = t.master != nullptr;
+    if (master != (t.master != nullptr)) return FP8_ERR_INVALID_ARGUMENT;
+    if (!aligned(t.p, ps) || !aligned(t.g, gs) || !aligned(t.m, ss) || !aligned(t.v, ss) || !aligned(t.master, 4))
+      return FP8_ERR_ALIGNMENT;
+  }
+  if (master < 0) return FP8_OK;
+  if (master && param_type == FP8_OUT_F32) return FP8_ERR_INVALID_ARGUMENT;
+  if (mx) {
+    const fp8_status st = resolve_e4m3(FP8_E4M3FN);  // the variant of the codes
+    if (st != FP8_OK) return st;
+  }
+  AdamwArgs a{tensors, count, param_type == FP8_OUT_F32, grad_type == FP8_OUT_F32, mx, master == 1, lr, beta1, beta2,
+              eps, weight_decay, step, seed, grad_mul, step_dev, lr_dev, (hipStream_t)stream};
+  return dev_err(launch_adamw(a));
+}
+
+static fp8_status check_grads(const fp8_grad_tensor* tensors, int32_t count) {
+  if (count < 0 || (count > 0 && !tensors)) return FP8_ERR_INVALID_ARGUMENT;
+  for (int32_t i = 0; i < count; ++i) {
+    const fp8_grad_tensor& t = tensors[i];
+    if (t.n < 0 || (t.type != FP8_OUT_BF16 && t.type != FP8_OUT_F32) || (t.n > 0 && !t.g))
+      return FP8_ERR_INVALID_ARGUMENT;
+    if (t.n > 0 && !aligned(t.g, t.type == FP8_OUT_F32 ? 4 : 2)) return FP8_ERR_ALIGNMENT;
+  }
+  return FP8_OK;
+}
+
+size_t fp8_grad_norm_ws_bytes(const fp8_grad_tensor* tensors, int32_t count) {
+  for (int32_t i = 0; i < count; ++i)
+    if (!tensors || tensors[i].n < 0) return 0;
+  return (size_t)grad_norm_partials(tensors, count) * 8;
+}
+
+fp8_status fp8_grad_norm(const fp8_grad_tensor* tensors, int32_t count, double grad_scale, double max_norm,
+                         float* norm, float* mul, int32_t* step, void* ws, size_t ws_bytes, void* stream) {
+  if (bad_factor(grad_scale) || grad_scale == 0.0 || !(max_norm > 0.0)) return FP8_ERR_INVALID_ARGUMENT;
+  fp8_status st = check_grads(tensors, count);
+  if (st != FP8_OK) return st;
+  if (!norm && !mul && !step) return FP8_ERR_INVALID_ARGUMENT;
+  if (!aligned(norm, 4) || !aligned(mul, 4) || !aligned(step, 4)) return FP8_ERR_ALIGNMENT;
+  const size_t need = fp8_grad_norm_ws_bytes(tensors, count);
+  if (need > 0) {
+    if (!ws || ws_bytes < need) return FP8_ERR_WORKSPACE;
+    if (!aligned(ws, 8)) return FP8_ERR_ALIGNMENT;
+  }
+  GradNormArgs a{tensors, count, grad_scale, max_norm, norm, mul, step, (double*)ws, (hipStream_t)stream};
+  return dev_err(launch_grad_norm(a));
+}
+
 fp8_status fp8_validate_offsets(const int32_t* host_offsets, int32_t E, int64_t Mtot) {
   if (!host_offsets || E < 1 || Mtot < 0) return FP8_ERR_INVALID_ARGUMENT;
   if (host_offsets[0] != 0 || host_offsets[E] != Mtot) return FP8_ERR_INVALID_ARGUMENT;

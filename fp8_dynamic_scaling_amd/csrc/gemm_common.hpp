@@ -67,6 +67,9 @@ __device__ __forceinline__ v8bf bf16x8_scaled(const v8i& f, int q, float scale) 
   return (v8bf){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
+// Gated products: the activation of the gate, a template parameter of the GEMM kernels.
+enum GateAct : int { kGateNone = 0, kGateSilu = 1, kGateGelu = 2 };
+
 constexpr int kMaxExperts = 1024;
 constexpr int kGroupM = 4;
 constexpr int kNumXcd = 8;
@@ -80,6 +83,7 @@ struct GemmParams {
   int32_t E;
   int64_t M, N, K;
   void* out;
+  uint16_t* gu = nullptr;  // gated products: both projections, or nullptr
 };
 
 // Tile bookkeeping shared by the workgroup.

@@ -7,6 +7,9 @@
 #include <stdint.h>
 #include <stddef.h>
 
+struct fp8_adamw_tensor;  // include/fp8dyn.h
+struct fp8_grad_tensor;
+
 namespace fp8dyn {
 
 struct QuantArgs {
@@ -139,6 +142,53 @@ struct MoeFewArgs {
 hipError_t launch_moe_few(const MoeFewArgs& a);  // F > 0
 size_t moe_few_ws_bytes(int64_t T, int k, int64_t F);
 
+// One AdamW step over many tensors (adamw.hip).
+struct AdamwArgs {
+  const fp8_adamw_tensor* tensors;  // host
+  int32_t count;
+  bool p_f32, g_f32, eight, master;
+  double lr, beta1, beta2, eps, wd;
+  int64_t step;
+  uint64_t seed;
+  const float* mul;         // device, or nullptr
+  const int32_t* step_dev;  // device, or nullptr: instead of step
+  const float* lr_dev;      // device, or nullptr: instead of lr
+  hipStream_t stream;
+};
+hipError_t launch_adamw(const AdamwArgs& a);
+
+// The gradients' norm and the factor that clips them (adamw.hip).
+struct GradNormArgs {
+  const fp8_grad_tensor* tensors;  // host
+  int32_t count;
+  double grad_scale, max_norm;
+  float* norm;
+  float* mul;
+  int32_t* step;
+  double* ws;  // grad_norm_partials()
+  hipStream_t stream;
+};
+hipError_t launch_grad_norm(const GradNormArgs& a);
+int64_t grad_norm_partials(const fp8_grad_tensor* tensors, int32_t count);
+
+// Gradient through a gated product with its rowwise quantization (gated_bwd.hip).
+struct GatedBwdArgs {
+  const uint16_t* dh;  // [M][F]
+  const uint16_t* gu;  // [M][2F]: gate, then up
+  int64_t M, F;        // F % 8 == 0, F <= kMaxGatedF
+  bool gelu;
+  bool e5;
+  double fmax, eps;
+  uint16_t* dgu;       // [M][2F] or nullptr; may be gu
+  uint8_t* q;          // [M][2F] or nullptr (then no scales)
+  float* scale;
+  float* inv;          // or nullptr
+  uint16_t* h;         // [M][F] or nullptr; may be dh
+  hipStream_t stream;
+};
+constexpr int64_t kMaxGatedF = 32768;  // a row's gradient lives in registers
+hipError_t launch_gated_bwd(const GatedBwdArgs& a);
+
 // Tensorwise quantization of up to kMaxTJobs tensors in three launches (clear
 // the amax words, amax of every tensor, one cast launch): each tensor gets its
 // transposed output qT [cols][rows] and, when q is set, its row-major output
@@ -205,6 +255,27 @@ bool gemm_fp8_fast_eligible(const GemmArgs& g);
 // of the generic kernel (at most one tile per CU)
 bool gemm_fp8_small_dense(int64_t M, int64_t N);
 hipError_t launch_gemm_fp8_fast(const GemmArgs& g);
+
+// Gated product (gemm_gated.hip): b holds [E][2F][K], gate rows before up rows; out [M][F] bf16.
+struct GatedMmArgs {
+  const uint8_t* a;        // [M][K] e4m3; packed and grouped: pair-interleaved
+  const uint8_t* b;        // packed: k-packed
+  const float* sa;         // [M], or one
+  const float* sb;         // [E][2F], or one
+  const int32_t* offsets;  // device [E + 1], or nullptr for a dense problem (E == 1)
+  int32_t E;
+  int64_t M, F, K;
+  bool row_scales;         // else one scale each
+  bool packed;
+  bool gelu;
+  bool exact;              // full-precision accumulation
+  uint16_t* gu;            // [M][2F], or nullptr
+  uint16_t* out;
+  hipStream_t stream;
+};
+hipError_t launch_gated_mm(const GatedMmArgs& g);
+// a shape that the packed form takes (the caller has checked its alignment)
+bool gated_mm_packed_ok(const GatedMmArgs& g);
 
 struct WgradArgs {
   const uint16_t* gy;  // [M][N]

@@ -119,6 +119,12 @@ typedef enum {
     FP8_GATE_SIGMOID = 2       /* sigmoid of each chosen logit */
 } fp8_gate;
 
+/* The gate of a gated product (fp8_gated_mm): act(x) = x * sigmoid(z). */
+typedef enum {
+    FP8_ACT_SILU = 0,     /* z = x */
+    FP8_ACT_GELU_TANH = 1 /* z = sqrt(8 / pi) * (x + 0.044715 x^3): GELU in its tanh form */
+} fp8_act;
+
 /* ---- device facts -------------------------------------------------------- */
 
 /* Measures, on `device`, which e4m3 and e5m2 variants the hardware FP8
@@ -408,6 +414,52 @@ FP8DYN_API fp8_status fp8_grouped_mm_kpacked(const uint8_t* a, fp8_format fa, co
                                              int64_t K, fp8_out out_type, void* out, int use_fast_accum,
                                              void* stream);
 
+/* ---- gated feed-forward block ------------------------------------------------------
+ * The first half of a gated MLP, h = act(x Wg^T) * (x Wu^T), both projections, the
+ * activation and the product in one FP8 GEMM, and its backward. Around them:
+ * fp8_quant_row (x, the weights [2F][K], h), fp8_scaled_mm for the down projection and
+ * for the gradient of x (the codes of fp8_gated_bwd times the weights' columns),
+ * fp8_wgrad_bf16 for those of the weights; or their grouped forms. */
+
+/* out[m][f] = act(g) * u, g = a_inv[m] * b_inv[f] * sum_k a[m][k] b[f][k], u the same of
+ * row F + f of b. a [M][K], b [2F][K]: e4m3 codes (fmt the native variant), gate rows
+ * before up rows; scaling ROW (a_inv [M], b_inv [2F]) or TENSOR (one each). g, u and the
+ * activation are fp32; out [M][F] and, if gu is not NULL, gu [M][2F] = [g | u] (what
+ * fp8_gated_bwd takes) are rounded to bf16 once. act is computed as x / (1 + exp(-z)) in
+ * IEEE arithmetic: -inf gives NaN. packed nonzero: b k-packed as fp8_quant_row_kpacked
+ * writes it, F % 16 == 0 and K % 128 == 0 (else FP8_ERR_ALIGNMENT), 2F <= 2^22,
+ * K <= 2^22 and 2F * K < 2^31 (else FP8_ERR_UNSUPPORTED). K % 16 == 0; M < 2^31, F < 2^30
+ * (else FP8_ERR_UNSUPPORTED). use_fast_accum as for fp8_scaled_mm. K = 0 writes zeros. */
+FP8DYN_API fp8_status fp8_gated_mm(const uint8_t* a, const uint8_t* b, fp8_format fmt, fp8_scaling scaling,
+                                   const float* a_inv, const float* b_inv, int64_t M, int64_t F, int64_t K,
+                                   fp8_act act, int packed, uint16_t* gu, uint16_t* out, int use_fast_accum,
+                                   void* stream);
+
+/* fp8_gated_mm of the rows of each expert, as fp8_grouped_mm: rows [offsets[e],
+ * offsets[e+1]) of a with b[e] ([E][2F][K]) and b_inv [E][2F]; ROW scaling. packed nonzero:
+ * a pair-interleaved and b k-packed as for fp8_grouped_mm_kpacked (Mtot % 2 == 0 too).
+ * Rows behind offsets[E] are neither used nor written. */
+FP8DYN_API fp8_status fp8_grouped_gated_mm(const uint8_t* a, const uint8_t* b, fp8_format fmt, const float* a_inv,
+                                           const float* b_inv, const int32_t* offsets, int32_t E, int64_t Mtot,
+                                           int64_t F, int64_t K, fp8_act act, int packed, uint16_t* gu,
+                                           uint16_t* out, int use_fast_accum, void* stream);
+
+/* Backward of the gate. dh [M][F]: the gradient of out; gu [M][2F]: the forward's. Per row
+ * d = [dh * u * act'(g) | dh * act(g)], 2F values in fp32, then
+ *   dgu [M][2F] = bf16(d) (the weights' gradient takes it), if not NULL;
+ *   q [M][2F], scale, inv_scale [M]: the row's codes as fp8_quant_row forms them, but of the
+ *   fp32 d, if q is not NULL (inv_scale may be NULL; without q scale must be too). A row
+ *   that is not finite has NaN scales, so that its codes stand for NaN;
+ *   h [M][F] = bf16(act(g) * u), the forward's out but for the projections' rounding, if
+ *   not NULL (the down projection's weight gradient, where out was not kept).
+ * At least one of dgu, q and h. dgu may be gu and h may be dh; otherwise outputs overlap
+ * no input. F % 8 == 0 and 16-byte aligned dh, gu, dgu, h, 8-byte aligned q (else
+ * FP8_ERR_ALIGNMENT); F <= 32768 (else FP8_ERR_UNSUPPORTED). F = 0 writes the scales of
+ * empty rows. eps as for the quantizers; fmt a native variant. */
+FP8DYN_API fp8_status fp8_gated_bwd(const uint16_t* dh, const uint16_t* gu, int64_t M, int64_t F, fp8_act act,
+                                    fp8_format fmt, double eps, uint16_t* dgu, uint8_t* q, float* scale,
+                                    float* inv_scale, uint16_t* h, void* stream);
+
 /* BF16 weight-gradient GEMM [P-AMD Figure 1 caption: the weight-update GEMM
  * stays in BF16]: gw[n][k] = sum_m gy[m][n] * x[m][k], fp32 accumulation,
  * bf16 out. gy [M][N], x [M][K], gw [N][K], all bf16 row-major; no
@@ -538,6 +590,73 @@ FP8DYN_API fp8_status fp8_linear_bwd(const uint16_t* gy, const uint16_t* x, cons
                                      uint16_t* gx, uint16_t* gw, void* ws, size_t ws_bytes,
                                      void* stream);
 FP8DYN_API size_t fp8_linear_ws_bytes(int64_t M, int64_t N, int64_t K, fp8_recipe recipe);
+
+/* ---- optimizer ---------------------------------------------------------------------
+ * The tables of tensors are HOST arrays, read before the call returns; what they point to
+ * is device memory. Captured into a graph, a call keeps the table's pointers. */
+
+/* One tensor of an AdamW step: n consecutive elements. */
+typedef struct fp8_adamw_tensor {
+    void* p;          /* parameters, bf16 or fp32 */
+    const void* g;    /* gradients, bf16 or fp32 */
+    void* m;          /* first moments: fp32, or e4m3 codes */
+    void* v;          /* second moments in fp32, or e4m3 codes of their square roots */
+    uint8_t* m_scale; /* 8-bit states: one E8M0 byte for each 32 elements, the last may be fewer */
+    uint8_t* v_scale;
+    float* master;    /* fp32 copy of bf16 parameters, which is then what is updated, or NULL */
+    int64_t n;
+} fp8_adamw_tensor;
+
+typedef enum {
+    FP8_STATE_F32 = 0, /* m and v in fp32 */
+    FP8_STATE_MX8 = 1  /* m and sqrt(v) as MXFP8: e4m3 codes, a power of two for each 32 */
+} fp8_adamw_state;
+
+/* One AdamW step over `count` tensors. Per element in fp32, each operation rounded by
+ * itself, t the number of this step (1 for the first):
+ *   g = g * mul (if grad_mul is not NULL)
+ *   m = m * beta1 + g * (1 - beta1);  v = v * beta2 + (g * g) * (1 - beta2);  r = sqrt(v)
+ *   p = p * (1 - lr * weight_decay) - (m / (r / sqrt(1 - beta2^t) + eps)) * (lr / (1 - beta1^t))
+ * (factors of one step are formed in 64 bits and rounded; the divisions by r's factor and by
+ * the sum are products with a reciprocal). All tensors of a call share param_type, grad_type
+ * and state; all or none have a master (bf16 parameters only).
+ * FP8_STATE_MX8 keeps m and r as e4m3 codes with one E8M0 byte for 32 elements, the smallest
+ * power of two (at least 2^-115) with which the largest is at most 448. r's code of a value
+ * above zero is at least the smallest. A group that is not finite has byte 255 and NaN codes.
+ * Zeroed codes and bytes are the states before the first step.
+ * seed: 0 rounds codes, and bf16 parameters without a master, to nearest. Any other value
+ * rounds them stochastically: with 16 bits below the last place from a hash of seed, the
+ * tensor's place in the table, t and the element's place (its low 32 bits). Needed where a
+ * step changes a value by less than half its last place, as beta2 near 1 does to 8-bit states.
+ * grad_mul: device fp32, or NULL. If it is not finite, the call changes nothing.
+ * step_dev, lr_dev: device int32 and fp32, or NULL: t and lr are read there when the kernels
+ * run (for graphs); step and lr are then not used.
+ * betas in [0, 1), eps, lr and weight_decay finite and >= 0, step >= 1 unless step_dev. Every
+ * pointer aligned to its elements (else FP8_ERR_ALIGNMENT); 16-byte aligned ones are faster.
+ * One launch for each 48 tensors. Tensors that overlap are not detected. */
+FP8DYN_API fp8_status fp8_adamw(const fp8_adamw_tensor* tensors, int32_t count, fp8_out param_type,
+                                fp8_out grad_type, fp8_adamw_state state, double lr, double beta1, double beta2,
+                                double eps, double weight_decay, int64_t step, uint64_t seed, const float* grad_mul,
+                                const int32_t* step_dev, const float* lr_dev, void* stream);
+
+/* One tensor of fp8_grad_norm. */
+typedef struct fp8_grad_tensor {
+    const void* g;
+    int64_t n;
+    int32_t type; /* fp8_out: bf16 or fp32 */
+} fp8_grad_tensor;
+
+/* norm = grad_scale * sqrt(sum of squares of all elements), summed in 64 bits in a fixed order;
+ * mul = grad_scale * min(1, max_norm / (norm + 1e-6)), the factor that fp8_adamw takes: NaN if the
+ * norm is not finite, which skips that step; *step is increased by one if it is finite. norm, mul
+ * [1] fp32 and step [1] int32 on the device, each may be NULL. grad_scale (what undoes a loss
+ * scale; 1 for none) finite and > 0; max_norm > 0, infinity for no clipping. ws:
+ * fp8_grad_norm_ws_bytes() bytes, 8-byte aligned, content on entry of no matter; calls that may run
+ * at the same time need one each. count = 0 is the norm 0. */
+FP8DYN_API fp8_status fp8_grad_norm(const fp8_grad_tensor* tensors, int32_t count, double grad_scale,
+                                    double max_norm, float* norm, float* mul, int32_t* step, void* ws,
+                                    size_t ws_bytes, void* stream);
+FP8DYN_API size_t fp8_grad_norm_ws_bytes(const fp8_grad_tensor* tensors, int32_t count);
 
 /* Host helper: checks a HOST copy of an offsets array (offsets[0] == 0,
  * non-decreasing, offsets[E] == Mtot). */
