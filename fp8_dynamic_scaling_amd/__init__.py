@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
+from itertools import chain
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8dyn.so")
@@ -708,54 +710,70 @@ def fp8_adamw(params, grads, exp_avgs, exp_avg_sqs, lr, beta1, beta2, eps, weigh
     count = len(params)
     if count == 0:
         return
-    first, g0 = params[0], grads[0]
-    p_type, g_type = _float_type(fn, "params", first), _float_type(fn, "grads", g0)
+    T, p_dt, g_dt = torch.Tensor, params[0].dtype, grads[0].dtype
+    p_type, g_type = _float_type(fn, "params", params[0]), _float_type(fn, "grads", grads[0])
     mx = exp_avgs[0].dtype is not f32
     if mx and (exp_avg_scales is None or exp_avg_sq_scales is None):
         raise ValueError(f"{fn}: 8-bit states need exp_avg_scales and exp_avg_sq_scales")
-    sdt = (1 if mx else f32)
-    lists = [("params", params, first.dtype, 1, 0), ("grads", grads, g0.dtype, 1, 0),
-             ("exp_avgs", exp_avgs, sdt, 1, 0), ("exp_avg_sqs", exp_avg_sqs, sdt, 1, 0)]
+    state = 1 if mx else f32
+    sizes = list(map(T.numel, params))
+    lists = [("params", params, p_dt, sizes), ("grads", grads, g_dt, sizes), ("exp_avgs", exp_avgs, state, sizes),
+             ("exp_avg_sqs", exp_avg_sqs, state, sizes)]
     if mx:
-        lists += [("exp_avg_scales", exp_avg_scales, 1, 32, 31), ("exp_avg_sq_scales", exp_avg_sq_scales, 1, 32, 31)]
+        groups = [(n + 31) >> 5 for n in sizes]
+        lists += [("exp_avg_scales", exp_avg_scales, 1, groups), ("exp_avg_sq_scales", exp_avg_sq_scales, 1, groups)]
     if masters is not None:
-        lists.append(("masters", masters, f32, 1, 0))
-    dev = first.get_device()
-    sizes = [p.numel() for p in params]
-    columns = []
-    for name, ts, dtype, per, up in lists:
-        if len(ts) != count:
-            raise ValueError(f"{fn}: {name} holds {len(ts)} tensors, params {count}")
-        for t, n in zip(ts, sizes):
-            kind = t.dtype is dtype or dtype == 1 and t.element_size() == 1
-            if not (kind and t.get_device() == dev >= 0 and t.numel() == (n + up) // per and t.is_contiguous()):
-                _args(fn, (name, t, None, dtype), (name, first, None, None))  # raises if it is one of these
-                raise ValueError(f"{fn}: {name} holds {t.numel()} elements for a parameter of {n}")
-        columns.append([t.data_ptr() for t in ts])
-    none = [0] * count
+        lists.append(("masters", masters, f32, sizes))
+    dev = _tensor_lists(fn, T, lists)
+    columns = [map(T.data_ptr, ts) for _, ts, _, _ in lists]
+    none = (0,) * count
     p, g, m, v = columns[:4]
     ms, vs = columns[4:6] if mx else (none, none)
     w = columns[-1] if masters is not None else none
-    table = (ctypes.c_int64 * (8 * count))(*[x for row in zip(p, g, m, v, ms, vs, w, sizes) for x in row])
-    _launch(fn, dev, stream, table, count, p_type, g_type, STATE_MX8 if mx else STATE_F32, lr, beta1, beta2, eps,
-            weight_decay, step, seed, _scalar(fn, "grad_mul", grad_mul, f32, dev),
+    table = array("q", chain.from_iterable(zip(p, g, m, v, ms, vs, w, sizes)))
+    _launch(fn, dev, stream, table.buffer_info()[0], count, p_type, g_type, STATE_MX8 if mx else STATE_F32, lr, beta1,
+            beta2, eps, weight_decay, step, seed, _scalar(fn, "grad_mul", grad_mul, f32, dev),
             _scalar(fn, "step_dev", step_dev, torch.int32, dev), _scalar(fn, "lr_dev", lr_dev, f32, dev))
+
+
+def _tensor_lists(fn, T, lists):
+    """Checks of (name, tensors, dtype, elements of each) lists: contiguous tensors of that dtype (1: any of
+    one byte) on one GPU, which is returned. Each check runs over a whole list at once, since a call may have
+    hundreds of tensors and little else to do; what is wrong is looked for only then."""
+    dev = lists[0][1][0].get_device()
+    every, fine = [], dev >= 0
+    for _, ts, dtype, sizes in lists:
+        every += ts
+        kinds = {t.dtype for t in ts}
+        fine = fine and len(ts) == len(sizes) and list(map(T.numel, ts)) == sizes and (
+            all(k.itemsize == 1 for k in kinds) if dtype == 1 else kinds == {dtype})
+    if fine and all(map(T.is_contiguous, every)) and set(map(T.get_device, every)) == {dev}:
+        return dev
+    for name, ts, dtype, sizes in lists:
+        if len(ts) != len(sizes):
+            raise ValueError(f"{fn}: {name} holds {len(ts)} tensors, {lists[0][0]} {len(sizes)}")
+        for t, n in zip(ts, sizes):
+            _args(fn, (lists[0][0], lists[0][1][0], None, None), (name, t, None, dtype))
+            if t.numel() != n:
+                raise ValueError(f"{fn}: {name} has a tensor of {t.numel()} elements where {n} are wanted")
+    raise ValueError(f"{fn}: tensors must be contiguous, of one type a list and on one GPU")
 
 
 def _grad_table(fn, grads):
     import torch
-    dev, rows = None, []
-    for g in grads:
-        if not g.is_contiguous() or not g.is_cuda or dev is not None and g.get_device() != dev:
-            raise ValueError(f"{fn}: grads must be contiguous tensors on one GPU")
-        dev = g.get_device()
-        rows += (g.data_ptr(), g.numel(), OUT_F32 if g.dtype is torch.float32 else _float_type(fn, "grads", g))
-    return (ctypes.c_int64 * max(1, len(rows)))(*rows), len(grads), dev
+    T, f32 = torch.Tensor, torch.float32
+    if not grads:
+        return array("q", (0,)), 0, None
+    dev = grads[0].get_device()
+    if dev < 0 or not all(map(T.is_contiguous, grads)) or set(map(T.get_device, grads)) != {dev}:
+        raise ValueError(f"{fn}: grads must be contiguous tensors on one GPU")
+    kinds = [OUT_F32 if g.dtype is f32 else _float_type(fn, "grads", g) for g in grads]
+    return array("q", chain.from_iterable(zip(map(T.data_ptr, grads), map(T.numel, grads), kinds))), len(grads), dev
 
 
 def fp8_grad_norm_ws_bytes(grads) -> int:
     table, count, _ = _grad_table("fp8_grad_norm_ws_bytes", grads)
-    return load().fp8_grad_norm_ws_bytes(table, count)
+    return load().fp8_grad_norm_ws_bytes(table.buffer_info()[0], count)
 
 
 def fp8_grad_norm(grads, norm, mul, ws, grad_scale=1.0, max_norm=float("inf"), step=None, stream=None):
@@ -771,7 +789,7 @@ def fp8_grad_norm(grads, norm, mul, ws, grad_scale=1.0, max_norm=float("inf"), s
         _args(fn, ("ws", ws, None, None))
         if dev is not None and ws.get_device() != dev:
             raise ValueError(f"{fn}: ws is on another GPU than the tensors")
-    _launch(fn, dev, stream, table, count, grad_scale, max_norm, _scalar(fn, "norm", norm, torch.float32, dev),
+    _launch(fn, dev, stream, table.buffer_info()[0], count, grad_scale, max_norm, _scalar(fn, "norm", norm, torch.float32, dev),
             _scalar(fn, "mul", mul, torch.float32, dev), _scalar(fn, "step", step, torch.int32, dev), _ptr(ws),
             0 if ws is None else ws.nbytes)
 

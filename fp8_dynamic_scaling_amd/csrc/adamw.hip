@@ -19,6 +19,7 @@
 // amount in the mean: 16 random bits below the code's last place, from Wellons' 32-bit
 // integer hash "lowbias32" of (seed, tensor, step, element).
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/fp8dyn.h"
 #include "common.hpp"
@@ -32,9 +33,16 @@ typedef __bf16 aw_bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTensorsALaunch = 48;  // their table travels in the kernel's arguments (4 KB)
 constexpr int kNormTensorsALaunch = 128;
-constexpr int kStepV4 = 256 * 4 * 2;      // elements of a workgroup, 32-bit states
-constexpr int kStepV8 = 256 * 8;          // and 8-bit states
-constexpr int64_t kNormChunk = 32768;     // elements of a workgroup of the norm
+constexpr int kPiece32 = 256 * 4, kPiece8 = 256 * 8;  // elements a workgroup takes at once, by the states
+
+// Elements of a workgroup of the norm: some 2048 workgroups, so that a small table has them on every CU and a
+// large one has few partial sums.
+int64_t norm_chunk(int64_t total) {
+  const int64_t c = (total / 2048 + 2047) / 2048 * 2048;
+  return c < 2048 ? 2048 : c > 32768 ? 32768 : c;
+}
+
+int step_iters(bool eight, int64_t pieces) { return eight && pieces >= 8192 ? 2 : 1; }
 
 struct StepTensor {
   void* p;
@@ -51,7 +59,7 @@ struct StepTensor {
 struct StepArgs {
   StepTensor t[kTensorsALaunch];
   int32_t first[kTensorsALaunch + 1];  // chunks before each tensor
-  int32_t count;
+  int32_t count, iters;
   float b1, c1, b2, c2m;  // c1 = 1 - b1, c2m = 1 - b2
   float eps, decay, step, c2;
   uint32_t now;  // the step's number for the random bits
@@ -68,7 +76,7 @@ struct NormArgs {
   int64_t n[kNormTensorsALaunch];
   int32_t first[kNormTensorsALaunch + 1];
   uint32_t f32[(kNormTensorsALaunch + 31) / 32];
-  int32_t count;
+  int32_t count, chunk;
   double* part;
 };
 static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
@@ -93,34 +101,70 @@ __device__ __forceinline__ int tensor_of(const A& a, int32_t chunk) {
   return lo;
 }
 
-// V consecutive values of an fp32 or bf16 array as fp32; `left` of them exist
+// V consecutive values of an fp32 or bf16 array, as they are in memory
 template <bool F32, int V>
-__device__ __forceinline__ void load_v(const void* base, int64_t i, bool wide, int left, float* x) {
-  if (wide) {
-    if constexpr (F32) {
+struct Raw {
+  uint32_t w[F32 ? V : V / 2];
+  __device__ __forceinline__ float operator[](int j) const {
+    if constexpr (F32) return __uint_as_float(w[j]);
+    return j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+  }
+  // `left` of them exist; the others are zeros
+  __device__ __forceinline__ void load(const void* base, int64_t i, bool wide, int left) {
+    constexpr int W = F32 ? V : V / 2;
+    if (wide) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(base) + i * (F32 ? 4 : 2));
+      if constexpr (W == 2) {
+        const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+        w[0] = x[0], w[1] = x[1];
+      } else {
 #pragma unroll
-      for (int j = 0; j < V; j += 4) {
-        const uint4 w = ld_nt16(reinterpret_cast<const float*>(base) + i + j);
-        x[j] = __uint_as_float(w.x), x[j + 1] = __uint_as_float(w.y);
-        x[j + 2] = __uint_as_float(w.z), x[j + 3] = __uint_as_float(w.w);
+        for (int j = 0; j < W; j += 4) {
+          const uint4 x = ld_nt16(p + j);
+          w[j] = x.x, w[j + 1] = x.y, w[j + 2] = x.z, w[j + 3] = x.w;
+        }
       }
-    } else if constexpr (V == 8) {
-      const uint4 w = ld_nt16(reinterpret_cast<const uint16_t*>(base) + i);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[2 * j] = bf16_lo(u[j]), x[2 * j + 1] = bf16_hi(u[j]);
-    } else {
-      const u32x2 w =
-          __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(base) + i));
-      x[0] = bf16_lo(w[0]), x[1] = bf16_hi(w[0]), x[2] = bf16_lo(w[1]), x[3] = bf16_hi(w[1]);
+      return;
     }
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j] = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < left) {
+        if constexpr (F32)
+          w[j] = reinterpret_cast<const uint32_t*>(base)[i + j];
+        else
+          w[j >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(base)[i + j] << (16 * (j & 1));
+      }
+  }
+};
+
+// eight codes
+struct RawCodes {
+  uint2 w;
+  __device__ __forceinline__ void load(const void* base, int64_t i, bool wide, int left) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(base) + i;
+    if (wide) {
+      const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+      w = make_uint2(x[0], x[1]);
+      return;
+    }
+    w = make_uint2(0, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) (j < 4 ? w.x : w.y) |= (uint32_t)p[j] << (8 * (j & 3));
+  }
+};
+
+__device__ __forceinline__ void store_codes(void* base, int64_t i, bool wide, int left, uint2 c) {
+  uint8_t* p = reinterpret_cast<uint8_t*>(base) + i;
+  if (wide) {
+    st_nt8(p, c);
     return;
   }
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    x[j] = j >= left ? 0.0f
-           : F32     ? reinterpret_cast<const float*>(base)[i + j]
-                     : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(base)[i + j] << 16);
+  for (int j = 0; j < 8; ++j)
+    if (j < left) p[j] = (uint8_t)((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
@@ -159,10 +203,21 @@ __device__ __forceinline__ void store_v(void* base, int64_t i, bool wide, int le
 __device__ __forceinline__ void decode8(uint2 c, uint32_t e8, float* x) {
   typedef float v2f __attribute__((ext_vector_type(2)));
   const float s = __uint_as_float(e8 << 23);
-  const v2f a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
-  const v2f d = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false), e = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
-  x[0] = a[0] * s, x[1] = a[1] * s, x[2] = b[0] * s, x[3] = b[1] * s;
-  x[4] = d[0] * s, x[5] = d[1] * s, x[6] = e[0] * s, x[7] = e[1] * s;
+  const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c.x, s, false);
+  const v2f b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c.x, s, true);
+  const v2f d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c.y, s, false);
+  const v2f e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c.y, s, true);
+  x[0] = a[0], x[1] = a[1], x[2] = b[0], x[3] = b[1];
+  x[4] = d[0], x[5] = d[1], x[6] = e[0], x[7] = e[1];
+}
+
+// sqrt(v), correctly rounded for v >= 2^-100 (compared with the library's root for every mantissa, at both
+// parities of the exponent); zero below, where the remainder would lose bits. Seven instructions for the 15
+// of the root that covers everything: with 8-bit states the step is bound by its instructions.
+__device__ __forceinline__ float root(float v) {
+  const float y = __builtin_amdgcn_rsqf(v), g = v * y;
+  const float r = __builtin_fmaf(__builtin_fmaf(-g, g, v), 0.5f * y, g);
+  return v < 0x1p-100f ? 0.0f : r;
 }
 
 // the largest of a group's 32 magnitudes as bits (those of a NaN are above all others): a lane
@@ -180,28 +235,39 @@ __device__ __forceinline__ uint32_t group_top(const float* x) {
   return o > t ? o : t;
 }
 
-// MXFP8 of eight values of a group: codes and the group's E8M0 byte. SR: bits[j] holds 16 random
-// bits. LIFT: values are not negative, and one above zero keeps a code above zero.
+// four codes of x / s, s a power of two. SR: rnd[j]'s upper 20 bits are added below the last place (below the
+// smallest normal code too, where codes are 2^-9 apart) before the rest is cut off.
+template <bool SR>
+__device__ __forceinline__ uint32_t codes4(const float* x, const uint32_t* rnd, float s) {
+  if constexpr (SR) {
+    int w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(0, x[0], rnd[0], s, 0);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[1], rnd[1], s, 1);
+    w = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[2], rnd[2], s, 2);
+    return (uint32_t)__builtin_amdgcn_cvt_scalef32_sr_fp8_f32(w, x[3], rnd[3], s, 3);
+  } else {
+    typedef short v2s __attribute__((ext_vector_type(2)));
+    v2s w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[0], x[1], s, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, x[2], x[3], s, true);
+    return __builtin_bit_cast(uint32_t, w);
+  }
+}
+
+// MXFP8 of eight values of a group: codes and the group's E8M0 byte. LIFT: values are not negative, and one
+// above zero keeps a code above zero.
 template <bool SR, bool LIFT>
-__device__ __forceinline__ uint2 encode8(const float* x, const uint32_t* bits, uint32_t& e8) {
+__device__ __forceinline__ uint2 encode8(float* x, const uint32_t* rnd, uint32_t& e8) {
   const uint32_t top = group_top(x);
   int e = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
   e = e < 12 ? 12 : e;
-  const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-  float y[8];
+  const float s = __uint_as_float((uint32_t)e << 23);
+  if constexpr (LIFT) {
+    // the middle one of x, the smallest code's value and x made large: x, that value, or 0
+    const float least = s * 0x1p-9f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    y[j] = x[j] * inv;
-    if constexpr (SR) {
-      // codes below 2^-6 are 2^-9 apart, as they are in the binade above it: 2^-6 is added there
-      const float a = fabsf(y[j]);
-      const float shift = a < 0x1p-6f ? 0x1p-6f : 0.0f;
-      const uint32_t t = (__float_as_uint(a + shift) + bits[j] * 16u + 8u) & ~0xfffffu;
-      y[j] = copysignf(__uint_as_float(t) - shift, y[j]);
-    }
-    if constexpr (LIFT) y[j] = x[j] > 0.0f && y[j] < 0x1p-9f ? 0x1p-9f : y[j];
+    for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_fmed3f(x[j], least, x[j] * 0x1p126f);
   }
-  uint2 c = make_uint2(cvt4<false>(y[0], y[1], y[2], y[3]), cvt4<false>(y[4], y[5], y[6], y[7]));
+  uint2 c = make_uint2(codes4<SR>(x, rnd, s), codes4<SR>(x + 4, rnd + 4, s));
   e8 = (uint32_t)e;
   if (top >= 0x7f800000u) {  // not finite: the whole group stands for NaN
     e8 = 255u;
@@ -210,10 +276,11 @@ __device__ __forceinline__ uint2 encode8(const float* x, const uint32_t* bits, u
   return c;
 }
 
+// A workgroup takes a.iters pieces of 256 V elements of one tensor, each piece's loads under way while the
+// one before it is computed.
 template <bool P32, bool G32, bool MASTER, bool EIGHT, bool SR>
 __global__ __launch_bounds__(256) void k_adamw(const StepArgs a) {
-  constexpr int V = EIGHT ? 8 : 4, U = EIGHT ? 1 : 2;
-  constexpr int CH = 256 * V * U;
+  constexpr int V = EIGHT ? 8 : 4;
   float mul = 1.0f;
   if (a.mul) {
     mul = *a.mul;
@@ -233,68 +300,60 @@ __global__ __launch_bounds__(256) void k_adamw(const StepArgs a) {
   for (int32_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
     const int k = tensor_of(a, chunk);
     const StepTensor& T = a.t[k];
-    const int64_t n = T.n, begin = (int64_t)(chunk - a.first[k]) * CH;
+    const int64_t n = T.n, begin = (int64_t)(chunk - a.first[k]) * a.iters * (256 * V);
     const uint32_t key = SR ? lowbias32(T.key + now) : 0u;
-    float p[U][V], g[U][V], m[U][V], v[U][V];
-    uint2 cm = make_uint2(0, 0), cv = cm;
-    uint32_t em = 0, ev = 0;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = begin + (int64_t)(u * 256 + threadIdx.x) * V;
+    struct Piece {
+      Raw<G32, V> g;
+      Raw<MASTER || P32, V> p;
+      std::conditional_t<EIGHT, RawCodes, Raw<true, V>> m, v;
+      uint32_t em, ev;
+    } next;
+    auto load = [&](int it) {
+      const int64_t i = begin + (int64_t)(it * 256 + (int)threadIdx.x) * V;
       const int left = n - i < V ? (int)(n - i) : V;
       const bool wide = T.vec && left == V;
-      load_v<G32, V>(T.g, i, wide, left, g[u]);
-      if constexpr (MASTER)
-        load_v<true, V>(T.master, i, wide, left, p[u]);
-      else
-        load_v<P32, V>(T.p, i, wide, left, p[u]);
-      if constexpr (EIGHT) {
-        const uint8_t *qm = reinterpret_cast<const uint8_t*>(T.m) + i, *qv = reinterpret_cast<const uint8_t*>(T.v) + i;
-        if (wide) {
-          const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(qm));
-          const u32x2 y = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(qv));
-          cm = make_uint2(x[0], x[1]), cv = make_uint2(y[0], y[1]);
-        } else {
-          uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < left) {
-              w[j >> 2] |= (uint32_t)qm[j] << (8 * (j & 3));
-              w[2 + (j >> 2)] |= (uint32_t)qv[j] << (8 * (j & 3));
-            }
-          cm = make_uint2(w[0], w[1]), cv = make_uint2(w[2], w[3]);
-        }
-        if (left > 0) em = T.ms[i >> 5], ev = T.vs[i >> 5];
-      } else {
-        load_v<true, V>(T.m, i, wide, left, m[u]);
-        load_v<true, V>(T.v, i, wide, left, v[u]);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = begin + (int64_t)(u * 256 + threadIdx.x) * V;
+      next.g.load(T.g, i, wide, left);
+      next.p.load(MASTER ? T.master : T.p, i, wide, left);
+      next.m.load(T.m, i, wide, left);
+      next.v.load(T.v, i, wide, left);
+      next.em = next.ev = 0;
+      if constexpr (EIGHT)
+        if (left > 0) next.em = T.ms[i >> 5], next.ev = T.vs[i >> 5];
+    };
+    load(0);
+    for (int it = 0; it < a.iters; ++it) {
+      const int64_t i = begin + (int64_t)(it * 256 + (int)threadIdx.x) * V;
+      if (begin + (int64_t)it * (256 * V) >= n) break;
       const int left = n - i < V ? (int)(n - i) : V;
       const bool wide = T.vec && left == V;
-      float r[V];
+      Piece cur = next;
+      if (it + 1 < a.iters) load(it + 1);
+      float p[V], m[V], v[V], r[V];
       if constexpr (EIGHT) {
-        decode8(cm, em, m[u]);
-        decode8(cv, ev, v[u]);
+        decode8(cur.m.w, cur.em, m);
+        decode8(cur.v.w, cur.ev, v);
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        if constexpr (EIGHT) v[u][j] = v[u][j] * v[u][j];
-        const float x = a.mul ? g[u][j] * mul : g[u][j];
-        m[u][j] = m[u][j] * a.b1 + x * a.c1;
-        v[u][j] = v[u][j] * a.b2 + (x * x) * a.c2m;
-        r[j] = sqrtf(v[u][j]);
-        p[u][j] = p[u][j] * decay - (m[u][j] * __builtin_amdgcn_rcpf(r[j] * c2 + a.eps)) * step;
+        if constexpr (EIGHT) {
+          v[j] = v[j] * v[j];
+        } else {
+          m[j] = cur.m[j];
+          v[j] = cur.v[j];
+        }
+        const float x = a.mul ? cur.g[j] * mul : cur.g[j];
+        m[j] = m[j] * a.b1 + x * a.c1;
+        v[j] = v[j] * a.b2 + (x * x) * a.c2m;
+        r[j] = EIGHT ? root(v[j]) : sqrtf(v[j]);
+        p[j] = cur.p[j] * decay - (m[j] * __builtin_amdgcn_rcpf(r[j] * c2 + a.eps)) * step;
       }
       uint32_t lo[V], hi[V];
       if constexpr (SR) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+          // 16 bits each and a half below them, at the top of a word
           const uint32_t b = lowbias32((uint32_t)i + (uint32_t)j + key);
-          lo[j] = b & 0xffffu, hi[j] = b >> 16;
+          lo[j] = b << 16 | 0x8000u, hi[j] = (b & 0xffff0000u) | 0x8000u;
         }
       }
       if constexpr (EIGHT) {
@@ -302,36 +361,26 @@ __global__ __launch_bounds__(256) void k_adamw(const StepArgs a) {
         if (left < V) {
 #pragma unroll
           for (int j = 0; j < V; ++j)
-            if (j >= left) m[u][j] = r[j] = 0.0f;
+            if (j >= left) m[j] = r[j] = 0.0f;
         }
-        cm = encode8<SR, false>(m[u], lo, em);
-        cv = encode8<SR, true>(r, hi, ev);
-        uint8_t *qm = reinterpret_cast<uint8_t*>(T.m) + i, *qv = reinterpret_cast<uint8_t*>(T.v) + i;
-        if (wide) {
-          st_nt8(qm, cm);
-          st_nt8(qv, cv);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < left) {
-              qm[j] = (uint8_t)((j < 4 ? cm.x : cm.y) >> (8 * (j & 3)));
-              qv[j] = (uint8_t)((j < 4 ? cv.x : cv.y) >> (8 * (j & 3)));
-            }
-        }
+        uint32_t em, ev;
+        const uint2 cm = encode8<SR, false>(m, lo, em), cv = encode8<SR, true>(r, hi, ev);
+        store_codes(T.m, i, wide, left, cm);
+        store_codes(T.v, i, wide, left, cv);
         if ((threadIdx.x & 3) == 0 && left > 0) T.ms[i >> 5] = (uint8_t)em, T.vs[i >> 5] = (uint8_t)ev;
       } else {
-        store_v<true, V>(T.m, i, wide, left, m[u]);
-        store_v<true, V>(T.v, i, wide, left, v[u]);
+        store_v<true, V>(T.m, i, wide, left, m);
+        store_v<true, V>(T.v, i, wide, left, v);
       }
-      if constexpr (MASTER) store_v<true, V>(T.master, i, wide, left, p[u]);
+      if constexpr (MASTER) store_v<true, V>(T.master, i, wide, left, p);
       if constexpr (SR && !P32 && !MASTER) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {  // bf16 with 16 random bits below its last place
-          const uint32_t b = __float_as_uint(p[u][j]);
-          if ((b & 0x7fffffffu) <= 0x7f800000u) p[u][j] = __uint_as_float((b + (lo[j] ^ hi[j])) & 0xffff0000u);
+          const uint32_t b = __float_as_uint(p[j]);
+          if ((b & 0x7fffffffu) <= 0x7f800000u) p[j] = __uint_as_float((b + ((lo[j] ^ hi[j]) >> 16)) & 0xffff0000u);
         }
       }
-      store_v<P32, V>(T.p, i, wide, left, p[u]);
+      store_v<P32, V>(T.p, i, wide, left, p);
     }
   }
 }
@@ -342,8 +391,8 @@ __global__ __launch_bounds__(256) void k_grad_sq(const NormArgs a) {
   const int32_t chunks = a.first[a.count];
   for (int32_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
     const int t = tensor_of(a, chunk);
-    const int64_t n = a.n[t], begin = (int64_t)(chunk - a.first[t]) * kNormChunk;
-    const int64_t end = begin + kNormChunk < n ? begin + kNormChunk : n;
+    const int64_t n = a.n[t], begin = (int64_t)(chunk - a.first[t]) * a.chunk;
+    const int64_t end = begin + a.chunk < n ? begin + a.chunk : n;
     const bool f32 = (a.f32[t >> 5] >> (t & 31)) & 1u;
     const bool vec = ((uintptr_t)a.g[t] & 15) == 0;
     double s = 0.0;
@@ -421,8 +470,12 @@ hipError_t launch_step(const StepArgs& s, bool eight, bool sr, unsigned grid, hi
 }  // namespace
 
 hipError_t launch_adamw(const AdamwArgs& a) {
-  const int64_t ch = a.eight ? kStepV8 : kStepV4;
+  int64_t total = 0;
+  for (int32_t i = 0; i < a.count; ++i) total += a.tensors[i].n;
+  const int64_t piece = a.eight ? kPiece8 : kPiece32;
   StepArgs s;
+  s.iters = step_iters(a.eight, total / piece);
+  const int64_t ch = piece * s.iters;
   s.b1 = (float)a.beta1, s.c1 = (float)(1.0 - a.beta1);
   s.b2 = (float)a.beta2, s.c2m = (float)(1.0 - a.beta2);
   s.eps = (float)a.eps;
@@ -473,14 +526,19 @@ hipError_t launch_adamw(const AdamwArgs& a) {
 }
 
 int64_t grad_norm_partials(const fp8_grad_tensor* tensors, int32_t count) {
-  int64_t chunks = 0;
-  for (int32_t i = 0; i < count; ++i) chunks += (tensors[i].n + kNormChunk - 1) / kNormChunk;
+  int64_t total = 0, chunks = 0;
+  for (int32_t i = 0; i < count; ++i) total += tensors[i].n;
+  const int64_t chunk = norm_chunk(total);
+  for (int32_t i = 0; i < count; ++i) chunks += (tensors[i].n + chunk - 1) / chunk;
   return chunks;
 }
 
 hipError_t launch_grad_norm(const GradNormArgs& a) {
   NormArgs s;
-  int64_t chunks = 0, before = 0;
+  int64_t chunks = 0, before = 0, total = 0;
+  for (int32_t i = 0; i < a.count; ++i) total += a.tensors[i].n;
+  const int64_t chunk = norm_chunk(total);
+  s.chunk = (int32_t)chunk;
   s.count = 0;
   auto flush = [&]() -> hipError_t {
     if (s.count == 0) return hipSuccess;
@@ -496,7 +554,7 @@ hipError_t launch_grad_norm(const GradNormArgs& a) {
   for (int32_t i = 0; i < a.count; ++i) {
     const fp8_grad_tensor& t = a.tensors[i];
     if (t.n == 0) continue;
-    const int64_t c = (t.n + kNormChunk - 1) / kNormChunk;
+    const int64_t c = (t.n + chunk - 1) / chunk;
     if (s.count == kNormTensorsALaunch || chunks + c > INT32_MAX) {
       const hipError_t e = flush();
       if (e != hipSuccess) return e;

@@ -44,9 +44,11 @@ def mx(x, rnd, lift):
     y = (pad.reshape(-1, 32) * inv[:, None]).reshape(-1)[:n]
     if rnd is not None:
         a = np.abs(y)
-        shift = np.where(a < F32(2.0 ** -6), F32(2.0 ** -6), F32(0))
-        t = ((a + shift).view(np.uint32) + rnd * np.uint32(16) + np.uint32(8)) & np.uint32(0xFFF00000)
-        y = np.copysign(t.view(F32) - shift, y)
+        r20 = rnd * np.uint32(16) + np.uint32(8)
+        t = ((a.view(np.uint32) + r20) & np.uint32(0xFFF00000)).view(F32)
+        # below 2^-6 codes are 2^-9 apart: in 64 bits, which hold the 20 bits below them
+        small = np.floor(a.astype(np.float64) * 512 + r20 * 2.0 ** -20) / 512
+        y = np.copysign(np.where(a < F32(2.0 ** -6), small, t).astype(F32), y)
     if lift:
         y = np.where((x > 0) & (y < F32(2.0 ** -9)), F32(2.0 ** -9), y)
     return e4m3(y), e.astype(np.uint8)
