@@ -7,7 +7,11 @@
 // The amax is that of the fp32 values, not of their bf16 copies: one rounding, not two.
 //
 // One pass: a row's gradient stays in registers from the loads to the codes. The kernel is
-// bound by HBM: 2 + 4 B read and 4 + 2 B written for each element of h.
+// bound by HBM: 2 + 4 B read and 4 + 2 B written for each element of h. Measured, 8192 x 14336
+// SiLU with e5m2 codes (1.41 GB): 235 us, 6.0 TB/s, where a large torch copy reaches 5.3. dgu
+// leaves by streaming stores, the codes by plain ones: the next GEMM reads them, and with both
+// streaming 255 us, with streaming loads as well; with both plain 252. Two pieces a lane:
+// four 251 us; a persistent grid of two workgroups a CU 254.
 #include "gated.hpp"
 #include "internal.hpp"
 
@@ -32,9 +36,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_gated_bwd(const GatedBwdA
     for (int j = 0; j < J; ++j) {
       const int64_t c = 8 * (t + (int64_t)threads * j);
       const bool in = c < F;
-      vd[j] = in ? ld_nt16(dh + c) : make_uint4(0, 0, 0, 0);
-      vg[j] = in ? ld_nt16(gu + c) : make_uint4(0, 0, 0, 0);
-      vu[j] = in ? ld_nt16(gu + F + c) : make_uint4(0, 0, 0, 0);
+      vd[j] = in ? *reinterpret_cast<const uint4*>(dh + c) : make_uint4(0, 0, 0, 0);
+      vg[j] = in ? *reinterpret_cast<const uint4*>(gu + c) : make_uint4(0, 0, 0, 0);
+      vu[j] = in ? *reinterpret_cast<const uint4*>(gu + F + c) : make_uint4(0, 0, 0, 0);
     }
     float dg[J][8], du[J][8];
     uint32_t top = 0;
@@ -102,8 +106,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_gated_bwd(const GatedBwdA
       const int64_t c = 8 * (t + (int64_t)threads * j);
       if (c < F) {
         uint8_t* o = a.q + row * 2 * F + c;
-        st_nt8(o, codes(dg[j]));
-        st_nt8(o + F, codes(du[j]));
+        *reinterpret_cast<uint2*>(o) = codes(dg[j]);
+        *reinterpret_cast<uint2*>(o + F) = codes(du[j]);
       }
     }
   }
