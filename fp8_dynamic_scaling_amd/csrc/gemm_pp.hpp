@@ -9,6 +9,127 @@
 
 namespace fp8dyn {
 
+// Epilogue of a gated tile of 256 rows x 128 features. A wave has 128 rows x 32 features: element 4 q + u of
+// block i is row 32 i + lane % 32, feature 8 q + 4 (lane / 32) + u; block column 0 holds g, column 1 u. Lanes l
+// and l + 32 exchange halves of two neighbouring q, after which each has 8 features of its row. Every 32 rows of
+// a group's four waves then go through LDS (the ring is idle), so that a store writes whole lines, 256 bytes of
+// each of four rows: CHANGE_ME. F % 8 != 0 or outputs off 16 bytes: single values.
+template <bool GELU, bool ROW>
+__device__ __forceinline__ void gated_epilogue(const GemmParams& p, const TileInfo& ti, int64_t F,
+                                               const float __attribute__((ext_vector_type(16))) (&acc)[4][2],
+                                               uint8_t* lds, int wave, int lane) {
+  constexpr int ARRAY = 32 * 256, GROUP = 3 * ARRAY, BUF = 2 * GROUP;  // 32 rows of out, g and u; two groups
+  // opaque: offsets formed before the K loop would hold registers through it
+  asm volatile("" : "+v"(lane));
+  const int lrow = lane & 31, lg = lane >> 5, grp = wave >> 2, wn = wave & 3;
+  const int row0 = grp * 128, f0 = wn * 32;
+  const float* SA = reinterpret_cast<const float*>(p.sa);
+  const float* SB = reinterpret_cast<const float*>(p.sb);
+  float* s_cs = reinterpret_cast<float*>(lds + 2 * BUF) + wave * 64;
+  float st = 1.0f, rs[4];
+  if constexpr (ROW) {  // lanes 0-31: the gate rows' scales, 32-63 the up rows'
+    int64_t f = ti.n0 + f0 + lrow;
+    f = f < F ? f : F - 1;
+    s_cs[lane] = SB[(int64_t)ti.e * 2 * F + lg * F + f];
+  } else {
+    st = SA[0] * SB[0];
+  }
+  const int32_t m_lim = (int32_t)(ti.m_end - ti.m0) - row0, f_lim = (int32_t)(F - ti.n0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int64_t m = ti.m0 + row0 + 32 * i + lrow;
+    m = m < ti.m_end ? m : ti.m_end - 1;
+    rs[i] = ROW ? SA[m] : 1.0f;
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+  uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + (ti.m0 + row0) * F + ti.n0;
+  uint16_t* gu = p.gu ? p.gu + (ti.m0 + row0) * 2 * F + ti.n0 : nullptr;
+  const bool wide = F % 8 == 0 && (((uintptr_t)p.out | (uintptr_t)p.gu) & 15) == 0;
+  int32_t F32 = (int32_t)F;
+  asm volatile("" : "+s"(F32));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint8_t* buf = lds + (i & 1) * BUF + grp * GROUP;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 16 features: q = 2 h and 2 h + 1
+      uint32_t w[3][2][2];         // out, g, u; q; pairs of features
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float cg[4], cu[4];
+        if constexpr (ROW) {
+          const float4 a = *reinterpret_cast<const float4*>(s_cs + 16 * h + 8 * q + 4 * lg);
+          const float4 b = *reinterpret_cast<const float4*>(s_cs + 32 + 16 * h + 8 * q + 4 * lg);
+          cg[0] = a.x, cg[1] = a.y, cg[2] = a.z, cg[3] = a.w;
+          cu[0] = b.x, cu[1] = b.y, cu[2] = b.z, cu[3] = b.w;
+        }
+        float g[4], u[4], o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          g[e] = acc[i][0][8 * h + 4 * q + e] * (ROW ? rs[i] * cg[e] : st);
+          u[e] = acc[i][1][8 * h + 4 * q + e] * (ROW ? rs[i] * cu[e] : st);
+          o[e] = gate_act<GELU>(g[e]) * u[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          w[0][q][e] = pack_bf16(o[2 * e], o[2 * e + 1]);
+          w[1][q][e] = pack_bf16(g[2 * e], g[2 * e + 1]);
+          w[2][q][e] = pack_bf16(u[2 * e], u[2 * e + 1]);
+        }
+      }
+      // upper lanes' q = 0 against lower lanes' q = 1: features 16 h + 8 lg .. + 7 of the row
+#pragma unroll
+      for (int c = 0; c < 3; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const auto s = __builtin_amdgcn_permlane32_swap(w[c][0][e], w[c][1][e], false, false);
+          w[c][0][e] = s[0], w[c][1][e] = s[1];
+        }
+      if (wide) {
+        // a row's 16 pieces of 16 bytes swizzled by the row, so that 16 rows' stores hit all banks
+        const int at = lrow * 256 + (((wn * 4 + 2 * h + lg) ^ (lrow & 15)) * 16);
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          if (c == 0 || gu)
+            *reinterpret_cast<uint4*>(buf + c * ARRAY + at) = make_uint4(w[c][0][0], w[c][0][1], w[c][1][0], w[c][1][1]);
+        continue;
+      }
+      const int32_t ml = 32 * i + lrow, fl = f0 + 16 * h + 8 * lg;
+      if (ml >= m_lim) continue;
+      const uint32_t off = (uint32_t)(ml * F32 + fl), off2 = off + (uint32_t)(ml * F32);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (fl + e >= f_lim) continue;
+        const int sh = 16 * (e & 1);
+        out[off + e] = (uint16_t)(w[0][e >> 2][(e >> 1) & 1] >> sh);
+        if (gu) {
+          gu[off2 + e] = (uint16_t)(w[1][e >> 2][(e >> 1) & 1] >> sh);
+          gu[off2 + F32 + e] = (uint16_t)(w[2][e >> 2][(e >> 1) & 1] >> sh);
+        }
+      }
+    }
+    if (wide) {
+      // the four waves' 32 rows are in LDS; the last step's reads of the other buffer are done as well
+      wait_lgkm_and_barrier();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int row = 16 * s + wn * 4 + (lane >> 4), piece = lane & 15;
+        const int32_t ml = 32 * i + row, fl = 8 * piece;
+        const int at = row * 256 + ((piece ^ (row & 15)) * 16);
+        const uint32_t off = (uint32_t)(ml * F32 + fl), off2 = off + (uint32_t)(ml * F32);
+        if (ml < m_lim && fl < f_lim) {
+          st_nt16(out + off, *reinterpret_cast<const uint4*>(buf + at));
+          if (gu) {
+            st_nt16(gu + off2, *reinterpret_cast<const uint4*>(buf + ARRAY + at));
+            st_nt16(gu + off2 + F32, *reinterpret_cast<const uint4*>(buf + 2 * ARRAY + at));
+          }
+        }
+      }
+    }
+  }
+  // the next tile's first loads refill the ring
+  wait_lgkm_and_barrier();
+}
+
 // ---------------------------------------------------------------------------
 // Ping-pong kernel (tensorwise, rowwise and MX scales): 256 x 256 tile, 8 waves
 // of 128 x 64 in two groups of four, one wave of each group per SIMD. The
@@ -57,8 +178,10 @@ namespace fp8dyn {
 //    A tile is 256 x 128 features: the 64 B rows of a wave in LDS are the 32
 //    gate rows of its features, then their 32 up rows, so that a lane holds g
 //    and u of the same elements in its two column blocks and the epilogue needs
-//    no exchange; the main loop does not know of it. p.gu, if given, gets g and
-//    u as bf16, [M][2F].
+//    no exchange; the main loop does not know of it. The products are transposed
+//    (B rows as the instruction's rows), so that a lane has one row of the output
+//    and groups of four neighbouring features. p.gu, if given, gets g and u as
+//    bf16, [M][2F].
 template <bool AE5, bool BE5, int SK, bool OF32, bool GR, bool PKB, bool EX = false, int GATE = kGateNone>
 __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
   constexpr int BM = 256, BN = 256, BK = 64, NS = 4;
@@ -325,7 +448,8 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
           for (int j = 0; j < NI; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ad[b][q], bd[j][q], acc[i][j], 0, 0, 0);
+              acc[i][j] = GT ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(bd[j][q], ad[b][q], acc[i][j], 0, 0, 0)
+                             : __builtin_amdgcn_mfma_f32_32x32x16_bf16(ad[b][q], bd[j][q], acc[i][j], 0, 0, 0);
           if (i + 1 < MI) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) ad[b ^ 1][q] = bf16x8<AE5>(fa[i + 1], q);
@@ -354,6 +478,9 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
           if constexpr (MXS)
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[j], acc[i][j], AE5 ? 1 : 0,
                                                                         BE5 ? 1 : 0, SEL, sa[i], SEL, sb[j]);
+          else if constexpr (GT)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa[i], acc[i][j], BE5 ? 1 : 0,
+                                                                        AE5 ? 1 : 0, 0, 127, 0, 127);
           else
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[j], acc[i][j], AE5 ? 1 : 0,
                                                                         BE5 ? 1 : 0, 0, 127, 0, 127);
@@ -428,6 +555,10 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
     // ---- epilogue (the ring is idle: every wave passed the last barrier) ----
     const float* SA = reinterpret_cast<const float*>(p.sa);
     const float* SB = reinterpret_cast<const float*>(p.sb);
+    if constexpr (GT) {
+      gated_epilogue<GATE == kGateGelu, SK == kScaleRow>(p, ti, F, acc, lds, wave, lane);
+      continue;
+    }
     float cs[NI];
     float st = 1.0f;
     if constexpr (SK == kScaleTensor || MXS) {
@@ -437,9 +568,8 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
     } else {
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
-        int64_t n = ti.n0 + (GT ? wn * 32 : wn * TN + 32 * j) + lrow;
-        n = n < F ? n : F - 1;
-        if (GT) n += j * F;
+        int64_t n = ti.n0 + wn * TN + 32 * j + lrow;
+        n = n < N ? n : N - 1;
         cs[j] = SB[(int64_t)ti.e * N + n];
       }
     }
@@ -457,40 +587,9 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
     __builtin_amdgcn_s_waitcnt(0);
     int32_t N32 = (int32_t)F;
     asm volatile("" : "+s"(N32));
-    int32_t ml0 = wm * TM + 4 * lg, nl0 = wn * (GT ? 32 : TN) + lrow;
+    int32_t ml0 = wm * TM + 4 * lg, nl0 = wn * TN + lrow;
     asm volatile("" : "+v"(ml0), "+v"(nl0));
     const int64_t corner = ti.m0 * F + ti.n0;
-    if constexpr (GT) {
-      // column block 0 is g, block 1 u of the same features
-      uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + corner;
-      uint16_t* gu = p.gu ? p.gu + corner + ti.m0 * F : nullptr;
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float4 rs4 = make_float4(st, st, st, st);
-          if constexpr (SK == kScaleRow) rs4 = *reinterpret_cast<const float4*>(&s_rs[32 * i + 8 * q + 4 * lg]);
-          const float rsv[4] = {rs4.x, rs4.y, rs4.z, rs4.w};
-          if (nl0 >= n_lim) continue;
-#pragma unroll
-          for (int t2 = 0; t2 < 4; ++t2) {
-            const int32_t ml = ml0 + 32 * i + 8 * q + t2;
-            if (ml >= m_lim) continue;
-            const float g = acc[i][0][4 * q + t2] * rsv[t2] * cs[0], u = acc[i][1][4 * q + t2] * rsv[t2] * cs[1];
-            const uint32_t o = (uint32_t)(ml * N32 + nl0);
-            out[o] = (uint16_t)pack_bf16(gate_act<GATE == kGateGelu>(g) * u, 0.0f);
-            if (gu) {
-              const uint32_t w = pack_bf16(g, u);
-              const uint32_t og = o + (uint32_t)(ml * N32);
-              gu[og] = (uint16_t)w;
-              gu[og + (uint32_t)N32] = (uint16_t)(w >> 16);
-            }
-          }
-        }
-      }
-      if constexpr (SK == kScaleRow) __syncthreads();
-      continue;
-    }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
 #pragma unroll
