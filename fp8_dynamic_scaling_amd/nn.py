@@ -1,6 +1,7 @@
 """Autograd layers over the library's kernels: Float8Linear, a Linear layer whose GEMMs
-run in FP8; AddNorm, the normalization of a residual stream with the addition into it;
-route, an expert router whose sorted rows and offsets the grouped GEMMs take.
+run in FP8; Float8GatedLinear and Float8GatedMLP, the gated feed-forward block; AddNorm,
+the normalization of a residual stream with the addition into it; route, an expert router
+whose sorted rows and offsets the grouped GEMMs take.
 
 Float8Linear is one autograd node with a hand-written backward, as in "FP8
 Training: Quantization, Autograd, Torchao", section 6: the quantization and
@@ -22,6 +23,10 @@ The kernels write every FP8 operand in the layout its GEMM reads straight
 from bf16, so the backward re-quantizes instead of transposing FP8 copies
 saved by the forward; a deterministic quantizer gives the forward's bytes.
 
+Float8GatedLinear is one node too, of the library's calls (fp8_quant_row, fp8_gated_mm;
+fp8_gated_bwd, fp8_scaled_mm, fp8_wgrad_bf16), with the rowwise recipe. Its backward keeps
+the bf16 input and weight and both projections in bf16.
+
 AddNorm and route are one node each as well (fp8_add_norm_quant_row / fp8_add_norm_bwd,
 fp8_moe_route / fp8_moe_route_bwd). As for any node, a backward pass captured into a
 graph needs leaves whose gradients were not accumulated on another stream: capture
@@ -35,13 +40,16 @@ from typing import NamedTuple
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (E4M3_NATIVE, GATE_SIGMOID, GATE_SOFTMAX, GATE_SOFTMAX_TOPK, NORM_LAYER, NORM_RMS, OUT_BF16,
-               RECIPE_ROWWISE_BF16_WGRAD, RECIPE_TENSORWISE, fp8_add_norm_bwd, fp8_add_norm_bwd_ws_bytes,
-               fp8_add_norm_quant_row, fp8_linear_bwd, fp8_linear_fwd, fp8_linear_ws_bytes, fp8_moe_route,
-               fp8_moe_route_bwd, fp8_moe_route_ws_bytes, load)
+from . import (ACT_GELU_TANH, ACT_SILU, E4M3_NATIVE, E5M2_NATIVE, GATE_SIGMOID, GATE_SOFTMAX, GATE_SOFTMAX_TOPK,
+               NORM_LAYER, NORM_RMS, OUT_BF16, RECIPE_ROWWISE_BF16_WGRAD, RECIPE_TENSORWISE, SCALE_ROW,
+               fp8_add_norm_bwd, fp8_add_norm_bwd_ws_bytes, fp8_add_norm_quant_row, fp8_gated_bwd, fp8_gated_mm,
+               fp8_linear_bwd, fp8_linear_fwd, fp8_linear_ws_bytes, fp8_moe_route, fp8_moe_route_bwd,
+               fp8_moe_route_ws_bytes, fp8_quant_col, fp8_quant_col_kpacked, fp8_quant_col_ws_bytes, fp8_quant_row,
+               fp8_quant_row_kpacked, fp8_scaled_mm, fp8_scaled_mm_kpacked, fp8_wgrad_bf16, load)
 
 _NORMS = {"rms": NORM_RMS, "layer": NORM_LAYER}
 _GATES = {"softmax": GATE_SOFTMAX, "softmax_topk": GATE_SOFTMAX_TOPK, "sigmoid": GATE_SIGMOID}
+_ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU_TANH}
 _RECIPES = {"rowwise": RECIPE_ROWWISE_BF16_WGRAD, "tensorwise": RECIPE_TENSORWISE}
 
 
@@ -136,6 +144,126 @@ class Float8Linear(torch.nn.Module):
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
                 f"bias={self.bias is not None}, recipe={self.recipe}")
+
+
+class Float8GatedLinearFunction(torch.autograd.Function):
+    """h = act(x Wg^T) * (x Wu^T) with the rowwise recipe: x [..., K] and weight [2F, K] (gate rows, then up
+    rows) bf16 on the GPU; h [..., F] bf16. save: a backward will follow, which takes both projections."""
+
+    @staticmethod
+    def forward(ctx, x, weight, act: int, eps: float, use_fast_accum: bool, save: bool):
+        for t, name in ((x, "input"), (weight, "weight")):
+            if t.device.type != "cuda":
+                raise RuntimeError(f"Float8GatedLinear: {name} must be on a ROCm GPU (got {t.device})")
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"Float8GatedLinear: {name} must be bfloat16 (got {t.dtype})")
+        if weight.device != x.device:
+            raise RuntimeError(f"Float8GatedLinear: input is on {x.device}, weight on {weight.device}")
+        K, N = x.shape[-1], weight.shape[0]
+        if weight.dim() != 2 or weight.shape[1] != K:
+            raise ValueError(f"Float8GatedLinear: input has {K} features, weight is {tuple(weight.shape)}")
+        if N % 16:
+            raise ValueError(f"Float8GatedLinear: weight must have a multiple of 16 rows (got {N})")
+        F = N // 2
+        x2, w = _dense(x.reshape(-1, K)), _dense(weight)
+        M = x2.shape[0]
+        # x's own shape, not a view's: the output may be changed in place
+        h = torch.empty((*x.shape[:-1], F), dtype=x.dtype, device=x.device)
+        gu = torch.empty((M, N), dtype=x.dtype, device=x.device) if save else None
+        codes, f32 = dict(dtype=torch.uint8, device=x.device), dict(dtype=torch.float32, device=x.device)
+        with torch.cuda.device(x.device):
+            if M and N:
+                xq, wq = torch.empty((M, K), **codes), torch.empty((N, K), **codes)
+                xs, ws = torch.empty((2, M), **f32), torch.empty((2, N), **f32)
+                packed = F % 16 == 0 and K % 128 == 0 and 0 < K <= 16384 and N <= 1 << 22 and N * K < 1 << 31
+                fp8_quant_row(x2, E4M3_NATIVE, eps, xq, xs[0], xs[1])
+                (fp8_quant_row_kpacked if packed else fp8_quant_row)(w, E4M3_NATIVE, eps, wq, ws[0], ws[1])
+                fp8_gated_mm(xq, wq, E4M3_NATIVE, SCALE_ROW, xs[1], ws[1], act, gu, h.view(M, F), packed=packed,
+                             use_fast_accum=use_fast_accum)
+        ctx.save_for_backward(x2, w, gu)
+        ctx.act, ctx.eps, ctx.shape = act, eps, x.shape
+        return h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        x2, w, gu = ctx.saved_tensors
+        (M, K), N = x2.shape, w.shape[0]
+        F = N // 2
+        dh = _dense(grad_out.to(torch.bfloat16).reshape(M, F))
+        codes, f32 = dict(dtype=torch.uint8, device=x2.device), dict(dtype=torch.float32, device=x2.device)
+        dx = torch.empty_like(x2) if ctx.needs_input_grad[0] else None
+        dw = torch.empty_like(w) if ctx.needs_input_grad[1] else None
+        with torch.cuda.device(x2.device):
+            if M and N:
+                dgu = torch.empty_like(gu) if dw is not None else None
+                q, s = (torch.empty((M, N), **codes), torch.empty((2, M), **f32)) if dx is not None else (None, None)
+                fp8_gated_bwd(dh, gu, ctx.act, E5M2_NATIVE, ctx.eps, dgu, q, None if s is None else s[0],
+                              None if s is None else s[1])
+                if dx is not None:
+                    wq, ws = torch.empty((K, N), **codes), torch.empty((2, K), **f32)
+                    wk = torch.empty(fp8_quant_col_ws_bytes(1, N, K), **codes)
+                    # the layouts fp8_linear_bwd chooses: row-major for outputs of few 64 x 64 tiles
+                    cus = torch.cuda.get_device_properties(x2.device).multi_processor_count
+                    if N % 128 == 0 and N * K < 1 << 30 and -(-M // 64) * -(-K // 64) > cus:
+                        fp8_quant_col_kpacked(w, E4M3_NATIVE, ctx.eps, wq, ws[0], ws[1], wk)
+                        fp8_scaled_mm_kpacked(q, E5M2_NATIVE, wq, E4M3_NATIVE, SCALE_ROW, s[1], ws[1], OUT_BF16, dx, K,
+                                              use_fast_accum=False)
+                    else:
+                        fp8_quant_col(w, E4M3_NATIVE, ctx.eps, wq, ws[0], ws[1], wk)
+                        fp8_scaled_mm(q, E5M2_NATIVE, wq, E4M3_NATIVE, SCALE_ROW, s[1], ws[1], OUT_BF16, dx,
+                                      use_fast_accum=False)
+                if dw is not None:
+                    fp8_wgrad_bf16(dgu, x2, dw)
+            else:
+                for t in (dx, dw):
+                    if t is not None:
+                        t.zero_()
+        return None if dx is None else dx.reshape(ctx.shape), dw, None, None, None, None
+
+
+class Float8GatedLinear(torch.nn.Module):
+    """The first half of a gated feed-forward block, act(x Wg^T) * (x Wu^T), as one FP8 product with the
+    activation ("silu", or "gelu" in its tanh form) in its epilogue. weight [2 hidden][in_features] bf16 holds
+    the gate's rows, then the up projection's. in_features must be a multiple of 16, hidden of 8 and at most
+    32768. Rows and weight rows are quantized one by one (e4m3 forward, e5m2 gradients); the weight gradient is
+    a BF16 product, the input's a full-precision FP8 one."""
+
+    def __init__(self, in_features: int, hidden: int, act: str = "silu", eps: float = 1e-12,
+                 use_fast_accum: bool = True, device=None):
+        super().__init__()
+        if act not in _ACTS:
+            raise ValueError(f"act must be one of {sorted(_ACTS)}")
+        if in_features % 16 or hidden % 8 or hidden > 32768:
+            raise ValueError("in_features must be a multiple of 16, hidden a multiple of 8 and at most 32768 "
+                             f"(got {in_features}, {hidden})")
+        self.in_features, self.hidden, self.act = in_features, hidden, act
+        self.eps, self.use_fast_accum = float(eps), bool(use_fast_accum)
+        self.weight = torch.nn.Parameter(torch.empty((2 * hidden, in_features), dtype=torch.bfloat16, device=device))
+        torch.nn.init.kaiming_uniform_(self.weight, a=math.sqrt(5))
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        load()
+        save = torch.is_grad_enabled() and (x.requires_grad or self.weight.requires_grad)
+        return Float8GatedLinearFunction.apply(x, self.weight, _ACTS[self.act], self.eps, self.use_fast_accum, save)
+
+    def extra_repr(self) -> str:
+        return f"in_features={self.in_features}, hidden={self.hidden}, act={self.act}"
+
+
+class Float8GatedMLP(torch.nn.Module):
+    """A gated feed-forward block: Float8GatedLinear, then a Float8Linear back to the model's features.
+    hidden must be a multiple of 16."""
+
+    def __init__(self, features: int, hidden: int, act: str = "silu", eps: float = 1e-12, device=None):
+        super().__init__()
+        if hidden % 16:
+            raise ValueError(f"hidden must be a multiple of 16 (got {hidden})")
+        self.up = Float8GatedLinear(features, hidden, act, eps, device=device)
+        self.down = Float8Linear(hidden, features, eps=eps, device=device)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        return self.down(self.up(x))
 
 
 def _dense(t: torch.Tensor) -> torch.Tensor:

@@ -197,3 +197,76 @@ def test_gated_kernels_have_no_mfma_hazard(tmp_path):
     assert not mfma_overlaps(asm)
     assert not mfma_raw_hazards(asm)
 
+
+
+def test_layers_refuse():
+    from fp8_dynamic_scaling_amd import nn
+    with pytest.raises(ValueError, match="act must be"):
+        nn.Float8GatedLinear(64, 32, "relu")
+    for K, F in ((40, 32), (64, 12), (64, 32776)):
+        with pytest.raises(ValueError, match="multiple of 16"):
+            nn.Float8GatedLinear(K, F)
+    with pytest.raises(ValueError, match="multiple of 16"):
+        nn.Float8GatedMLP(64, 24)
+    with pytest.raises(RuntimeError, match="ROCm GPU"):
+        nn.Float8GatedLinear(64, 32)(torch.zeros(2, 64, dtype=torch.bfloat16))
+
+
+def _bf16(*shape):
+    return torch.nn.Parameter(torch.zeros(shape, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(state_bits=16), "state_bits"), (dict(lr=-1.0), "lr must"), (dict(lr=torch.zeros(1)), "capturable"),
+    (dict(betas=(0.9, 1.0)), "betas"), (dict(betas=(-0.1, 0.9)), "betas"), (dict(eps=-1.0), "negative"),
+    (dict(weight_decay=-1.0), "negative"), (dict(max_norm=0.0), "max_norm"), (dict(seed=0), "seed"),
+])
+def test_optimizer_refuses(kw, match):
+    from fp8_dynamic_scaling_amd.optim import AdamW
+    with pytest.raises(ValueError, match=match):
+        AdamW([_bf16(4, 4)], **kw)
+
+
+def test_optimizer_refuses_parameters():
+    from fp8_dynamic_scaling_amd.optim import AdamW
+    with pytest.raises(TypeError, match="bfloat16 or float32"):
+        AdamW([torch.nn.Parameter(torch.zeros(4, dtype=torch.float16))])
+    with pytest.raises(ValueError, match="contiguous"):
+        AdamW([torch.nn.Parameter(torch.zeros(4, 6).t())])
+    p = _bf16(4, 4)
+    opt = AdamW([p])
+    opt.step()  # nothing has a gradient
+    with pytest.raises(ValueError, match="max_norm"):
+        opt.step(grad_scale=0.5)
+    p.grad = torch.zeros_like(p)
+    with pytest.raises(ValueError, match="on the GPU"):
+        opt.step()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(max_norm=1.0), dict(capturable=True)])
+def test_optimizer_loads_states_as_they_were(kw):
+    """Codes, fp32 moments of bf16 parameters and the count of steps survive load_state_dict, which casts states to the
+    parameter's type by itself; with the count on the device it is one tensor for all parameters."""
+    import copy
+    from fp8_dynamic_scaling_amd.optim import AdamW
+    for bits in (8, 32):
+        a, b = (AdamW([_bf16(5, 7), _bf16(3)], state_bits=bits, master_weights=True, **kw) for _ in range(2))
+        for p in a.param_groups[0]["params"]:
+            a._new_state(p)
+            for k, v in a.state[p].items():
+                if torch.is_tensor(v) and k != "step":
+                    v.copy_(torch.arange(v.numel()) * (1 if v.dtype == torch.uint8 else 1.0009))
+        for p in a.param_groups[0]["params"]:
+            if kw:
+                a.state[p]["step"].fill_(9)
+            else:
+                a.state[p]["step"] = 9
+        b.load_state_dict(copy.deepcopy(a.state_dict()))
+        steps = []
+        for p, q in zip(a.param_groups[0]["params"], b.param_groups[0]["params"]):
+            assert a.state[p].keys() == b.state[q].keys()
+            for k, v in a.state[p].items():
+                w = b.state[q][k]
+                assert (torch.equal(v, w) and v.dtype == w.dtype) if torch.is_tensor(v) else v == w
+            steps.append(b.state[q]["step"])
+        assert int(steps[0]) == 9 and (steps[0] is steps[1] if kw else True)
