@@ -13,9 +13,9 @@ namespace fp8dyn {
 
 namespace {
 
-// as the plain products' conditions: 32-bit offsets within a tile of A, in B and in the output
+// two stages at least, and 32-bit offsets within a tile of A, in B and in the output
 bool fast_eligible(const GatedMmArgs& g) {
-  return g.K % 128 == 0 && 2 * g.F <= (1 << 22) && g.K <= (1 << 22) && 2 * g.F * g.K < ((int64_t)1 << 31);
+  return g.K > 64 && 2 * g.F <= (1 << 22) && g.K <= (1 << 22) && 2 * g.F * g.K < ((int64_t)1 << 31);
 }
 
 // ---------------------------------------------------------------------------

@@ -213,7 +213,9 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
   const int64_t N = p.N, K = p.K;
   const int64_t F = GT ? N / 2 : N;  // output columns
   const int64_t nt = (F + FN - 1) / FN;
-  const int64_t nk = K / BK;
+  // gated, row-major: K a multiple of 16, the last stage then partly zeros
+  const int64_t nk = GT ? (K + BK - 1) / BK : K / BK;
+  const int32_t tail = GT && !PKB ? (int32_t)(K % BK) : 0;
   const uint32_t lds0 = lds_addr(lds);
   // MX scales 16 bytes per row at a time: a dword per row touches a cache
   // line per lane, and the DMA pays per line touched
@@ -317,6 +319,9 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
       }
     }
     const uint32_t part_lds = (grp == 0 ? 0u : (uint32_t)SA_BYTES) + (uint32_t)(wn * 4096);
+    // the lane's 16 bytes of the last stage lie past K: it loads the stage's first ones, and zeroes them
+    const int32_t ld_c = 16 * (ld_pch ^ ((ld_row >> 2) & 3));
+    const bool past = tail != 0 && ld_c >= tail;
     // MX: this wave's 64 rows (those of its stage loads) of its operand's
     // E8M0 bytes, 4 per row per stage pair (rows past the expert / N fetch a
     // valid row)
@@ -336,8 +341,9 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
     auto issue = [&](int64_t s) {
       const uint32_t slot = lds0 + (uint32_t)((s & (NS - 1)) * STAGE) + part_lds;
       const uint8_t* bk = base + s * sstride;
+      const uint32_t back = GT && !PKB && past && s == nk - 1 ? (uint32_t)ld_c : 0u;
 #pragma unroll
-      for (int d = 0; d < DH; ++d) dma16(bk, off[d], slot + (uint32_t)(d * 1024));
+      for (int d = 0; d < DH; ++d) dma16(bk, off[d] - back, slot + (uint32_t)(d * 1024));
       if constexpr (MXS) {
         const uint32_t o = sc_off + (uint32_t)(2 * s);  // byte 4 (s / 2) of the row
         if (scl16) {
@@ -510,8 +516,17 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
           wait_vm_lgkm_and_barrier<2 * DH + X>();
         }
       } else if (u + 2 < nk) {
-        wait_vm_lgkm_and_barrier<DH>();  // stage nk - 1 is odd
+        wait_vm_lgkm_and_barrier<DH>();  // MX: stage nk - 1 is odd
       } else {
+        if (GT && !PKB && tail != 0 && u + 2 == nk) {
+          // this wave's loads of the last stage have landed, and nobody reads it before the barrier
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+          if (past) {
+            uint8_t* at = lds + (int)((nk - 1) & (NS - 1)) * STAGE + part_lds + 16 * lane;
+#pragma unroll
+            for (int d = 0; d < DH; ++d) *reinterpret_cast<uint4*>(at + d * 1024) = make_uint4(0, 0, 0, 0);
+          }
+        }
         wait_vm_lgkm_and_barrier<0>();
       }
     };
@@ -519,7 +534,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
     // prologue: stages 0 .. min(nk, 3) - 1; then stage 0 has landed
     issue(0);
     issue(1);
-    if (nk >= 4) {
+    if (nk >= 3) {
       issue(2);
       if (scl16) wait_vm_lgkm_and_barrier<2 * DH>();
       else wait_vm_lgkm_and_barrier<2 * DH + X>();

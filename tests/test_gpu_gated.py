@@ -53,7 +53,10 @@ def check(out, gu, a, w, act, fast, label):
 DENSE = [(1, 16, 128, True), (1, 1, 16, False), (3, 7, 48, False), (5, 129, 256, False), (64, 48, 128, True),
          (255, 144, 256, True), (257, 272, 384, True), (300, 80, 640, False), (513, 515, 720, False),
          (260, 1000, 128, False), (1024, 1040, 256, True), (2048, 2064, 128, False), (33, 8192, 256, True),
-         (17, 8200, 256, False), (2, 4096, 1040, False)]
+         (17, 8200, 256, False), (2, 4096, 1040, False),
+         # the large kernel's last stage of 64: one of 16, 32 and 48, with two stages, three and more
+         (1500, 1000, 80, False), (1500, 1001, 144, False), (1500, 1000, 176, False), (1301, 1200, 224, False),
+         (1500, 1000, 304, False), (1500, 1000, 720, False), (1500, 1008, 128, True)]
 
 
 @pytest.mark.parametrize("M,F,K,packed", DENSE)
@@ -101,7 +104,7 @@ def test_gated_mm_tensorwise(M, F, K, packed, fast):
 # rows of each expert (empty ones among them), rows of none at the end
 GROUPED = [([0, 1, 0, 3], 0, 16, 128, True), ([5, 0, 250, 9], 6, 144, 256, True), ([300, 257, 0, 1], 2, 80, 128, True),
            ([0, 0, 0], 4, 48, 128, True), ([7, 0, 3], 0, 33, 48, False), ([129, 130, 0, 4], 3, 136, 272, False),
-           ([300, 0, 2], 1, 200, 384, False)]
+           ([300, 0, 2], 1, 200, 384, False), ([1, 513, 0], 2, 264, 208, False)]
 
 
 @pytest.mark.parametrize("rows,pad,F,K,packed", GROUPED)
