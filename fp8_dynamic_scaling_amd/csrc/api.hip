@@ -689,7 +689,7 @@ static fp8_status check_gated(const void* a, const void* b, const void* sa, cons
   if (M < 0 || F < 0 || K < 0) return FP8_ERR_INVALID_ARGUMENT;
   if (act != FP8_ACT_SILU && act != FP8_ACT_GELU_TANH) return FP8_ERR_INVALID_ARGUMENT;
   if (M == 0 || F == 0) return FP8_OK;
-  if (M > INT32_MAX || F >= (1 << 30)) return FP8_ERR_UNSUPPORTED;
+  if (M > INT32_MAX || F > (1 << 21)) return FP8_ERR_UNSUPPORTED;
   if (!out) return FP8_ERR_INVALID_ARGUMENT;
   if (K > 0 && (!a || !b || !sa || !sb)) return FP8_ERR_INVALID_ARGUMENT;
   if (K % 16 != 0 || (packed && (F % 16 != 0 || K % 128 != 0))) return FP8_ERR_ALIGNMENT;

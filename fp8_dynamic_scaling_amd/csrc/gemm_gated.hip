@@ -6,6 +6,9 @@
 // a tile holds, the gate and up rows of the same features, so that both end up in the same lane, and the
 // epilogue, which forms act(g) u in fp32 and rounds it once. The projections themselves are written only
 // for a backward: without them F values a row leave the kernel instead of 2F, and no pass reads them again.
+#include <algorithm>
+#include <cmath>
+
 #include "gemm_generic.hpp"
 #include "gemm_pp.hpp"
 
@@ -40,11 +43,10 @@ __global__ __launch_bounds__(64 * WV) void k_gated_few(GemmParams p) {
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t F = p.N / 2, K = p.K, M = p.M;
-  const int64_t f0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * MT);
   const int64_t units = (K + 127) / 128;
   const int64_t u0 = wave * units / WV, u1 = (wave + 1) * units / WV;
   uint8_t* mine = lds + wave * WAVE_BYTES;
-
+  const int64_t f0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * MT);
   // a unit's loads: 4 of B (row-major: 8 rows each, gate rows first; k-packed: gate chunks, then up chunks),
   // 2 MT of A (8 rows each). Rows past F or M read the last one, and are never stored.
   const int lr = lane >> 3, lp = lane & 7;
@@ -158,11 +160,10 @@ __global__ __launch_bounds__(64 * WV) void k_gated_few(GemmParams p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) red[wave][8 * i + 4 * h + e][lane] = acc[i][h][e];
   __syncthreads();
-  if (wave >= MT) return;
   // wave i: the rows 16 i + lane % 16, features 4 (lane / 16) + e
   const int64_t m = m0 + 16 * wave + r;
   const int64_t f = f0 + 4 * g;
-  if (m >= M || f >= F) return;
+  if (wave >= MT || m >= M || f >= F) return;
   const float* SA = reinterpret_cast<const float*>(p.sa);
   const float* SB = reinterpret_cast<const float*>(p.sb);
   const float sm = ROW ? SA[m] : SA[0];
@@ -201,80 +202,121 @@ __global__ __launch_bounds__(64 * WV) void k_gated_few(GemmParams p) {
 
 template <int GATE, int SK>
 hipError_t launch_few(const GatedMmArgs& g) {
-  GemmParams p{g.a, g.b, g.sa, g.sb, nullptr, 1, g.M, 2 * g.F, g.K, g.out, g.gu};
   constexpr bool ROW = SK == kScaleRow;
   const int mt = g.M <= 16 ? 1 : g.M <= 32 ? 2 : 4;
-  const dim3 grid((unsigned)((g.F + 15) / 16), (unsigned)((g.M + 16 * mt - 1) / (16 * mt)));
-  // eight waves for K where a wave's registers let them all run, or few workgroups need them
-  const bool eight = mt == 1 || (int64_t)grid.x * grid.y <= 256;
-  auto run = [&](auto m) {
-    constexpr int MT = decltype(m)::value;
-    if (eight) {
-      if (g.packed) hipLaunchKernelGGL((k_gated_few<MT, 8, GATE, true, ROW>), grid, dim3(512), 0, g.stream, p);
-      else hipLaunchKernelGGL((k_gated_few<MT, 8, GATE, false, ROW>), grid, dim3(512), 0, g.stream, p);
-    } else {
-      if (g.packed) hipLaunchKernelGGL((k_gated_few<MT, 4, GATE, true, ROW>), grid, dim3(256), 0, g.stream, p);
-      else hipLaunchKernelGGL((k_gated_few<MT, 4, GATE, false, ROW>), grid, dim3(256), 0, g.stream, p);
+  const int64_t nf = (g.F + 15) / 16, nm = (g.M + 16 * mt - 1) / (16 * mt);
+  // eight waves for K where few registers or few workgroups let them all run
+  const bool eight = mt == 1 || nf * nm <= 256;
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(65535, ((int64_t)1 << 22) / nf));  // of one grid
+  for (int64_t y = 0; y < nm; y += most) {
+    const int64_t m0 = y * 16 * mt;
+    GemmParams p{g.a + m0 * g.K, g.b, g.sa + (ROW ? m0 : 0), g.sb, nullptr, 1, g.M - m0, 2 * g.F, g.K,
+                 g.out + m0 * g.F, g.gu ? g.gu + m0 * 2 * g.F : nullptr};
+    const dim3 grid((unsigned)nf, (unsigned)std::min<int64_t>(most, nm - y));
+    auto run = [&](auto m) {
+      constexpr int MT = decltype(m)::value;
+      if (eight) {
+        if (g.packed) hipLaunchKernelGGL((k_gated_few<MT, 8, GATE, true, ROW>), grid, dim3(512), 0, g.stream, p);
+        else hipLaunchKernelGGL((k_gated_few<MT, 8, GATE, false, ROW>), grid, dim3(512), 0, g.stream, p);
+      } else {
+        if (g.packed) hipLaunchKernelGGL((k_gated_few<MT, 4, GATE, true, ROW>), grid, dim3(256), 0, g.stream, p);
+        else hipLaunchKernelGGL((k_gated_few<MT, 4, GATE, false, ROW>), grid, dim3(256), 0, g.stream, p);
+      }
+    };
+    if (mt == 1) run(std::integral_constant<int, 1>{});
+    else if (mt == 2) run(std::integral_constant<int, 2>{});
+    else run(std::integral_constant<int, 4>{});
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// Rows of a workgroup's tile in the ping-pong kernel, or 0 for k_gated_few: the least of what each would take,
+//   rounds over the CUs x (2 us + K x the time for 1024 of K),
+// with times from measurements of one full round each (us for 1024 of K; the last with full precision):
+//   k_gated_few, 64 rows x 16 features, two a CU         3.6
+//   tiles of 64 x 128 features                           7.4 (10.8): a stage's loads bound it, not its products
+//   tiles of 128 x 128 features                          9.3 (12.9)
+//   tiles of 256 x 128 features, up to half of the CUs  10.5 (16.6); all of them 13.5 (22)
+// Measured, k_gated_few / 64 / 128 / 256 rows, us: 256 x 2048 x 2048 11.8 / 17.1 / 19.4 / 23.4; 1024 x 1040 x 720
+// 18.3 / 12.1 / 14.0 / 30.9; 1024 x 2048 x 2048 - / 19.0 / 20.7 / 24.6; 256 x 14336 x 4096 - / 60.3 / 44.4 / 51.4;
+// 2048 x 4096 x 4096 - / 117 / 77.6 / 59.2. An expert's rows are taken as the mean, and half a tile more.
+int tile_rows(const GatedMmArgs& g) {
+  const double cus = device_cus(), k = (double)g.K / 1024.0;
+  if (!g.offsets && g.M <= 32) return 0;
+  const double nt = (double)((g.F + 127) / 128);
+  double best = 1e300;
+  int rows = 256;
+  if (!g.offsets) {
+    const double wgs = (double)((g.F + 15) / 16) * (double)((g.M + 63) / 64);
+    best = std::ceil(wgs / (2.0 * cus)) * (2.0 + 3.6 * k);
+    rows = 0;
+  }
+  if (g.packed || fast_eligible(g)) {
+    for (const int bm : {64, 128, 256}) {
+      double mt = (double)((g.M + bm - 1) / bm);
+      if (g.offsets) {
+        mt = (double)g.M / g.E / bm + 0.5;
+        mt = (mt < 1.0 ? 1.0 : mt) * g.E;
+      }
+      const double tiles = mt * nt;
+      const double c = bm == 64    ? (g.exact ? 10.8 : 7.4)
+                       : bm == 128 ? (g.exact ? 12.9 : 9.3)
+                       : 2.0 * tiles <= cus ? (g.exact ? 16.6 : 10.5)
+                                            : (g.exact ? 22.0 : 13.5);
+      const double t = std::ceil(tiles / cus) * (2.0 + c * k);
+      if (t < best) best = t, rows = bm;
     }
-  };
-  if (mt == 1) run(std::integral_constant<int, 1>{});
-  else if (mt == 2) run(std::integral_constant<int, 2>{});
-  else run(std::integral_constant<int, 4>{});
-  return hipGetLastError();
+  }
+  return rows;
 }
 
-// Few rows, or so few tiles that those of 256 x 128 features would leave most CUs idle: a workgroup of this
-// kernel takes some 4 us for each 1024 of K with two on a CU, a tile of the ping-pong kernel 10.5 us.
-bool few_rows(const GatedMmArgs& g) {
-  if (g.offsets) return false;
-  const int64_t wgs = ((g.F + 15) / 16) * ((g.M + 63) / 64);
-  const int64_t rounds = (((g.M + 255) / 256) * ((g.F + 127) / 128) + device_cus() - 1) / device_cus();
-  return g.M <= 64 || wgs <= 1344 * rounds;
-}
-
-template <int GATE, int SK, bool GR, bool PKB, bool EX>
-hipError_t launch_pp(const GatedMmArgs& g) {
+template <int GATE, int SK, bool GR, bool PKB, bool EX, int BM>
+hipError_t launch_pp_rows(const GatedMmArgs& g) {
   GemmParams p{g.a, g.b, g.sa, g.sb, g.offsets, g.E, g.M, 2 * g.F, g.K, g.out, g.gu};
   const int64_t nt = (g.F + 127) / 128;
-  const int64_t tiles = ((g.M + 255) / 256 + (GR ? g.E : 0)) * nt;
+  const int64_t tiles = ((g.M + BM - 1) / BM + (GR ? g.E : 0)) * nt;
   int64_t grid = device_cus();
   if (tiles < grid) grid = tiles;
   if (grid >= kNumXcd) grid -= grid % kNumXcd;
-  hipLaunchKernelGGL((k_gemm_fp8_pp<false, false, SK, false, GR, PKB, EX, GATE>), dim3((unsigned)grid), dim3(512), 0,
-                     g.stream, p);
+  hipLaunchKernelGGL((k_gemm_fp8_pp<false, false, SK, false, GR, PKB, EX, GATE, BM>), dim3((unsigned)grid), dim3(512),
+                     0, g.stream, p);
   return hipGetLastError();
 }
 
-template <int B, int GATE, int SK, bool EX>
+template <int GATE, int SK, bool GR, bool PKB, bool EX>
+hipError_t launch_pp(const GatedMmArgs& g, int rows) {
+  return rows == 64    ? launch_pp_rows<GATE, SK, GR, PKB, EX, 64>(g)
+         : rows == 128 ? launch_pp_rows<GATE, SK, GR, PKB, EX, 128>(g)
+                       : launch_pp_rows<GATE, SK, GR, PKB, EX, 256>(g);
+}
+
+// Grouped products of K below two stages, or of weights past 32-bit offsets.
+template <int GATE, bool EX>
 hipError_t launch_generic(const GatedMmArgs& g) {
   GemmParams p{g.a, g.b, g.sa, g.sb, g.offsets, g.E, g.M, 2 * g.F, g.K, g.out, g.gu};
-  const int64_t nt = (g.F + B / 2 - 1) / (B / 2);
-  const int64_t tiles = ((g.M + B - 1) / B + (g.offsets ? g.E : 0)) * nt;
+  const int64_t tiles = ((g.M + 127) / 128 + g.E) * ((g.F + 63) / 64);
   int64_t grid = device_cus();
   if (tiles < grid)
     grid = tiles;
   else if (grid >= kNumXcd)
     grid -= grid % kNumXcd;
-  hipLaunchKernelGGL((k_gemm_fp8<B, B, 2, 2, false, false, SK, false, EX, GATE>), dim3((unsigned)grid), dim3(256), 0,
-                     g.stream, p);
+  hipLaunchKernelGGL((k_gemm_fp8<128, 128, 2, 2, false, false, kScaleRow, false, EX, GATE>), dim3((unsigned)grid),
+                     dim3(256), 0, g.stream, p);
   return hipGetLastError();
 }
 
 template <int GATE, int SK, bool EX>
 hipError_t launch_form(const GatedMmArgs& g) {
-  if (few_rows(g)) return launch_few<GATE, SK>(g);
-  if (g.packed) {
-    if constexpr (SK == kScaleRow)
-      if (g.offsets) return launch_pp<GATE, SK, true, true, EX>(g);
-    return launch_pp<GATE, SK, false, true, EX>(g);
+  const int rows = tile_rows(g);
+  if (rows == 0) return launch_few<GATE, SK>(g);
+  if constexpr (SK == kScaleRow) {
+    if (!g.packed && !fast_eligible(g)) return launch_generic<GATE, EX>(g);
+    if (g.offsets)
+      return g.packed ? launch_pp<GATE, SK, true, true, EX>(g, rows) : launch_pp<GATE, SK, true, false, EX>(g, rows);
   }
-  if (!g.offsets && gemm_fp8_small_dense(g.M, 2 * g.F)) return launch_generic<64, GATE, SK, EX>(g);
-  if (fast_eligible(g)) {
-    if constexpr (SK == kScaleRow)
-      if (g.offsets) return launch_pp<GATE, SK, true, false, EX>(g);
-    return launch_pp<GATE, SK, false, false, EX>(g);
-  }
-  return launch_generic<128, GATE, SK, EX>(g);
+  return g.packed ? launch_pp<GATE, SK, false, true, EX>(g, rows) : launch_pp<GATE, SK, false, false, EX>(g, rows);
 }
 
 template <int GATE>

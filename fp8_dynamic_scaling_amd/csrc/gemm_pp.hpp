@@ -9,24 +9,27 @@
 
 namespace fp8dyn {
 
-// Epilogue of a gated tile of 256 rows x 128 features. A wave has 128 rows x 32 features: element 4 q + u of
+// Epilogue of a gated tile of 64 MI rows x 128 features. A wave has 32 MI rows x 32 features: element 4 q + u of
 // block i is row 32 i + lane % 32, feature 8 q + 4 (lane / 32) + u; block column 0 holds g, column 1 u. Lanes l
 // and l + 32 exchange halves of two neighbouring q, after which each has 8 features of its row. Every 32 rows of
 // a group's four waves then go through LDS (the ring is idle), so that a store writes whole lines, 256 bytes of
 // each of four rows: CHANGE_ME. F % 8 != 0 or outputs off 16 bytes: single values.
-template <bool GELU, bool ROW>
+constexpr int kGatedEpilogueLds = 2 * 2 * 3 * 32 * 256 + 8 * 64 * 4;
+
+template <bool GELU, bool ROW, int MI>
 __device__ __forceinline__ void gated_epilogue(const GemmParams& p, const TileInfo& ti, int64_t F,
-                                               const float __attribute__((ext_vector_type(16))) (&acc)[4][2],
+                                               const float __attribute__((ext_vector_type(16))) (&acc)[MI][2],
                                                uint8_t* lds, int wave, int lane) {
   constexpr int ARRAY = 32 * 256, GROUP = 3 * ARRAY, BUF = 2 * GROUP;  // 32 rows of out, g and u; two groups
   // opaque: offsets formed before the K loop would hold registers through it
   asm volatile("" : "+v"(lane));
   const int lrow = lane & 31, lg = lane >> 5, grp = wave >> 2, wn = wave & 3;
-  const int row0 = grp * 128, f0 = wn * 32;
+  const int row0 = grp * 32 * MI, f0 = wn * 32;
   const float* SA = reinterpret_cast<const float*>(p.sa);
   const float* SB = reinterpret_cast<const float*>(p.sb);
-  float* s_cs = reinterpret_cast<float*>(lds + 2 * BUF) + wave * 64;
-  float st = 1.0f, rs[4];
+  static_assert(2 * BUF + 8 * 64 * 4 == kGatedEpilogueLds, "epilogue buffers");
+  float* s_cs = reinterpret_cast<float*>(lds + (MI == 1 ? 1 : 2) * BUF) + wave * 64;
+  float st = 1.0f, rs[MI];
   if constexpr (ROW) {  // lanes 0-31: the gate rows' scales, 32-63 the up rows'
     int64_t f = ti.n0 + f0 + lrow;
     f = f < F ? f : F - 1;
@@ -36,7 +39,7 @@ __device__ __forceinline__ void gated_epilogue(const GemmParams& p, const TileIn
   }
   const int32_t m_lim = (int32_t)(ti.m_end - ti.m0) - row0, f_lim = (int32_t)(F - ti.n0);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < MI; ++i) {
     int64_t m = ti.m0 + row0 + 32 * i + lrow;
     m = m < ti.m_end ? m : ti.m_end - 1;
     rs[i] = ROW ? SA[m] : 1.0f;
@@ -48,7 +51,7 @@ __device__ __forceinline__ void gated_epilogue(const GemmParams& p, const TileIn
   int32_t F32 = (int32_t)F;
   asm volatile("" : "+s"(F32));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < MI; ++i) {
     uint8_t* buf = lds + (i & 1) * BUF + grp * GROUP;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // 16 features: q = 2 h and 2 h + 1
@@ -90,7 +93,8 @@ __device__ __forceinline__ void gated_epilogue(const GemmParams& p, const TileIn
 #pragma unroll
         for (int c = 0; c < 3; ++c)
           if (c == 0 || gu)
-            *reinterpret_cast<uint4*>(buf + c * ARRAY + at) = make_uint4(w[c][0][0], w[c][0][1], w[c][1][0], w[c][1][1]);
+            *reinterpret_cast<uint4*>(buf + c * ARRAY + at) =
+                make_uint4(w[c][0][0], w[c][0][1], w[c][1][0], w[c][1][1]);
         continue;
       }
       const int32_t ml = 32 * i + lrow, fl = f0 + 16 * h + 8 * lg;
@@ -182,22 +186,29 @@ __device__ __forceinline__ void gated_epilogue(const GemmParams& p, const TileIn
 //    (B rows as the instruction's rows), so that a lane has one row of the output
 //    and groups of four neighbouring features. p.gu, if given, gets g and u as
 //    bf16, [M][2F].
-template <bool AE5, bool BE5, int SK, bool OF32, bool GR, bool PKB, bool EX = false, int GATE = kGateNone>
+//  - BMT (gated products): rows of a tile, 256, 128 or 64, for shapes of few tiles and experts of few rows. A
+//    group's waves then have half as many rows each and load half as much of A.
+template <bool AE5, bool BE5, int SK, bool OF32, bool GR, bool PKB, bool EX = false, int GATE = kGateNone,
+          int BMT = 256>
 __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
-  constexpr int BM = 256, BN = 256, BK = 64, NS = 4;
+  constexpr int BM = BMT, BN = 256, BK = 64, NS = 4;
   constexpr bool GT = GATE != kGateNone;
   constexpr int FN = GT ? BN / 2 : BN;  // output columns of a tile
-  constexpr int TM = 128, TN = 64, MI = TM / 32, NI = TN / 32;
-  constexpr int SA_BYTES = BM * BK, STAGE = 2 * SA_BYTES;
-  constexpr int DH = 4;  // wave-wide loads per wave per stage: its group's half over 4 waves
+  constexpr int TM = BM / 2, TN = 64, MI = TM / 32, NI = TN / 32;
+  constexpr int SA_BYTES = BM * BK, STAGE = SA_BYTES + BN * BK;
+  // wave-wide loads per wave per stage: its group's operand over 4 waves
+  constexpr int DA = BM / 64, DH = BN / 64;
   typedef float v16f __attribute__((ext_vector_type(16)));
   constexpr bool MXS = SK == kScaleMX;
   constexpr int X = MXS ? 1 : 0;  // scale loads of an even stage
   static_assert(SK == kScaleTensor || SK == kScaleRow || MXS, "tensorwise, rowwise or MX");
   static_assert(!(EX && MXS), "full-precision accumulation: tensorwise or rowwise scales");
   static_assert(!GT || (!MXS && !OF32), "gated products: tensorwise or rowwise scales, bf16");
+  static_assert(BM == 256 || (GT && (BM == 128 || BM == 64)), "smaller tiles: gated products");
 
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
+  // the gated epilogue's two buffers and scales take the ring's place, and are larger than that of 128 rows
+  constexpr int LDS = GT && BM == 128 ? kGatedEpilogueLds : NS * STAGE;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
   __shared__ int32_t s_off[GR ? kMaxExperts + 1 : 2];
   __shared__ int64_t s_pref[GR ? kMaxExperts + 1 : 2];
   // MX: E8M0 scales, A rows then B rows. Either a ring of 4 stage pairs, one
@@ -292,7 +303,8 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
     uint32_t off[DH];
 #pragma unroll
     for (int d = 0; d < DH; ++d) {
-      const int r = 64 * wn + 16 * d + ld_row;
+      if (grp == 0 && d >= DA) continue;
+      const int r = (grp == 0 ? 16 * DA : 16 * DH) * wn + 16 * d + ld_row;
       const int c = ld_pch ^ ((r >> 2) & 3);
       if (GT && grp == 1) {
         // rows past F fetch the last; never stored
@@ -318,7 +330,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
         off[d] = (uint32_t)(rr * K32 + 16 * c);
       }
     }
-    const uint32_t part_lds = (grp == 0 ? 0u : (uint32_t)SA_BYTES) + (uint32_t)(wn * 4096);
+    const uint32_t part_lds = grp == 0 ? (uint32_t)(wn * DA * 1024) : (uint32_t)(SA_BYTES + wn * DH * 1024);
     // the lane's 16 bytes of the last stage lie past K: it loads the stage's first ones, and zeroes them
     const int32_t ld_c = 16 * (ld_pch ^ ((ld_row >> 2) & 3));
     const bool past = tail != 0 && ld_c >= tail;
@@ -343,7 +355,8 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
       const uint8_t* bk = base + s * sstride;
       const uint32_t back = GT && !PKB && past && s == nk - 1 ? (uint32_t)ld_c : 0u;
 #pragma unroll
-      for (int d = 0; d < DH; ++d) dma16(bk, off[d] - back, slot + (uint32_t)(d * 1024));
+      for (int d = 0; d < DH; ++d)
+        if (d < DA || grp != 0) dma16(bk, off[d] - back, slot + (uint32_t)(d * 1024));
       if constexpr (MXS) {
         const uint32_t o = sc_off + (uint32_t)(2 * s);  // byte 4 (s / 2) of the row
         if (scl16) {
@@ -468,8 +481,8 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
           }
           __builtin_amdgcn_sched_barrier(0);
         }
-        asm volatile("" ::"v"(ad[0][0]), "v"(ad[0][1]), "v"(ad[0][2]), "v"(ad[0][3]), "v"(ad[1][0]), "v"(ad[1][1]),
-                     "v"(ad[1][2]), "v"(ad[1][3]));
+        asm volatile("" ::"v"(ad[0][0]), "v"(ad[0][1]), "v"(ad[0][2]), "v"(ad[0][3]));
+        if constexpr (MI > 1) asm volatile("" ::"v"(ad[1][0]), "v"(ad[1][1]), "v"(ad[1][2]), "v"(ad[1][3]));
 #pragma unroll
         for (int j = 0; j < NI; ++j)
           asm volatile("" ::"v"(bd[j][0]), "v"(bd[j][1]), "v"(bd[j][2]), "v"(bd[j][3]));
@@ -508,7 +521,10 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
     // keeps the wait from taking one of stage u + 2's loads early, which cost
     // about a tenth of the MX GEMM's time on the Llama-4-style MoE shape)
     auto wait_next = [&](int64_t u) {
-      if (u + 3 < nk) {
+      if (DA != DH && grp == 0 && u + 2 < nk) {
+        if (u + 3 < nk) wait_vm_lgkm_and_barrier<2 * DA>();
+        else wait_vm_lgkm_and_barrier<DA>();
+      } else if (u + 3 < nk) {
         if (scl16) {
           if ((u & 7) == 5 || (u & 7) == 6) wait_vm_lgkm_and_barrier<2 * DH + 1>();
           else wait_vm_lgkm_and_barrier<2 * DH>();
@@ -524,7 +540,8 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
           if (past) {
             uint8_t* at = lds + (int)((nk - 1) & (NS - 1)) * STAGE + part_lds + 16 * lane;
 #pragma unroll
-            for (int d = 0; d < DH; ++d) *reinterpret_cast<uint4*>(at + d * 1024) = make_uint4(0, 0, 0, 0);
+            for (int d = 0; d < DH; ++d)
+              if (d < DA || grp != 0) *reinterpret_cast<uint4*>(at + d * 1024) = make_uint4(0, 0, 0, 0);
           }
         }
         wait_vm_lgkm_and_barrier<0>();
@@ -536,10 +553,12 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
     issue(1);
     if (nk >= 3) {
       issue(2);
-      if (scl16) wait_vm_lgkm_and_barrier<2 * DH>();
+      if (DA != DH && grp == 0) wait_vm_lgkm_and_barrier<2 * DA>();
+      else if (scl16) wait_vm_lgkm_and_barrier<2 * DH>();
       else wait_vm_lgkm_and_barrier<2 * DH + X>();
     } else {
-      wait_vm_lgkm_and_barrier<DH>();
+      if (DA != DH && grp == 0) wait_vm_lgkm_and_barrier<DA>();
+      else wait_vm_lgkm_and_barrier<DH>();
     }
     // both groups run the same loop, group 1 one phase behind: memory phase
     // (reads of stage u, loads of stage u + 3, own loads of stage u + 1
@@ -571,7 +590,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_fp8_pp(GemmParams p) {
     const float* SA = reinterpret_cast<const float*>(p.sa);
     const float* SB = reinterpret_cast<const float*>(p.sb);
     if constexpr (GT) {
-      gated_epilogue<GATE == kGateGelu, SK == kScaleRow>(p, ti, F, acc, lds, wave, lane);
+      gated_epilogue<GATE == kGateGelu, SK == kScaleRow, MI>(p, ti, F, acc, lds, wave, lane);
       continue;
     }
     float cs[NI];

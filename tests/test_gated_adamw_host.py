@@ -39,8 +39,8 @@ GATED_REFUSALS = [
     (dict(packed=1, K=64), f.ERR_ALIGNMENT), (dict(packed=1, F=24), f.ERR_ALIGNMENT),
     (dict(a=FAKE + 8), f.ERR_ALIGNMENT), (dict(b=FAKE + 8), f.ERR_ALIGNMENT), (dict(a_inv=FAKE + 2), f.ERR_ALIGNMENT),
     (dict(b_inv=FAKE + 1), f.ERR_ALIGNMENT), (dict(gu=FAKE + 1), f.ERR_ALIGNMENT), (dict(out=FAKE + 1), f.ERR_ALIGNMENT),
-    (dict(M=1 << 31), f.ERR_UNSUPPORTED), (dict(F=1 << 30), f.ERR_UNSUPPORTED),
-    (dict(packed=1, F=1 << 22), f.ERR_UNSUPPORTED), (dict(packed=1, F=1 << 15, K=1 << 15), f.ERR_UNSUPPORTED),
+    (dict(M=1 << 31), f.ERR_UNSUPPORTED), (dict(F=(1 << 21) + 1), f.ERR_UNSUPPORTED),
+    (dict(packed=1, F=1 << 21, K=1024), f.ERR_UNSUPPORTED), (dict(packed=1, F=1 << 15, K=1 << 15), f.ERR_UNSUPPORTED),
 ]
 
 
