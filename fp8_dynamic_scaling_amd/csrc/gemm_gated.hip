@@ -2,15 +2,15 @@
 // dense, and grouped over a device offset tensor.
 //
 // Both projections are one product with N = 2F; the tile walk, the main loops, the scales and the packed
-// layouts are those of the plain products (gemm_pp.hpp, gemm_generic.hpp). What differs is which rows of B
+// layouts are those of the plain products (gemm_fp8_fast.hip, gemm_fp8.hip). What differs is which rows of B
 // a tile holds, the gate and up rows of the same features, so that both end up in the same lane, and the
 // epilogue, which forms act(g) u in fp32 and rounds it once. The projections themselves are written only
 // for a backward: without them F values a row leave the kernel instead of 2F, and no pass reads them again.
 #include <algorithm>
 #include <cmath>
 
+#include "gemm_gated_pp.hpp"
 #include "gemm_generic.hpp"
-#include "gemm_pp.hpp"
 
 namespace fp8dyn {
 
@@ -280,7 +280,7 @@ hipError_t launch_pp_rows(const GatedMmArgs& g) {
   int64_t grid = device_cus();
   if (tiles < grid) grid = tiles;
   if (grid >= kNumXcd) grid -= grid % kNumXcd;
-  hipLaunchKernelGGL((k_gemm_fp8_pp<false, false, SK, false, GR, PKB, EX, GATE, BM>), dim3((unsigned)grid), dim3(512),
+  hipLaunchKernelGGL((k_gated_pp<SK, GR, PKB, EX, GATE, BM>), dim3((unsigned)grid), dim3(512),
                      0, g.stream, p);
   return hipGetLastError();
 }

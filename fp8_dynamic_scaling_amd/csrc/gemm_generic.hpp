@@ -12,7 +12,7 @@ namespace fp8dyn {
 // of every lane feed instruction q on both operands. MX scales are powers of
 // two and are folded into the decode: a lane's low 16 bytes lie in 32-element
 // group g / 2 of the 128-deep step and its high 16 bytes in group 2 + g / 2.
-// GATE: a gated product (see gemm_pp.hpp): N = 2F, a tile is BM x BN / 2 features, and of
+// GATE: a gated product (see gemm_gated_pp.hpp): N = 2F, a tile is BM x BN / 2 features, and of
 // the TN rows of B that a wave has in LDS the first half are gate rows, the second the up
 // rows of the same features.
 template <int BM, int BN, int WM, int WN, bool AE5, bool BE5, int SK, bool OF32, bool EX = false,
