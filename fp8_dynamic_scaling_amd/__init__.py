@@ -625,6 +625,14 @@ def fp8_moe_few(x, ids, weights, w13, w13_inv, w2, w2_inv, fmt, out, ws, packed=
 
 # ---- gated feed-forward block ---------------------------------------------------------
 
+def _gated_operands(fn, b, gu, M, F, K, E):
+    """b holds E experts' [2F][K] codes and nothing else; gu is [M][2F] or None."""
+    if b.nbytes != 2 * E * F * K:
+        raise ValueError(f"{fn}: b must hold the {2 * E * F * K} codes of [{E}][{2 * F}][{K}] (got {tuple(b.shape)})")
+    if gu is not None and tuple(gu.shape) != (M, 2 * F):
+        raise ValueError(f"{fn}: gu must be [{M}][{2 * F}] (got {tuple(gu.shape)})")
+
+
 def fp8_gated_mm(a, b, fmt, scaling, a_inv, b_inv, act, gu, out, packed=False, use_fast_accum=True, stream=None):
     """out [M][F] = act(g) * u in bf16 for the projections [g | u] = a b^T of a [M][K] and b (the codes of
     [2F][K], gate rows first); gu [M][2F]: the projections in bf16, or None. packed: b k-packed."""
@@ -634,6 +642,7 @@ def fp8_gated_mm(a, b, fmt, scaling, a_inv, b_inv, act, gu, out, packed=False, u
     if out.dim() != 2 or out.shape[0] != M:
         raise ValueError(f"{fn}: out must be [M][F]")
     F = out.shape[1]
+    _gated_operands(fn, b, gu, M, F, K, 1)
     row = scaling == SCALE_ROW
     dev = _args(fn, ("a", a, M * K, 1), ("b", b, 2 * F * K, 1), ("a_inv", a_inv, K and 4 * (M if row else 1), f32),
                 ("b_inv", b_inv, K and 4 * (2 * F if row else 1), f32), ("gu", gu, gu is not None and 4 * M * F, bf),
@@ -651,9 +660,10 @@ def fp8_grouped_gated_mm(a, b, fmt, a_inv, b_inv, offsets, act, gu, out, packed=
     M, K = a.shape
     if out.dim() != 2 or out.shape[0] != M:
         raise ValueError(f"{fn}: out must be [Mtot][F]")
-    if offsets.dim() != 1 or offsets.numel() < 2:
+    if offsets is None or offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError(f"{fn}: offsets must hold E + 1 entries")
     F, E = out.shape[1], offsets.numel() - 1
+    _gated_operands(fn, b, gu, M, F, K, E)
     dev = _args(fn, ("a", a, M * K, 1), ("b", b, 2 * E * F * K, 1), ("a_inv", a_inv, K and 4 * M, f32),
                 ("b_inv", b_inv, K and 8 * E * F, f32), ("offsets", offsets, 4 * (E + 1), torch.int32),
                 ("gu", gu, gu is not None and 4 * M * F, bf), ("out", out, 2 * M * F, bf))
@@ -668,6 +678,9 @@ def fp8_gated_bwd(dh, gu, act, fmt, eps, dgu, q, scale, inv_scale=None, h=None, 
     fn, bf, f32 = "fp8_gated_bwd", torch.bfloat16, torch.float32
     M, F = dh.shape
     n = 2 * M * F
+    for name, t, shape in (("gu", gu, (M, 2 * F)), ("dgu", dgu, (M, 2 * F)), ("q", q, (M, 2 * F)), ("h", h, (M, F))):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{fn}: {name} must be {list(shape)} (got {tuple(t.shape)})")
     dev = _args(fn, ("dh", dh, n, bf), ("gu", gu, 2 * n, bf), ("dgu", dgu, dgu is not None and 2 * n, bf),
                 ("q", q, q is not None and n, 1), ("scale", scale, (q is not None or scale is not None) and 4 * M, f32),
                 ("inv_scale", inv_scale, inv_scale is not None and 4 * M, f32), ("h", h, h is not None and n, bf))
@@ -725,9 +738,11 @@ def fp8_adamw(params, grads, exp_avgs, exp_avg_sqs, lr, beta1, beta2, eps, weigh
     if masters is not None:
         lists.append(("masters", masters, f32, sizes))
     dev = _tensor_lists(fn, T, lists)
-    columns = [map(T.data_ptr, ts) for _, ts, _, _ in lists]
+    columns = [list(map(T.data_ptr, ts)) for _, ts, _, _ in lists]
     none = (0,) * count
     p, g, m, v = columns[:4]
+    if len(set(p)) != count and len(set(filter(None, p))) != sum(map(bool, p)):
+        raise ValueError(f"{fn}: a parameter is in the list twice")
     ms, vs = columns[4:6] if mx else (none, none)
     w = columns[-1] if masters is not None else none
     table = array("q", chain.from_iterable(zip(p, g, m, v, ms, vs, w, sizes)))

@@ -13,9 +13,16 @@ namespace fp8dyn {
 // comes out as zero.
 constexpr float kGeluC = 1.5957691216057308f, kGeluA = 0.044715f;
 
+// GELU's cube and square would leave fp32 for gates past 10^12 and 10^19; beyond +-64 its s is 0 or 1 either way.
+__device__ __forceinline__ float gelu_range(float x) { return __builtin_amdgcn_fmed3f(x, -64.0f, 64.0f); }
+
 template <bool GELU>
 __device__ __forceinline__ float gate_sigmoid(float x) {
-  const float z = GELU ? kGeluC * (x + kGeluA * x * x * x) : x;
+  float z = x;
+  if constexpr (GELU) {
+    const float c = gelu_range(x);
+    z = kGeluC * (c + kGeluA * c * c * c);
+  }
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
 
@@ -28,7 +35,11 @@ __device__ __forceinline__ float gate_act(float x) {
 template <bool GELU>
 __device__ __forceinline__ void gate_act_d(float x, float& a, float& da) {
   const float s = gate_sigmoid<GELU>(x);
-  const float dz = GELU ? kGeluC * (1.0f + 3.0f * kGeluA * x * x) : 1.0f;
+  float dz = 1.0f;
+  if constexpr (GELU) {
+    const float c = gelu_range(x);
+    dz = kGeluC * (1.0f + 3.0f * kGeluA * c * c);
+  }
   a = x * s;
   da = s + a * (1.0f - s) * dz;
 }

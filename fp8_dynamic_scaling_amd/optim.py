@@ -60,6 +60,10 @@ class AdamW(torch.optim.Optimizer):
             if not p.is_contiguous():
                 raise ValueError("AdamW: parameters must be contiguous")
 
+    def __getstate__(self):  # the base class keeps its own three attributes only
+        own = ("state_bits", "master_weights", "capturable", "seed", "max_norm", "grad_norm", "_mul")
+        return {**super().__getstate__(), **{k: getattr(self, k) for k in own}}
+
     @property
     def _counts_on_device(self) -> bool:
         return self.capturable or self.max_norm is not None

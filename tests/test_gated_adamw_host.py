@@ -270,3 +270,33 @@ def test_optimizer_loads_states_as_they_were(kw):
                 assert (torch.equal(v, w) and v.dtype == w.dtype) if torch.is_tensor(v) else v == w
             steps.append(b.state[q]["step"])
         assert int(steps[0]) == 9 and (steps[0] is steps[1] if kw else True)
+
+
+def test_optimizer_copies():
+    import copy
+    from fp8_dynamic_scaling_amd.optim import AdamW
+    a = AdamW([_bf16(5, 7), _bf16(3)], state_bits=8, max_norm=2.0, seed=9)
+    for p in a.param_groups[0]["params"]:
+        a._new_state(p)
+    b = copy.deepcopy(a)
+    assert (b.state_bits, b.max_norm, b.seed, b.capturable) == (8, 2.0, 9, False)
+    p, q = b.param_groups[0]["params"]
+    assert b.state[p]["step"] is b.state[q]["step"] and b.state[p]["exp_avg"].dtype == torch.uint8
+    b.step()
+
+
+def test_binding_refuses_shapes():
+    bf = dict(dtype=torch.bfloat16)
+    x, q = torch.zeros(4, 48, **bf), torch.zeros(4, 128, dtype=torch.uint8)
+    b, inv = torch.zeros(96, 128, dtype=torch.uint8), torch.zeros(96)
+    mm = lambda b, gu, out: f.fp8_gated_mm(q, b, f.E4M3_NATIVE, f.SCALE_ROW, inv, inv, f.ACT_SILU, gu, out)  # noqa: E731
+    with pytest.raises(ValueError, match="codes of"):
+        mm(torch.zeros(96, 256, dtype=torch.uint8), None, x)
+    with pytest.raises(ValueError, match="gu must be"):
+        mm(b, torch.zeros(8, 48, **bf), x)
+    with pytest.raises(ValueError, match=r"out must be"):
+        mm(b, None, torch.zeros(3, 48, **bf))
+    with pytest.raises(ValueError, match="offsets must"):
+        f.fp8_grouped_gated_mm(q, b, f.E4M3_NATIVE, inv, inv, None, f.ACT_SILU, None, x)
+    with pytest.raises(ValueError, match="gu must be"):
+        f.fp8_gated_bwd(x, x, f.ACT_SILU, f.E5M2_NATIVE, 1e-12, None, None, None)

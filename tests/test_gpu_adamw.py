@@ -287,6 +287,38 @@ def test_stochastic_rounding_is_right_in_the_mean():
         assert abs(float(got.mean()) - value) <= 6 * 0.5 * spacing / math.sqrt(got.numel()) + 1e-6 * abs(value)
 
 
+def test_adamw_past_32_bits():
+    """A tensor of more than 2^31 elements: its last ones as those of a short tensor of the same values."""
+    f = lib()
+    n, k = (1 << 31) + 4096 + 77, 4096 + 77
+    short = make([k], True, True, False, True, seed=1)
+    long = {}
+    for key, big in (("params", n), ("grads", n), ("m", n), ("v", n), ("ms", -(-n // 32)), ("vs", -(-n // 32))):
+        t = short[key][0]
+        x = torch.zeros(big, dtype=t.dtype, device="cuda")
+        x[x.numel() - t.numel():] = t
+        long[key] = [x]
+    long["masters"] = None
+    step(f, short, 3)
+    step(f, long, 3)
+    for key in ("params", "m", "v", "ms", "vs"):
+        t = short[key][0]
+        assert torch.equal(long[key][0][-t.numel():].view(torch.uint8), t.view(torch.uint8)), key
+    norm, mul = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+    ws = torch.empty(f.fp8_grad_norm_ws_bytes(long["grads"]), dtype=torch.uint8, device="cuda")
+    f.fp8_grad_norm(long["grads"], norm, mul, ws)
+    want = float(short["grads"][0].double().norm())
+    assert abs(float(norm) - want) <= 2.0 ** -23 * want
+
+
+def test_adamw_refuses_a_parameter_twice():
+    f = lib()
+    s = make([40], True, True, False, False)
+    two = {k: v and v * 2 for k, v in s.items()}
+    with pytest.raises(ValueError, match="twice"):
+        step(f, two, 1)
+
+
 # ---- norm ------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("sizes", [[1], [0, 5], SIZES, [32767, 32768, 32769, 200001], [11] * 300])

@@ -250,3 +250,64 @@ def test_gated_bwd_empty_rows():
     f.fp8_gated_bwd(e, e, f.ACT_SILU, f.E5M2_NATIVE, 1e-12, None, torch.empty((3, 0), dtype=torch.uint8, device="cuda"),
                     sc, inv)
     assert (sc == np.float32(57344.0 / 1e-12)).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gated_bwd_gates_far_out(act):
+    """Gates up to bf16's largest: act' is 1 or 0, nothing overflows on the way."""
+    f = lib()
+    g = torch.tensor([[3e38, 1e20, 1e13, 100.0, -100.0, -1e13, -1e20, -3e38]]).to(torch.bfloat16)
+    u = torch.full_like(g, 0.5)
+    dh = torch.ones_like(g)
+    dgu, q, sc, inv, h = run_bwd(f, dh.cuda(), torch.cat([g, u], 1).cuda(), act, False)
+    dgu = dgu.cpu().float()
+    assert torch.equal(dgu[0, :4], torch.full((4,), 0.5)) and (dgu[0, 4:8] == 0).all()
+    assert torch.equal(dgu[0, 8:12], g[0, :4].float()) and (dgu[0, 12:] == 0).all()
+    assert torch.isfinite(inv).all()
+
+
+def test_formats_that_are_refused():
+    f = lib()
+    out = torch.empty((2, 16), dtype=torch.bfloat16, device="cuda")
+    a, b = (torch.zeros((n, 128), dtype=torch.uint8, device="cuda") for n in (2, 32))
+    inv = torch.ones(32, device="cuda")
+    for fmt in (f.E5M2_NATIVE, f.E4M3FNUZ):
+        with pytest.raises(f.Fp8Error) as e:
+            f.fp8_gated_mm(a, b, fmt, f.SCALE_ROW, inv, inv, f.ACT_SILU, None, out)
+        assert e.value.status == f.ERR_UNSUPPORTED
+    dh = torch.zeros((2, 16), dtype=torch.bfloat16, device="cuda")
+    gu = torch.zeros((2, 32), dtype=torch.bfloat16, device="cuda")
+    q = torch.empty((2, 32), dtype=torch.uint8, device="cuda")
+    with pytest.raises(f.Fp8Error) as e:
+        f.fp8_gated_bwd(dh, gu, f.ACT_SILU, f.E5M2FNUZ, 1e-12, None, q, inv[:2].clone())
+    assert e.value.status == f.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_past_32_bits_of_elements(grouped):
+    """Projections of more than 2^31 elements: rows at both ends, forward and backward."""
+    f = lib()
+    M, F, K = 76000, 14336, 128
+    g = torch.Generator().manual_seed(4)
+    a, ai, av = codes(g, (M, K), 1.0)
+    b, bi, bv = codes(g, (2 * F, K), 2.0 / K ** 0.5)
+    out = torch.empty((M, F), dtype=torch.bfloat16, device="cuda")
+    gu = torch.empty((M, 2 * F), dtype=torch.bfloat16, device="cuda")
+    assert gu.numel() > 1 << 31
+    if grouped:
+        off = torch.tensor([0, 70000, M], dtype=torch.int32, device="cuda")
+        bb, bbi = torch.stack([b, b]).cuda(), torch.stack([bi, bi]).cuda()
+        f.fp8_grouped_gated_mm(a.cuda(), bb, f.E4M3_NATIVE, ai.cuda(), bbi, off, f.ACT_SILU, gu, out)
+    else:
+        f.fp8_gated_mm(a.cuda(), b.cuda(), f.E4M3_NATIVE, f.SCALE_ROW, ai.cuda(), bi.cuda(), f.ACT_SILU, gu, out)
+    rows = torch.tensor([0, 1, M // 2, 74899, 74900, M - 2, M - 1])
+    check(out[rows.cuda()].cpu(), gu[rows.cuda()].cpu(), av[rows], bv, "silu", True, "far rows")
+    if grouped:
+        return
+    q, sc = torch.empty((M, 2 * F), dtype=torch.uint8, device="cuda"), torch.empty(M, device="cuda")
+    keep = gu[rows.cuda()].clone()
+    dh = out  # any gradient will do
+    f.fp8_gated_bwd(dh, gu, f.ACT_SILU, f.E5M2_NATIVE, 1e-12, gu, q, sc)
+    few = run_bwd(f, dh[rows.cuda()].contiguous(), keep, "silu", True)
+    assert torch.equal(gu[rows.cuda()].view(torch.int16), few[0].view(torch.int16))
+    assert torch.equal(q[rows.cuda()], few[1].view(torch.uint8)) and torch.equal(sc[rows.cuda()], few[2])
