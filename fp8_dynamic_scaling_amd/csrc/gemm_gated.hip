@@ -203,8 +203,12 @@ __global__ __launch_bounds__(64 * WV) void k_gated_few(GemmParams p) {
 template <int GATE, int SK>
 hipError_t launch_few(const GatedMmArgs& g) {
   constexpr bool ROW = SK == kScaleRow;
-  const int mt = g.M <= 16 ? 1 : g.M <= 32 ? 2 : 4;
-  const int64_t nf = (g.F + 15) / 16, nm = (g.M + 16 * mt - 1) / (16 * mt);
+  const int64_t nf = (g.F + 15) / 16;
+  auto fits = [&](int m) { return nf * ((g.M + 16 * m - 1) / (16 * m)) <= 256; };
+  // fewer rows a workgroup where that many still run at once (40 x 512 x 4096: 64 rows 11.0 us, 32 7.8, 16 6.4;
+  // 333 x 1040 x 720, more than run at once, 8.3, 8.2 and 10.7)
+  const int mt = g.M <= 16 || fits(1) ? 1 : g.M <= 32 || fits(2) ? 2 : 4;
+  const int64_t nm = (g.M + 16 * mt - 1) / (16 * mt);
   // eight waves for K where few registers or few workgroups let them all run
   const bool eight = mt == 1 || nf * nm <= 256;
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(65535, ((int64_t)1 << 22) / nf));  // of one grid
