@@ -18,6 +18,16 @@
 // after some ten steps. Stochastic rounding (a seed other than 0) moves it by the right
 // amount in the mean: 16 random bits below the code's last place, from Wellons' 32-bit
 // integer hash "lowbias32" of (seed, tensor, step, element).
+//
+// The step is bound by HBM: 28 bytes an element with 32-bit states and an fp32 copy, 10.1 with
+// 8-bit states and bf16 parameters; the tensors' table travels in the kernel's arguments, so that
+// nothing is copied to the device first. Measured, 176 M elements in five tensors: 32-bit 790 to
+// 805 us (6.1 to 6.2 TB/s; a large torch copy reaches 5.3), 8-bit 314 us (5.7 TB/s; to nearest
+// 290). Loads and stores stream (non-temporal): plain loads 879 and 328 us, plain stores of the
+// 8-bit form 326. The 8-bit step had been bound by its instructions: 377 us with codes scaled and
+// rounded by integer steps and the library's square root, 343 with the scaled converts and a root
+// of seven instructions (below), 315 with two pieces a workgroup, the second's loads ahead.
+// Held to six waves a SIMD it spills: 392.
 #include <cmath>
 #include <type_traits>
 
@@ -42,6 +52,8 @@ int64_t norm_chunk(int64_t total) {
   return c < 2048 ? 2048 : c > 32768 ? 32768 : c;
 }
 
+// Pieces of a workgroup: two with 8-bit states (one 330 us, four 322), one with 32-bit ones (two 847 us,
+// four 880, eight 900: workgroups that run together then reach over more of memory).
 int step_iters(bool eight, int64_t pieces) { return eight && pieces >= 8192 ? 2 : 1; }
 
 struct StepTensor {
@@ -79,7 +91,7 @@ struct NormArgs {
   int32_t count, chunk;
   double* part;
 };
-static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
+static_assert(sizeof(NormArgs) <= 4000, "kernel arguments, with NormOut");
 
 __host__ __device__ __forceinline__ uint32_t lowbias32(uint32_t x) {
   x ^= x >> 16;
@@ -213,7 +225,7 @@ __device__ __forceinline__ void decode8(uint2 c, uint32_t e8, float* x) {
 
 // sqrt(v), correctly rounded for v >= 2^-100 (compared with the library's root for every mantissa, at both
 // parities of the exponent); zero below, where the remainder would lose bits. Seven instructions for the 15
-// of the root that covers everything: with 8-bit states the step is bound by its instructions.
+// of the root that covers everything.
 __device__ __forceinline__ float root(float v) {
   const float y = __builtin_amdgcn_rsqf(v), g = v * y;
   const float r = __builtin_fmaf(__builtin_fmaf(-g, g, v), 0.5f * y, g);
@@ -385,45 +397,57 @@ __global__ __launch_bounds__(256) void k_adamw(const StepArgs a) {
   }
 }
 
-// One partial sum of squares a workgroup, in 64 bits: a thread's elements in order, then a tree.
+// The part of a piece's sum of squares that thread `tid` of NT takes, in 64 bits, in order.
+template <int NT>
+__device__ __forceinline__ double square_sum(const NormArgs& a, int32_t chunk, int tid) {
+  const int t = tensor_of(a, chunk);
+  const int64_t n = a.n[t], begin = (int64_t)(chunk - a.first[t]) * a.chunk;
+  const int64_t end = begin + a.chunk < n ? begin + a.chunk : n;
+  const bool f32 = (a.f32[t >> 5] >> (t & 31)) & 1u;
+  const bool vec = ((uintptr_t)a.g[t] & 15) == 0;
+  double s = 0.0;
+  const int64_t whole = vec ? begin + ((end - begin) & ~(int64_t)7) : begin;
+  if (f32) {
+    const float* g = reinterpret_cast<const float*>(a.g[t]);
+    for (int64_t i = begin + 4 * tid; i < whole; i += 4 * NT) {
+      const uint4 w = ld_nt16(g + i);
+      const double x0 = __uint_as_float(w.x), x1 = __uint_as_float(w.y);
+      const double x2 = __uint_as_float(w.z), x3 = __uint_as_float(w.w);
+      s += x0 * x0 + x1 * x1 + x2 * x2 + x3 * x3;
+    }
+    for (int64_t i = whole + tid; i < end; i += NT) s += (double)g[i] * (double)g[i];
+  } else {
+    const uint16_t* g = reinterpret_cast<const uint16_t*>(a.g[t]);
+    for (int64_t i = begin + 8 * tid; i < whole; i += 8 * NT) {
+      const uint4 w = ld_nt16(g + i);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const double x = bf16_lo(u[j]), y = bf16_hi(u[j]);
+        s += x * x + y * y;
+      }
+    }
+    for (int64_t i = whole + tid; i < end; i += NT) {
+      const double x = __uint_as_float((uint32_t)g[i] << 16);
+      s += x * x;
+    }
+  }
+  return s;
+}
+
+__device__ __forceinline__ double wave_sum64(double s) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  return s;
+}
+
+// One partial sum of squares a workgroup: a thread's elements in order, then a tree. HBM-bound: 176 M bf16
+// values (352 MB) in 54 us, and 4 us for k_grad_norm, 6.0 TB/s together.
 __global__ __launch_bounds__(256) void k_grad_sq(const NormArgs a) {
   __shared__ double red[4];
   const int32_t chunks = a.first[a.count];
   for (int32_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-    const int t = tensor_of(a, chunk);
-    const int64_t n = a.n[t], begin = (int64_t)(chunk - a.first[t]) * a.chunk;
-    const int64_t end = begin + a.chunk < n ? begin + a.chunk : n;
-    const bool f32 = (a.f32[t >> 5] >> (t & 31)) & 1u;
-    const bool vec = ((uintptr_t)a.g[t] & 15) == 0;
-    double s = 0.0;
-    const int64_t whole = vec ? begin + ((end - begin) & ~(int64_t)7) : begin;
-    if (f32) {
-      const float* g = reinterpret_cast<const float*>(a.g[t]);
-      for (int64_t i = begin + 4 * threadIdx.x; i < whole; i += 4 * 256) {
-        const uint4 w = ld_nt16(g + i);
-        const double x0 = __uint_as_float(w.x), x1 = __uint_as_float(w.y);
-        const double x2 = __uint_as_float(w.z), x3 = __uint_as_float(w.w);
-        s += x0 * x0 + x1 * x1 + x2 * x2 + x3 * x3;
-      }
-      for (int64_t i = whole + threadIdx.x; i < end; i += 256) s += (double)g[i] * (double)g[i];
-    } else {
-      const uint16_t* g = reinterpret_cast<const uint16_t*>(a.g[t]);
-      for (int64_t i = begin + 8 * threadIdx.x; i < whole; i += 8 * 256) {
-        const uint4 w = ld_nt16(g + i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const double x = bf16_lo(u[j]), y = bf16_hi(u[j]);
-          s += x * x + y * y;
-        }
-      }
-      for (int64_t i = whole + threadIdx.x; i < end; i += 256) {
-        const double x = __uint_as_float((uint32_t)g[i] << 16);
-        s += x * x;
-      }
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+    const double s = wave_sum64(square_sum<256>(a, chunk, threadIdx.x));
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
     __syncthreads();
     if (threadIdx.x == 0) a.part[chunk] = (red[0] + red[1]) + (red[2] + red[3]);
@@ -431,26 +455,44 @@ __global__ __launch_bounds__(256) void k_grad_sq(const NormArgs a) {
   }
 }
 
-__global__ __launch_bounds__(1024) void k_grad_norm(const double* __restrict__ part, int64_t n, double grad_scale,
-                                                    double max_norm, float* norm, float* mul, int32_t* step) {
+struct NormOut {
+  double grad_scale, max_norm;
+  float* norm;
+  float* mul;
+  int32_t* step;
+};
+
+// The sum over 1024 threads, and what follows from it.
+__device__ __forceinline__ void finish_norm(double s, const NormOut& o) {
   __shared__ double red[16];
-  double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  s = wave_sum64(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    s = red[0];
-    for (int w = 1; w < 16; ++w) s += red[w];
-    const double x = sqrt(s) * fabs(grad_scale);
-    const float xf = (float)x;
-    if (norm) *norm = xf;
-    const bool fine = fabsf(xf) <= 3.402823466e38f;  // not for NaN
-    const double clip = max_norm / (x + 1e-6);
-    if (mul) *mul = fine ? (float)(clip < 1.0 ? grad_scale * clip : grad_scale) : __uint_as_float(0x7fc00000u);
-    if (step && fine) *step += 1;
-  }
+  if (threadIdx.x != 0) return;
+  s = red[0];
+  for (int w = 1; w < 16; ++w) s += red[w];
+  const double x = sqrt(s) * o.grad_scale;
+  const float xf = (float)x;
+  if (o.norm) *o.norm = xf;
+  const bool fine = fabsf(xf) <= 3.402823466e38f;  // not for NaN
+  const double clip = o.max_norm / (x + 1e-6);
+  if (o.mul) *o.mul = fine ? (float)(clip < 1.0 ? o.grad_scale * clip : o.grad_scale) : __uint_as_float(0x7fc00000u);
+  if (o.step && fine) *o.step += 1;
+}
+
+__global__ __launch_bounds__(1024) void k_grad_norm(const double* __restrict__ part, int64_t n, const NormOut o) {
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
+  finish_norm(s, o);
+}
+
+// Both in one launch, for tables of few pieces: a wavefront takes every sixteenth.
+__global__ __launch_bounds__(1024) void k_grad_norm_small(const NormArgs a, const NormOut o) {
+  const int32_t chunks = a.first[a.count];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  double s = 0.0;
+  for (int32_t chunk = wave; chunk < chunks; chunk += 16) s += square_sum<64>(a, chunk, threadIdx.x & 63);
+  finish_norm(s, o);
 }
 
 template <bool P32, bool G32, bool MASTER>
@@ -525,24 +567,40 @@ hipError_t launch_adamw(const AdamwArgs& a) {
   return flush();
 }
 
-int64_t grad_norm_partials(const fp8_grad_tensor* tensors, int32_t count) {
-  int64_t total = 0, chunks = 0;
+// Pieces of a table of tensors, and the elements of one; with at most kSmallNorm pieces (and one launch's tensors)
+// one workgroup takes all: it saves a launch, some 3 us of the host's and as much of the device's time.
+constexpr int64_t kSmallNorm = 64;
+struct NormPlan {
+  int64_t chunk, chunks, tensors;
+  bool small() const { return chunks <= kSmallNorm && tensors <= kNormTensorsALaunch; }
+};
+static NormPlan norm_plan(const fp8_grad_tensor* tensors, int32_t count) {
+  int64_t total = 0;
+  NormPlan p{0, 0, 0};
   for (int32_t i = 0; i < count; ++i) total += tensors[i].n;
-  const int64_t chunk = norm_chunk(total);
-  for (int32_t i = 0; i < count; ++i) chunks += (tensors[i].n + chunk - 1) / chunk;
-  return chunks;
+  p.chunk = norm_chunk(total);
+  for (int32_t i = 0; i < count; ++i) {
+    p.chunks += (tensors[i].n + p.chunk - 1) / p.chunk;
+    p.tensors += tensors[i].n > 0;
+  }
+  return p;
+}
+
+int64_t grad_norm_partials(const fp8_grad_tensor* tensors, int32_t count) {
+  const NormPlan p = norm_plan(tensors, count);
+  return p.small() ? 0 : p.chunks;
 }
 
 hipError_t launch_grad_norm(const GradNormArgs& a) {
+  const NormPlan plan = norm_plan(a.tensors, a.count);
+  const NormOut out{a.grad_scale, a.max_norm, a.norm, a.mul, a.step};
   NormArgs s;
-  int64_t chunks = 0, before = 0, total = 0;
-  for (int32_t i = 0; i < a.count; ++i) total += a.tensors[i].n;
-  const int64_t chunk = norm_chunk(total);
-  s.chunk = (int32_t)chunk;
+  int64_t chunks = 0, before = 0;
+  s.chunk = (int32_t)plan.chunk;
   s.count = 0;
+  s.first[0] = 0;
   auto flush = [&]() -> hipError_t {
     if (s.count == 0) return hipSuccess;
-    s.first[s.count] = (int32_t)chunks;
     s.part = a.ws + before;
     const unsigned grid = (unsigned)(chunks < kMaxGrid256 ? chunks : kMaxGrid256);
     hipLaunchKernelGGL(k_grad_sq, dim3(grid), dim3(256), 0, a.stream, s);
@@ -554,7 +612,7 @@ hipError_t launch_grad_norm(const GradNormArgs& a) {
   for (int32_t i = 0; i < a.count; ++i) {
     const fp8_grad_tensor& t = a.tensors[i];
     if (t.n == 0) continue;
-    const int64_t c = (t.n + chunk - 1) / chunk;
+    const int64_t c = (t.n + plan.chunk - 1) / plan.chunk;
     if (s.count == kNormTensorsALaunch || chunks + c > INT32_MAX) {
       const hipError_t e = flush();
       if (e != hipSuccess) return e;
@@ -565,11 +623,15 @@ hipError_t launch_grad_norm(const GradNormArgs& a) {
     s.n[s.count] = t.n;
     s.first[s.count++] = (int32_t)chunks;
     chunks += c;
+    s.first[s.count] = (int32_t)chunks;
+  }
+  if (plan.small()) {
+    hipLaunchKernelGGL(k_grad_norm_small, dim3(1), dim3(1024), 0, a.stream, s, out);
+    return hipGetLastError();
   }
   const hipError_t e = flush();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_grad_norm, dim3(1), dim3(1024), 0, a.stream, a.ws, before, a.grad_scale, a.max_norm, a.norm,
-                     a.mul, a.step);
+  hipLaunchKernelGGL(k_grad_norm, dim3(1), dim3(1024), 0, a.stream, a.ws, before, out);
   return hipGetLastError();
 }
 

@@ -651,8 +651,8 @@ typedef struct fp8_grad_tensor {
  * norm is not finite, which skips that step; *step is increased by one if it is finite. norm, mul
  * [1] fp32 and step [1] int32 on the device, each may be NULL. grad_scale (what undoes a loss
  * scale; 1 for none) finite and > 0; max_norm > 0, infinity for no clipping. ws:
- * fp8_grad_norm_ws_bytes() bytes, 8-byte aligned, content on entry of no matter; calls that may run
- * at the same time need one each. count = 0 is the norm 0. */
+ * fp8_grad_norm_ws_bytes() bytes (0 for small tables), 8-byte aligned, content on entry of no matter;
+ * calls that may run at the same time need one each. count = 0 is the norm 0. */
 FP8DYN_API fp8_status fp8_grad_norm(const fp8_grad_tensor* tensors, int32_t count, double grad_scale,
                                     double max_norm, float* norm, float* mul, int32_t* step, void* ws,
                                     size_t ws_bytes, void* stream);

@@ -132,7 +132,7 @@ def test_adamw_refusals(lib, tensors, kw, want):
     assert _adamw(lib, tensors, **kw) == want
 
 
-def _norm(lib, rows=((FAKE, 100, f.OUT_BF16),), **kw):
+def _norm(lib, rows=((FAKE, 1 << 20, f.OUT_BF16),), **kw):
     table = (ctypes.c_int64 * max(1, 3 * len(rows)))(*[x for r in rows for x in r])
     a = dict(table=table, count=len(rows), scale=1.0, max_norm=1.0, norm=FAKE, mul=FAKE, step=None, ws=FAKE, ws_bytes=1 << 20,
              stream=None)
@@ -156,9 +156,14 @@ def test_grad_norm_refusals(lib, kw, want):
 
 
 def test_grad_norm_workspace(lib):
-    rows = ((FAKE, 1, 0), (FAKE, 0, 0), (FAKE, 2049, 1))  # a partial sum of 8 bytes for each started piece of 2048
-    table = (ctypes.c_int64 * 9)(*[x for r in rows for x in r])
-    assert lib.fp8_grad_norm_ws_bytes(table, 3) == 8 * 3
+    # a partial sum of 8 bytes for each started piece of 2048, from 65 pieces or 129 tensors on
+    def need(*sizes):
+        table = (ctypes.c_int64 * (3 * len(sizes)))(*[x for n in sizes for x in (FAKE, n, 0)])
+        return lib.fp8_grad_norm_ws_bytes(table, len(sizes))
+
+    assert need(1, 0, 2049) == 0
+    assert need(64 * 2048, 0) == 0 and need(64 * 2048, 1) == 8 * 65 and need(64 * 2048 + 1) == 8 * 65
+    assert need(*[1] * 64) == 0 and need(*[1] * 65) == 8 * 65
     assert lib.fp8_grad_norm_ws_bytes(None, 0) == 0
     assert lib.fp8_grad_norm_ws_bytes(None, 2) == 0
 
