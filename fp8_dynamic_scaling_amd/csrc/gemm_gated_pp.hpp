@@ -126,10 +126,14 @@ __device__ __forceinline__ void gated_epilogue(const GemmParams& p, const TileIn
 //    groups of four neighbouring features.
 //  - BM = 256, 128 or 64 rows, for shapes of few tiles and experts of few rows: a group's waves then have half as
 //    many rows each and load half as much of A.
+//  - The loop's last three phases, which load nothing and wait in steps, are a loop of their own: with the shorter
+//    tiles a phase has few products, and its branches showed (512 x 2048 x 4096 26.7 -> 20.1 us, 1024 x 2048 x 2048
+//    17.6 -> 14.4; a ring of five or six stages was no faster: 21.7 and 15.6). With 256 rows and full precision it
+//    gains 3% where B is packed and costs 2% where it is not (8192 x 4096 x 4096 374 -> 361, 370 -> 377).
 //  - K is any multiple of 16 above 64 where B is row-major: the lanes whose 16 bytes of the last stage lie past K
 //    load the stage's first ones instead, and zero them once they have landed.
-//  - The lane's scales are loaded at a tile's start, and the next tile's first three stages are under way during a
-//    tile's epilogue, whose buffer is the ring's fourth slot and what lies behind it. (Its first phases wait for the
+//  - The lane's scales are loaded at a tile's start, and the next tile's first stages are under way during a
+//    tile's epilogue, whose buffer is the ring's last slot and what lies behind it. (Its first phases wait for the
 //    epilogue's stores, which the counter of outstanding accesses holds with the loads. Waits that left the known
 //    number of a whole tile's stores outstanding gained 0.5 to 1%, and cost the loop its registers.)
 template <int SK, bool GR, bool PKB, bool EX, int GATE, int BM>
@@ -241,9 +245,9 @@ __global__ __launch_bounds__(512, 1) void k_gated_pp(GemmParams p) {
       }
     }
   };
-  // the loads of stage s
-  auto issue = [&](int64_t s) {
-    const uint32_t slot = lds0 + (uint32_t)((s & (NS - 1)) * STAGE) + part_lds;
+  // the loads of stage s into a slot of the ring
+  auto issue = [&](int64_t s, int at) {
+    const uint32_t slot = lds0 + (uint32_t)(at * STAGE) + part_lds;
     const uint8_t* bk = base + s * sstride;
     const uint32_t back = !PKB && past && s == nk - 1 ? (uint32_t)ld_c : 0u;
 #pragma unroll
@@ -251,14 +255,14 @@ __global__ __launch_bounds__(512, 1) void k_gated_pp(GemmParams p) {
       if (d < DA || grp != 0) dma16(bk, off[d] - back, slot + (uint32_t)(d * 1024));
   };
   auto prologue = [&]() {
-    issue(0);
-    issue(1);
-    if (nk >= 3) issue(2);
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s)
+      if (s < 2 || s < nk) issue(s, s);
   };
   v8i fa[MI], fb[NI];
-  auto read = [&](int64_t s) {
+  auto read = [&](int at) {
     // slot offset opaque per call: the addresses are formed per read, not precomputed for all slots
-    uint32_t so = (uint32_t)((s & (NS - 1)) * STAGE);
+    uint32_t so = (uint32_t)(at * STAGE);
     asm volatile("" : "+s"(so));
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -328,34 +332,31 @@ __global__ __launch_bounds__(512, 1) void k_gated_pp(GemmParams p) {
     }
     __builtin_amdgcn_s_setprio(0);
   };
-  // waits until at most two stages of this wave's loads (or one) are outstanding, then for the barrier
-  auto wait_two = [&]() {
-    if (DA != DB && grp == 0) wait_vm_lgkm_and_barrier<2 * DA>();
-    else wait_vm_lgkm_and_barrier<2 * DB>();
-  };
-  auto wait_one = [&]() {
-    if (DA != DB && grp == 0) wait_vm_lgkm_and_barrier<DA>();
-    else wait_vm_lgkm_and_barrier<DB>();
-  };
-  // this wave's loads of stage u + 1 have landed: those of u + 2 and u + 3 may stay in flight
-  auto wait_next = [&](int64_t u) {
-    if (u + 3 < nk) {
-      wait_two();
-    } else if (u + 2 < nk) {
-      wait_one();
+  // waits until at most `stages` stages of this wave's loads are outstanding, then for the barrier
+  auto wait_but = [&](int64_t stages) {
+    if (stages >= 2) {
+      if (DA != DB && grp == 0) wait_vm_lgkm_and_barrier<2 * DA>();
+      else wait_vm_lgkm_and_barrier<2 * DB>();
+    } else if (stages == 1) {
+      if (DA != DB && grp == 0) wait_vm_lgkm_and_barrier<DA>();
+      else wait_vm_lgkm_and_barrier<DB>();
     } else {
-      if (!PKB && tail != 0 && u + 2 == nk) {
-        // this wave's loads of the last stage have landed, and nobody reads it before the barrier
-        wait_vm<0>();
-        if (past) {
-          uint8_t* at = lds + (int)((nk - 1) & (NS - 1)) * STAGE + part_lds + 16 * lane;
-#pragma unroll
-          for (int d = 0; d < DB; ++d)
-            if (d < DA || grp != 0) *reinterpret_cast<uint4*>(at + d * 1024) = make_uint4(0, 0, 0, 0);
-        }
-      }
       wait_vm_lgkm_and_barrier<0>();
     }
+  };
+  // this wave's loads of stage u + 1 have landed: later ones, up to stage u + NS - 1, may stay in flight
+  auto wait_next = [&](int64_t u, int last) {
+    if (!PKB && tail != 0 && u + 2 == nk) {
+      // this wave's loads of the last stage have landed, and nobody reads it before the barrier
+      wait_vm<0>();
+      if (past) {
+        uint8_t* at = lds + last * STAGE + part_lds + 16 * lane;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+          if (d < DA || grp != 0) *reinterpret_cast<uint4*>(at + d * 1024) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    wait_but(nk - 2 - u);
   };
 
   aim(t_begin);
@@ -375,8 +376,7 @@ __global__ __launch_bounds__(512, 1) void k_gated_pp(GemmParams p) {
 #pragma unroll
       for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[i][j]));
     // stage 0 has landed
-    if (nk >= 3) wait_two();
-    else wait_one();
+    wait_but(nk - 1);
     // the lane's scales, for the epilogue (the next two waits take them for loads of a stage: stricter, by
     // loads that have long landed)
     float rs[MI], cs;
@@ -397,15 +397,31 @@ __global__ __launch_bounds__(512, 1) void k_gated_pp(GemmParams p) {
     asm volatile("s_nop 1" ::: "memory");
     // both groups run the same loop, group 1 one phase behind
     if (grp == 1) wait_vm_lgkm_and_barrier<63>();
-    for (int64_t u = 0; u < nk; ++u) {
-      read(u);
-      if (u + 3 < nk) issue(u + 3);
-      predecode();
-      wait_next(u);
+    // slots of stage u and of the last one issued
+    int rd = 0, last = (int)(nk < NS ? nk - 1 : NS - 2);
+    auto products = [&]() {
       __builtin_amdgcn_sched_barrier(0);
+      // no vector instruction right before the products, in any order of the blocks
+      asm volatile("s_nop 1" ::: "memory");
       mma();
       __builtin_amdgcn_sched_barrier(0);
       asm volatile("s_barrier" ::: "memory");
+      rd = rd + 1 == NS ? 0 : rd + 1;
+    };
+    int64_t u = 0;
+    for (; u + NS - 1 < nk; ++u) {  // loads under way all the time
+      read(rd);
+      last = rd == 0 ? NS - 1 : rd - 1;
+      issue(u + NS - 1, last);
+      predecode();
+      wait_but(NS - 2);
+      products();
+    }
+    for (; u < nk; ++u) {
+      read(rd);
+      predecode();
+      wait_next(u, last);
+      products();
     }
     if (grp == 0) asm volatile("s_barrier" ::: "memory");
     // the ring is idle: every wave passed the last barrier. The scales are waited for here, with nothing else
