@@ -245,12 +245,12 @@ hipError_t launch_few(const GatedMmArgs& g) {
 //   rounds over the CUs x (2 us + K x the time for 1024 of K),
 // with times from measurements of one full round each (us for 1024 of K; the last with full precision):
 //   k_gated_few, 64 rows x 16 features, two a CU         3.6
-//   tiles of 64 x 128 features                           7.4 (10.8): a stage's loads bound it, not its products
-//   tiles of 128 x 128 features                          9.3 (12.9)
-//   tiles of 256 x 128 features, up to half of the CUs  10.5 (16.6); all of them 13.5 (22)
-// Measured, k_gated_few / 64 / 128 / 256 rows, us: 256 x 2048 x 2048 11.8 / 17.1 / 19.4 / 23.4; 1024 x 1040 x 720
-// 18.3 / 12.1 / 14.0 / 30.9; 1024 x 2048 x 2048 - / 19.0 / 20.7 / 24.6; 256 x 14336 x 4096 - / 60.3 / 44.4 / 51.4;
-// 2048 x 4096 x 4096 - / 117 / 77.6 / 59.2. An expert's rows are taken as the mean, and half a tile more.
+//   tiles of 64 x 128 features                           4.2 (8.2): a stage's loads bound it, not its products
+//   tiles of 128 x 128 features                          6.8 (12.9)
+//   tiles of 256 x 128 features, up to half of the CUs   9.6 (15.5); all of them 12.6 (22)
+// Measured, k_gated_few / 64 / 128 / 256 rows, us: 256 x 2048 x 2048 11.9 / 12.6 / 15.0 / 23.1; 1024 x 1040 x 720
+// 18.1 / 11.0 / 12.9 / 30.0; 1024 x 2048 x 2048 38.0 / 14.4 / 16.3 / 24.1; 256 x 14336 x 4096 124 / 53.9 / 43.4 /
+// 51.3; 2048 x 4096 x 4096 269 / 100 / 69.5 / 56.5. An expert's rows are taken as the mean, and half a tile more.
 int tile_rows(const GatedMmArgs& g) {
   const double cus = device_cus(), k = (double)g.K / 1024.0;
   if (!g.offsets && g.M <= 32) return 0;
@@ -270,10 +270,10 @@ int tile_rows(const GatedMmArgs& g) {
         mt = (mt < 1.0 ? 1.0 : mt) * g.E;
       }
       const double tiles = mt * nt;
-      const double c = bm == 64    ? (g.exact ? 10.8 : 7.4)
-                       : bm == 128 ? (g.exact ? 12.9 : 9.3)
-                       : 2.0 * tiles <= cus ? (g.exact ? 16.6 : 10.5)
-                                            : (g.exact ? 22.0 : 13.5);
+      const double c = bm == 64    ? (g.exact ? 8.2 : 4.2)
+                       : bm == 128 ? (g.exact ? 12.9 : 6.8)
+                       : 2.0 * tiles <= cus ? (g.exact ? 15.5 : 9.6)
+                                            : (g.exact ? 22.0 : 12.6);
       const double t = std::ceil(tiles / cus) * (2.0 + c * k);
       if (t < best) best = t, rows = bm;
     }
