@@ -24,7 +24,8 @@ class AdamW(torch.optim.Optimizer):
       in grad_norm, a tensor of one element. If it is not finite, the step changes nothing and is not counted.
       step(grad_scale=s) multiplies the gradients by s first, to undo a loss scale.
     capturable: count steps on the device, so that step() can be captured into a graph. A captured step keeps the
-      rate it was captured with unless lr is an fp32 tensor of one element on the device.
+      rate it was captured with unless lr is an fp32 tensor of one element on the device. The states have to be
+      there: one step is taken before.
 
     With max_norm or capturable all parameters are on one device and share one count of steps. Parameters must be
     contiguous; a gradient that is not is copied.
@@ -54,11 +55,15 @@ class AdamW(torch.optim.Optimizer):
 
     def add_param_group(self, group):
         super().add_param_group(group)
+        error = None
         for p in self.param_groups[-1]["params"]:
             if p.dtype not in (torch.bfloat16, torch.float32):
-                raise TypeError(f"AdamW: parameters must be bfloat16 or float32 (got {p.dtype})")
-            if not p.is_contiguous():
-                raise ValueError("AdamW: parameters must be contiguous")
+                error = TypeError(f"AdamW: parameters must be bfloat16 or float32 (got {p.dtype})")
+            elif not p.is_contiguous():
+                error = ValueError("AdamW: parameters must be contiguous")
+        if error is not None:
+            self.param_groups.pop()
+            raise error
 
     def __getstate__(self):  # the base class keeps its own three attributes only
         own = ("state_bits", "master_weights", "capturable", "seed", "max_norm", "grad_norm", "_mul")
@@ -115,6 +120,9 @@ class AdamW(torch.optim.Optimizer):
         load()
         if grad_scale != 1.0 and self.max_norm is None:
             raise ValueError("AdamW: grad_scale needs max_norm (infinity for no clipping)")
+        capturing = torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+        if capturing and not self._counts_on_device:
+            raise RuntimeError("AdamW: a step is captured only with capturable=True: the graph would keep its number")
         work, grads = {}, []
         for gi, group in enumerate(self.param_groups):
             for p in group["params"]:
@@ -123,6 +131,8 @@ class AdamW(torch.optim.Optimizer):
                 if p.grad.is_sparse:
                     raise RuntimeError("AdamW: sparse gradients are not supported")
                 if "exp_avg" not in self.state[p]:
+                    if capturing:  # each replay would begin with states of zero
+                        raise RuntimeError("AdamW: take a step before the captured one, which cannot make states")
                     self._new_state(p)
                 st, g = self.state[p], p.grad if p.grad.is_contiguous() else p.grad.contiguous()
                 grads.append(g)

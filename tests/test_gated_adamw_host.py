@@ -290,6 +290,30 @@ def test_optimizer_copies():
     b.step()
 
 
+def test_optimizer_refuses_capture_without_states(monkeypatch):
+    from fp8_dynamic_scaling_amd.optim import AdamW
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    p = _bf16(4)
+    p.grad = torch.zeros_like(p)
+    with pytest.raises(RuntimeError, match="capturable=True"):
+        AdamW([p]).step()
+    opt = AdamW([p], capturable=True)
+    with pytest.raises(RuntimeError, match="take a step before"):
+        opt.step()
+    assert "exp_avg" not in opt.state[p]
+
+
+def test_optimizer_drops_a_refused_group():
+    from fp8_dynamic_scaling_amd.optim import AdamW
+    opt = AdamW([_bf16(4)])
+    with pytest.raises(TypeError, match="bfloat16 or float32"):
+        opt.add_param_group(dict(params=[torch.nn.Parameter(torch.zeros(4, dtype=torch.float16))]))
+    with pytest.raises(ValueError, match="contiguous"):
+        opt.add_param_group(dict(params=[torch.nn.Parameter(torch.zeros(4, 3, dtype=torch.bfloat16).t())]))
+    assert len(opt.param_groups) == 1
+
+
 def test_binding_refuses_shapes():
     bf = dict(dtype=torch.bfloat16)
     x, q = torch.zeros(4, 48, **bf), torch.zeros(4, 128, dtype=torch.uint8)
