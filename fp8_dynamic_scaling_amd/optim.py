@@ -92,6 +92,8 @@ class AdamW(torch.optim.Optimizer):
             st["step"] = 0
 
     def load_state_dict(self, state_dict):
+        if any(("exp_avg_scale" in s) != (self.state_bits == 8) for s in state_dict["state"].values()):
+            raise ValueError(f"AdamW: states of another kind than state_bits={self.state_bits}")
         super().load_state_dict(state_dict)
         # the base class casts states to the parameter's type, which would round moments and spoil codes
         old = [i for g in state_dict["param_groups"] for i in g["params"]]
@@ -103,6 +105,8 @@ class AdamW(torch.optim.Optimizer):
             self.state[p] = {k: v.detach().to(p.device, copy=True) if torch.is_tensor(v) else v
                              for k, v in state_dict["state"][i].items()}
             st = self.state[p]
+            if self.master_weights and p.dtype == torch.bfloat16 and "master" not in st:
+                st["master"] = p.detach().float().reshape(-1)
             if self._counts_on_device:  # one count for all
                 if step is None:
                     t = st["step"]

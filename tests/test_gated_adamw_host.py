@@ -304,6 +304,22 @@ def test_optimizer_refuses_capture_without_states(monkeypatch):
     assert "exp_avg" not in opt.state[p]
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_optimizer_loads_its_own_kind_of_state(bits):
+    from fp8_dynamic_scaling_amd.optim import AdamW
+    make = lambda bits, **kw: AdamW([_bf16(5, 7)], state_bits=bits, **kw)  # noqa: E731
+    a, other, kept = make(bits), make(40 - bits), make(bits, master_weights=True)
+    a._new_state(a.param_groups[0]["params"][0])
+    with pytest.raises(ValueError, match="states of"):
+        other.load_state_dict(a.state_dict())
+    assert not other.state
+    p = kept.param_groups[0]["params"][0]
+    with torch.no_grad():
+        p.fill_(0.5)
+    kept.load_state_dict(a.state_dict())  # saved without fp32 copies: they are made of the parameters
+    assert torch.equal(kept.state[p]["master"], torch.full((35,), 0.5))
+
+
 def test_optimizer_drops_a_refused_group():
     from fp8_dynamic_scaling_amd.optim import AdamW
     opt = AdamW([_bf16(4)])
