@@ -707,7 +707,7 @@ static fp8_status resolve_e4m3(fp8_format fmt) {
 }
 
 static fp8_status run_gated(const GatedMmArgs& g) {
-  if (g.K == 0) {  // no contraction terms: act(0) * 0
+  if (g.K == 0 && !g.offsets) {  // no contraction terms: act(0) * 0
     const fp8_status st = dev_err(launch_zero_fill(g.out, g.M * g.F * 2, g.stream));
     return st != FP8_OK || !g.gu ? st : dev_err(launch_zero_fill(g.gu, g.M * g.F * 4, g.stream));
   }

@@ -316,6 +316,15 @@ hipError_t launch_generic(const GatedMmArgs& g) {
   return hipGetLastError();
 }
 
+// Grouped products of K = 0: act(0) * 0 in the experts' rows; those behind stay. end: offsets[E].
+__global__ void k_gated_zero(const int32_t* end, int64_t M, int64_t F, uint16_t* out, uint16_t* gu) {
+  const int64_t last = *end, n = (last < 0 ? 0 : last < M ? last : M) * F;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    out[i] = 0;
+    if (gu) gu[2 * i] = gu[2 * i + 1] = 0;
+  }
+}
+
 template <int GATE, int SK, bool EX>
 hipError_t launch_form(const GatedMmArgs& g) {
   const int rows = tile_rows(g);
@@ -339,6 +348,12 @@ hipError_t launch_act(const GatedMmArgs& g) {
 bool gated_mm_packed_ok(const GatedMmArgs& g) { return fast_eligible(g); }
 
 hipError_t launch_gated_mm(const GatedMmArgs& g) {
+  if (g.K == 0) {
+    const int64_t grid = std::min<int64_t>((g.M * g.F + 255) / 256, 8 * (int64_t)device_cus());
+    hipLaunchKernelGGL(k_gated_zero, dim3((unsigned)grid), dim3(256), 0, g.stream, g.offsets + g.E, g.M, g.F, g.out,
+                       g.gu);
+    return hipGetLastError();
+  }
   return g.gelu ? launch_act<kGateGelu>(g) : launch_act<kGateSilu>(g);
 }
 

@@ -140,6 +140,23 @@ def test_gated_mm_empty_sum():
     assert (out == 0).all() and (gu == 0).all()
 
 
+@pytest.mark.parametrize("offsets", [(0, 2, 2, 4), (0, 0, 0, 0), (0, 0, 7, 7)])
+def test_grouped_gated_mm_empty_sum(offsets):
+    """No terms: zeros in the experts' rows, and nothing behind them."""
+    f = lib()
+    M, F, E = 7, 5, len(offsets) - 1
+    out = torch.full((M, F), 7.5, dtype=torch.bfloat16, device="cuda")
+    gu = torch.full((M, 2 * F), 7.5, dtype=torch.bfloat16, device="cuda")
+    a = torch.empty((M, 0), dtype=torch.uint8, device="cuda")
+    b = torch.empty((E, 2 * F, 0), dtype=torch.uint8, device="cuda")
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    for g in (gu, None):
+        f.fp8_grouped_gated_mm(a, b, f.E4M3_NATIVE, None, None, off, f.ACT_SILU, g, out)
+        n = offsets[-1]
+        assert (out[:n] == 0).all() and (out[n:] == 7.5).all()
+        assert (gu[:n] == 0).all() and (gu[n:] == 7.5).all()
+
+
 def test_gated_mm_large_gates():
     """Gates far out on both sides: act goes to 0 and to the gate, without overflow of the exponential."""
     f = lib()
