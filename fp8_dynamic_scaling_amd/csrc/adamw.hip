@@ -22,11 +22,12 @@
 // The step is bound by HBM: 28 bytes an element with 32-bit states and an fp32 copy, 10.1 with
 // 8-bit states and bf16 parameters; the tensors' table travels in the kernel's arguments, so that
 // nothing is copied to the device first. Measured, 176 M elements in five tensors: 32-bit 790 to
-// 805 us (6.1 to 6.2 TB/s; a large torch copy reaches 5.3), 8-bit 314 us (5.7 TB/s; to nearest
-// 290). Loads and stores stream (non-temporal): plain loads 879 and 328 us, plain stores of the
+// 808 us (6.1 to 6.2 TB/s; a large torch copy reaches 5.3), 8-bit 314 to 323 us (5.5 to 5.7 TB/s; to
+// nearest 290). Loads and stores stream (non-temporal): plain loads 879 and 328 us, plain stores of the
 // 8-bit form 326. The 8-bit step had been bound by its instructions: 377 us with codes scaled and
 // rounded by integer steps and the library's square root, 343 with the scaled converts and a root
-// of seven instructions (below), 315 with two pieces a workgroup, the second's loads ahead.
+// of seven instructions (below), 315 with two pieces a workgroup, the second's loads ahead. Sending what
+// that root does not cover to the library's costs 1% (319.5 against 323 us, in turn).
 // Held to six waves a SIMD it spills: 392.
 #include <cmath>
 #include <type_traits>
@@ -223,13 +224,27 @@ __device__ __forceinline__ void decode8(uint2 c, uint32_t e8, float* x) {
   x[4] = d[0], x[5] = d[1], x[6] = e[0], x[7] = e[1];
 }
 
-// sqrt(v), correctly rounded for v >= 2^-100 (compared with the library's root for every mantissa, at both
-// parities of the exponent); zero below, where the remainder would lose bits. Seven instructions for the 15
-// of the root that covers everything.
+// sqrt(v), correctly rounded for 0 and v in [2^-100, infinity) (compared with the library's root for every mantissa,
+// at both parities of the exponent); what lies outside is far(). Seven instructions for the 15 of the root that covers
+// everything.
 __device__ __forceinline__ float root(float v) {
-  const float y = __builtin_amdgcn_rsqf(v), g = v * y;
-  const float r = __builtin_fmaf(__builtin_fmaf(-g, g, v), 0.5f * y, g);
-  return v < 0x1p-100f ? 0.0f : r;
+  const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f)), g = v * y;
+  return __builtin_fmaf(__builtin_fmaf(-g, g, v), 0.5f * y, g);
+}
+
+// Some v is infinite or in (0, 2^-100), where root()'s remainder would lose bits: as integers, v - 1 of zero is above
+// all others.
+template <int V>
+__device__ __forceinline__ bool far(const float* v) {
+  uint32_t lo = ~0u;
+  float hi = 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const uint32_t b = __float_as_uint(v[j]) - 1u;
+    lo = b < lo ? b : lo;
+    hi = fmaxf(hi, v[j]);
+  }
+  return lo < __builtin_bit_cast(uint32_t, 0x1p-100f) - 1u || hi > 3.402823466e38f;
 }
 
 // the largest of a group's 32 magnitudes as bits (those of a NaN are above all others): a lane
@@ -357,8 +372,15 @@ __global__ __launch_bounds__(256) void k_adamw(const StepArgs a) {
         m[j] = m[j] * a.b1 + x * a.c1;
         v[j] = v[j] * a.b2 + (x * x) * a.c2m;
         r[j] = EIGHT ? root(v[j]) : sqrtf(v[j]);
-        p[j] = cur.p[j] * decay - (m[j] * __builtin_amdgcn_rcpf(r[j] * c2 + a.eps)) * step;
       }
+      if constexpr (EIGHT)
+        if (far<V>(v)) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) r[j] = sqrtf(v[j]);
+        }
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        p[j] = cur.p[j] * decay - (m[j] * __builtin_amdgcn_rcpf(r[j] * c2 + a.eps)) * step;
       uint32_t lo[V], hi[V];
       if constexpr (SR) {
 #pragma unroll

@@ -1,0 +1,82 @@
+"""The AdamW step at the ends of its range: roots of subnormal numbers, and moments that overflow (GPU)."""
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_util import lib
+from tests.test_gpu_adamw import B1, B2, EPS, F32, LR, WD, check, host, make, step
+
+pytestmark = pytest.mark.gpu
+
+
+def far_gradients(n, seed):
+    """Groups of 32 of magnitudes 10^-24 to 10^-12 (squares down to fp32's last subnormal numbers and zero), every
+    third one with magnitudes up to 10^18 among them."""
+    g = torch.Generator().manual_seed(seed)
+    e = torch.rand(n, generator=g) * 12 - 24
+    large = (torch.arange(n) // 32 % 3 == 1) & (torch.rand(n, generator=g) < 0.5)
+    e = torch.where(large, torch.rand(n, generator=g) * 28 - 10, e)
+    return (torch.randint(0, 2, (n,), generator=g) * 2 - 1) * 10.0 ** e
+
+
+@pytest.mark.parametrize("p16,master", [(False, False), (True, True)])
+@pytest.mark.parametrize("mx8", [True, False])
+@pytest.mark.parametrize("seed", [0, (3 << 32) + 5])
+def test_adamw_far_second_moments(p16, master, mx8, seed):
+    """Codes and scales bit for bit over three steps from zeroed states, the second and third with smaller gradients,
+    so that the squares of small roots are subnormal too."""
+    f = lib()
+    s = make([96, 4099, 70001], p16, False, master, mx8)
+    for k in ("m", "v", "ms", "vs"):
+        for t in s[k] or ():
+            t.zero_()
+    for t in (1, 2, 3):
+        for i, g in enumerate(s["grads"]):
+            g.copy_(far_gradients(g.numel(), 10 * t + i) * 4.0 ** (1 - t))
+        before = host(s)
+        step(f, s, t, seed)
+        check(f, before, s, t, seed, None, p16, master, mx8)
+
+
+@pytest.mark.parametrize("mx8", [True, False])
+def test_adamw_small_gradients_take_a_whole_first_step(mx8):
+    """Without epsilon a first step moves by the rate, whatever the gradient's size. Relative error: two roundings of m,
+    three of v (halved by the root), one each of the root, its factor, their product, the quotient, the step and the
+    update, and two of the reciprocal (1 ulp): 11.5 of 2^-24."""
+    f = lib()
+    n = 4096
+    # squares times 1 - b2 from 5e-36 on: normal numbers, so that each rounding is 2^-24
+    g = (10.0 ** torch.linspace(-17, 2, n)).cuda()
+    g[1::2] *= -1
+    p = torch.zeros(n, device="cuda")
+    kind = dict(dtype=torch.uint8 if mx8 else torch.float32, device="cuda")
+    m, v = torch.zeros(n, **kind), torch.zeros(n, **kind)
+    ms, vs = (torch.zeros(n // 32, dtype=torch.uint8, device="cuda") for _ in range(2))
+    scales = dict(exp_avg_scales=[ms], exp_avg_sq_scales=[vs]) if mx8 else {}
+    f.fp8_adamw([p], [g], [m], [v], LR, B1, B2, 0.0, 0.0, 1, **scales)
+    want = -LR * g.sign().double()
+    assert ((p.double() - want).abs() <= 12 * 2.0 ** -24 * LR).all()
+    if mx8:
+        assert (v != 0).all()  # a code above zero for each root above zero
+
+
+@pytest.mark.parametrize("mx8", [True, False])
+def test_adamw_second_moment_that_overflows(mx8):
+    """A finite gradient whose square is infinite: the root is infinite and the update 0, beside the decay."""
+    f = lib()
+    s = make([100], False, False, False, mx8)
+    ref = make([100], False, False, False, mx8)
+    s["grads"][0][37], s["grads"][0][70] = 1e20, -3e38
+    step(f, s, 1)
+    step(f, ref, 1)
+    p, before = s["params"][0].cpu().numpy(), make([100], False, False, False, mx8)["params"][0].cpu().numpy()
+    for i in (37, 70):
+        assert p[i] == before[i] * F32(1.0 - LR * WD)
+    others = [i for i in range(100) if i not in (37, 70)]
+    assert np.array_equal(p[others], ref["params"][0].cpu().numpy()[others])
+    if mx8:
+        assert s["vs"][0].tolist()[1:3] == [255, 255] and (s["v"][0][32:96] == 0x7F).all()
+        assert (s["ms"][0] != 255).all()
+    else:
+        assert torch.isinf(s["v"][0][[37, 70]]).all() and torch.isfinite(s["m"][0]).all()
+    assert EPS > 0
