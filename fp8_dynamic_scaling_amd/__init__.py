@@ -793,8 +793,8 @@ def fp8_grad_norm_ws_bytes(grads) -> int:
 
 def fp8_grad_norm(grads, norm, mul, ws, grad_scale=1.0, max_norm=float("inf"), step=None, stream=None):
     """The 2-norm of a list of bf16 and fp32 tensors into norm [1], and into mul [1] the factor that clips them to
-    max_norm (fp8_adamw's grad_mul; NaN where the norm is not finite); step [1] int32 is increased by one where
-    it is finite. norm, mul and step may be None."""
+    max_norm (fp8_adamw's grad_mul; NaN where the norm or the factor is not finite); step [1] int32 is increased by
+    one where both are. norm, mul and step may be None."""
     import torch
     fn = "fp8_grad_norm"
     table, count, dev = _grad_table(fn, grads)

@@ -496,9 +496,11 @@ __device__ __forceinline__ void finish_norm(double s, const NormOut& o) {
   const double x = sqrt(s) * o.grad_scale;
   const float xf = (float)x;
   if (o.norm) *o.norm = xf;
-  const bool fine = fabsf(xf) <= 3.402823466e38f;  // not for NaN
   const double clip = o.max_norm / (x + 1e-6);
-  if (o.mul) *o.mul = fine ? (float)(clip < 1.0 ? o.grad_scale * clip : o.grad_scale) : __uint_as_float(0x7fc00000u);
+  const float mul = (float)(clip < 1.0 ? o.grad_scale * clip : o.grad_scale);
+  // the steps that k_adamw takes and no other are counted: not those of a NaN, nor of a factor past fp32
+  const bool fine = fabsf(xf) <= 3.402823466e38f && fabsf(mul) <= 3.402823466e38f;
+  if (o.mul) *o.mul = fine ? mul : __uint_as_float(0x7fc00000u);
   if (o.step && fine) *o.step += 1;
 }
 

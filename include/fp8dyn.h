@@ -648,8 +648,8 @@ typedef struct fp8_grad_tensor {
 
 /* norm = grad_scale * sqrt(sum of squares of all elements), summed in 64 bits in a fixed order;
  * mul = grad_scale * min(1, max_norm / (norm + 1e-6)), the factor that fp8_adamw takes: NaN if the
- * norm is not finite, which skips that step; *step is increased by one if it is finite. norm, mul
- * [1] fp32 and step [1] int32 on the device, each may be NULL. grad_scale (what undoes a loss
+ * norm or the factor is not finite in fp32, which skips that step; *step is increased by one if both
+ * are. norm, mul [1] fp32 and step [1] int32 on the device, each may be NULL. grad_scale (what undoes a loss
  * scale; 1 for none) finite and > 0; max_norm > 0, infinity for no clipping. ws:
  * fp8_grad_norm_ws_bytes() bytes (0 for small tables), 8-byte aligned, content on entry of no matter;
  * calls that may run at the same time need one each. count = 0 is the norm 0. */

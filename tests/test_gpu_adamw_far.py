@@ -1,10 +1,11 @@
-"""The AdamW step at the ends of its range: roots of subnormal numbers, and moments that overflow (GPU)."""
+"""The AdamW step and the norm at the ends of their ranges: roots of subnormal numbers, moments and factors that
+overflow (GPU)."""
 import numpy as np
 import pytest
 import torch
 
 from tests.gpu_util import lib
-from tests.test_gpu_adamw import B1, B2, EPS, F32, LR, WD, check, host, make, step
+from tests.test_gpu_adamw import B1, B2, F32, LR, WD, check, host, make, step
 
 pytestmark = pytest.mark.gpu
 
@@ -79,4 +80,20 @@ def test_adamw_second_moment_that_overflows(mx8):
         assert (s["ms"][0] != 255).all()
     else:
         assert torch.isinf(s["v"][0][[37, 70]]).all() and torch.isfinite(s["m"][0]).all()
-    assert EPS > 0
+
+
+def test_grad_norm_factor_that_overflows():
+    """A factor past fp32 makes the step change nothing, and it is not counted either."""
+    f = lib()
+    g = torch.full((100,), 1e-30, device="cuda")
+    norm, mul = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+    t = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for grads in ([g], [g] * 70):  # one launch and two
+        ws = torch.empty(f.fp8_grad_norm_ws_bytes(grads), dtype=torch.uint8, device="cuda")
+        f.fp8_grad_norm(grads, norm, mul, ws, grad_scale=1e39, step=t)
+        want = 1e39 * float(g[0].double()) * (100 * len(grads)) ** 0.5
+        assert abs(float(norm) - want) <= 2.0 ** -23 * want
+        assert torch.isnan(mul).all() and int(t) == 0
+        f.fp8_grad_norm(grads, norm, mul, ws, grad_scale=1e39, max_norm=1.0, step=t)  # clipped to a factor of 1e29
+        assert abs(float(mul) * want / 1e39 - 1) <= 2.0 ** -23 and int(t) == 1
+        t.zero_()
