@@ -92,7 +92,7 @@ class AdamW(torch.optim.Optimizer):
             st["step"] = 0
 
     def load_state_dict(self, state_dict):
-        if any(("exp_avg_scale" in s) != (self.state_bits == 8) for s in state_dict["state"].values()):
+        if any(s and ("exp_avg_scale" in s) != (self.state_bits == 8) for s in state_dict["state"].values()):
             raise ValueError(f"AdamW: states of another kind than state_bits={self.state_bits}")
         super().load_state_dict(state_dict)
         # the base class casts states to the parameter's type, which would round moments and spoil codes
@@ -100,7 +100,8 @@ class AdamW(torch.optim.Optimizer):
         new = [p for g in self.param_groups for p in g["params"]]
         step = None
         for i, p in zip(old, new):
-            if i not in state_dict["state"]:
+            if not state_dict["state"].get(i):  # no entry, or one that holds nothing
+                self.state.pop(p, None)
                 continue
             self.state[p] = {k: v.detach().to(p.device, copy=True) if torch.is_tensor(v) else v
                              for k, v in state_dict["state"][i].items()}
@@ -134,7 +135,7 @@ class AdamW(torch.optim.Optimizer):
                     continue
                 if p.grad.is_sparse:
                     raise RuntimeError("AdamW: sparse gradients are not supported")
-                if "exp_avg" not in self.state[p]:
+                if "exp_avg" not in self.state.get(p, ()):  # reading self.state[p] would make an entry
                     if capturing:  # each replay would begin with states of zero
                         raise RuntimeError("AdamW: take a step before the captured one, which cannot make states")
                     self._new_state(p)

@@ -1,0 +1,49 @@
+"""optim.AdamW on the host (CPU only): states that are loaded, and what a refused call leaves."""
+import pytest
+import torch
+
+from fp8_dynamic_scaling_amd.optim import AdamW
+
+
+def _param(*shape, dtype=torch.bfloat16):
+    return torch.nn.Parameter(torch.zeros(shape, dtype=dtype))
+
+
+def _stepped(counts, bits=32, **kw):
+    """An optimizer over vectors that have taken `counts` steps."""
+    ps = [_param(40 + i) for i in range(len(counts))]
+    opt = AdamW(ps, state_bits=bits, **kw)
+    for p, n in zip(ps, counts):
+        opt._new_state(p)
+        opt.state[p]["step"] = n
+    return opt
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("kw", [dict(capturable=True), dict(max_norm=1.0)])
+def test_refused_capture_leaves_no_state(monkeypatch, bits, kw):
+    p = _param(4)
+    p.grad = torch.zeros_like(p)
+    opt = AdamW([p], state_bits=bits, **kw)
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "is_initialized", lambda: True)
+        m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        with pytest.raises(RuntimeError, match="take a step before"):
+            opt.step()
+    assert p not in opt.state
+    saved = opt.state_dict()
+    assert saved["state"] == {}
+    AdamW([_param(4)], state_bits=bits, **kw).load_state_dict(saved)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("kw", [{}, dict(max_norm=1.0)])
+def test_loads_past_empty_entries(bits, kw):
+    """A parameter whose entry holds nothing has no states, as one without an entry."""
+    opt = _stepped([3, 3], bits)
+    saved = opt.state_dict()
+    saved["state"][1] = {}
+    new = AdamW([_param(40), _param(41)], state_bits=bits, **kw)
+    new.load_state_dict(saved)
+    p, q = new.param_groups[0]["params"]
+    assert int(new.state[p]["step"]) == 3 and q not in new.state
