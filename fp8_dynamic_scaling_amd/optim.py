@@ -94,6 +94,10 @@ class AdamW(torch.optim.Optimizer):
     def load_state_dict(self, state_dict):
         if any(s and ("exp_avg_scale" in s) != (self.state_bits == 8) for s in state_dict["state"].values()):
             raise ValueError(f"AdamW: states of another kind than state_bits={self.state_bits}")
+        counts = {int(s["step"]) for s in state_dict["state"].values() if s}
+        if self._counts_on_device and len(counts) > 1:
+            raise ValueError("AdamW: max_norm and capturable share one count of steps, the saved counts of steps are "
+                             f"{sorted(counts)}")
         super().load_state_dict(state_dict)
         # the base class casts states to the parameter's type, which would round moments and spoil codes
         old = [i for g in state_dict["param_groups"] for i in g["params"]]

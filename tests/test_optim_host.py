@@ -1,4 +1,6 @@
 """optim.AdamW on the host (CPU only): states that are loaded, and what a refused call leaves."""
+import copy
+
 import pytest
 import torch
 
@@ -47,3 +49,16 @@ def test_loads_past_empty_entries(bits, kw):
     new.load_state_dict(saved)
     p, q = new.param_groups[0]["params"]
     assert int(new.state[p]["step"]) == 3 and q not in new.state
+
+
+@pytest.mark.parametrize("kw", [dict(max_norm=1.0), dict(capturable=True)])
+def test_refuses_counts_that_differ(kw):
+    """With one count on the device two saved ones cannot both go on; without it each keeps its own."""
+    saved = _stepped([100, 3]).state_dict()
+    shared = AdamW([_param(40), _param(41)], **kw)
+    with pytest.raises(ValueError, match="counts of steps"):
+        shared.load_state_dict(copy.deepcopy(saved))
+    assert not shared.state
+    own = AdamW([_param(40), _param(41)])
+    own.load_state_dict(saved)
+    assert [own.state[p]["step"] for p in own.param_groups[0]["params"]] == [100, 3]
