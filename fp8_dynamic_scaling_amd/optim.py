@@ -92,33 +92,56 @@ class AdamW(torch.optim.Optimizer):
             st["step"] = 0
 
     def load_state_dict(self, state_dict):
-        if any(s and ("exp_avg_scale" in s) != (self.state_bits == 8) for s in state_dict["state"].values()):
+        """States of this optimizer or, with state_bits=32, of torch.optim.AdamW. What is refused changes nothing."""
+        states = state_dict["state"]
+        if any(s and ("exp_avg_scale" in s) != (self.state_bits == 8) for s in states.values()):
             raise ValueError(f"AdamW: states of another kind than state_bits={self.state_bits}")
-        counts = {int(s["step"]) for s in state_dict["state"].values() if s}
+        old = [i for g in state_dict["param_groups"] for i in g["params"]]
+        new = [p for g in self.param_groups for p in g["params"]]
+        for i, p in zip(old, new):
+            if states.get(i):
+                self._check_state(states[i], p.numel())
+        counts = {int(s["step"]) for s in states.values() if s}
         if self._counts_on_device and len(counts) > 1:
             raise ValueError("AdamW: max_norm and capturable share one count of steps, the saved counts of steps are "
                              f"{sorted(counts)}")
         super().load_state_dict(state_dict)
         # the base class casts states to the parameter's type, which would round moments and spoil codes
-        old = [i for g in state_dict["param_groups"] for i in g["params"]]
-        new = [p for g in self.param_groups for p in g["params"]]
         step = None
         for i, p in zip(old, new):
-            if not state_dict["state"].get(i):  # no entry, or one that holds nothing
+            if not states.get(i):  # no entry, or one that holds nothing
                 self.state.pop(p, None)
                 continue
-            self.state[p] = {k: v.detach().to(p.device, copy=True) if torch.is_tensor(v) else v
-                             for k, v in state_dict["state"][i].items()}
-            st = self.state[p]
+            st = self.state[p] = {}
+            for k, v in states[i].items():
+                if torch.is_tensor(v) and k != "step":
+                    v = v.detach().to(p.device, copy=True)
+                    # torch.optim.AdamW's moments have the parameter's shape and type
+                    if k == "master" or (k in ("exp_avg", "exp_avg_sq") and self.state_bits == 32):
+                        v = v.float().reshape(-1)
+                st[k] = v
             if self.master_weights and p.dtype == torch.bfloat16 and "master" not in st:
                 st["master"] = p.detach().float().reshape(-1)
+            st["step"] = int(st["step"])
             if self._counts_on_device:  # one count for all
                 if step is None:
-                    t = st["step"]
-                    step = t if torch.is_tensor(t) else torch.full((1,), t, dtype=torch.int32, device=p.device)
+                    step = torch.full((1,), st["step"], dtype=torch.int32, device=p.device)
                 st["step"] = step
-            elif torch.is_tensor(st["step"]):
-                st["step"] = int(st["step"])
+
+    def _check_state(self, st, n):
+        eight = self.state_bits == 8
+        sizes = {"exp_avg": n, "exp_avg_sq": n, "step": 1}
+        if eight:
+            sizes.update(exp_avg_scale=-(-n // 32), exp_avg_sq_scale=-(-n // 32))
+        if "master" in st:
+            sizes["master"] = n
+        for k, want in sizes.items():
+            v = st.get(k)
+            got = v.numel() if torch.is_tensor(v) else 1 if k == "step" and v is not None else None
+            if got != want:
+                raise ValueError(f"AdamW: a saved {k} has {got or 'no'} elements where {want} are wanted")
+            if eight and k not in ("step", "master") and v.dtype.itemsize != 1:
+                raise ValueError(f"AdamW: a saved {k} is {v.dtype} where codes are wanted")
 
     @torch.no_grad()
     def step(self, closure=None, grad_scale: float = 1.0):

@@ -62,3 +62,43 @@ def test_refuses_counts_that_differ(kw):
     own = AdamW([_param(40), _param(41)])
     own.load_state_dict(saved)
     assert [own.state[p]["step"] for p in own.param_groups[0]["params"]] == [100, 3]
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_refuses_states_of_other_sizes(bits):
+    saved = _stepped([1, 1], bits).state_dict()
+    for name, n in (("exp_avg", 39), ("exp_avg_sq", 0)) + ((("exp_avg_scale", 1),) if bits == 8 else ()):
+        bad = copy.deepcopy(saved)
+        bad["state"][0][name] = bad["state"][0][name][:n]
+        new = AdamW([_param(40), _param(41)], state_bits=bits)
+        with pytest.raises(ValueError, match=name):
+            new.load_state_dict(bad)
+        assert not new.state
+    del saved["state"][1]["exp_avg"]
+    with pytest.raises(ValueError, match="exp_avg"):
+        AdamW([_param(40), _param(41)], state_bits=bits).load_state_dict(saved)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kw", [{}, dict(max_norm=1.0), dict(capturable=True)])
+def test_loads_torchs_states(dtype, kw):
+    """torch.optim.AdamW keeps moments of the parameter's shape and type and an fp32 count."""
+    ps = [_param(5, 7, dtype=dtype), _param(3, dtype=dtype)]
+    ref = torch.optim.AdamW(ps, lr=1e-2)
+    for t in range(3):
+        for p in ps:
+            p.grad = torch.full_like(p, 0.01 * (t + 1))
+        ref.step()
+    new = AdamW([_param(5, 7, dtype=dtype), _param(3, dtype=dtype)], **kw)
+    new.load_state_dict(ref.state_dict())
+    steps = []
+    for p, q in zip(ps, new.param_groups[0]["params"]):
+        st = new.state[q]
+        for k in ("exp_avg", "exp_avg_sq"):
+            assert st[k].dtype == torch.float32 and torch.equal(st[k], ref.state[p][k].float().reshape(-1))
+        steps.append(st["step"])
+    if kw:
+        assert steps[0] is steps[1] and steps[0].dtype == torch.int32 and steps[0].tolist() == [3]
+    else:
+        assert steps == [3, 3] and all(isinstance(s, int) for s in steps)
+    assert new.param_groups[0]["lr"] == 1e-2
