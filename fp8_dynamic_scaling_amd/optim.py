@@ -96,6 +96,9 @@ class AdamW(torch.optim.Optimizer):
         states = state_dict["state"]
         if any(s and ("exp_avg_scale" in s) != (self.state_bits == 8) for s in states.values()):
             raise ValueError(f"AdamW: states of another kind than state_bits={self.state_bits}")
+        for variant in ("amsgrad", "maximize"):
+            if any(g.get(variant) for g in state_dict["param_groups"]):
+                raise ValueError(f"AdamW: the states of a run with {variant} cannot go on without it")
         old = [i for g in state_dict["param_groups"] for i in g["params"]]
         new = [p for g in self.param_groups for p in g["params"]]
         for i, p in zip(old, new):

@@ -102,3 +102,15 @@ def test_loads_torchs_states(dtype, kw):
     else:
         assert steps == [3, 3] and all(isinstance(s, int) for s in steps)
     assert new.param_groups[0]["lr"] == 1e-2
+
+
+@pytest.mark.parametrize("other", [dict(amsgrad=True), dict(maximize=True)])
+def test_refuses_torchs_variants(other):
+    p = _param(4)
+    p.grad = torch.ones_like(p)
+    ref = torch.optim.AdamW([p], **other)
+    ref.step()
+    new = AdamW([_param(4)])
+    with pytest.raises(ValueError, match=next(iter(other))):
+        new.load_state_dict(ref.state_dict())
+    assert not new.state
