@@ -6,6 +6,8 @@ A step is one launch for each 48 tensors of a kind. Nothing is read back to the 
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import fp8_adamw, fp8_grad_norm, fp8_grad_norm_ws_bytes, load
@@ -146,6 +148,20 @@ class AdamW(torch.optim.Optimizer):
             if eight and k not in ("step", "master") and v.dtype.itemsize != 1:
                 raise ValueError(f"AdamW: a saved {k} is {v.dtype} where codes are wanted")
 
+    @staticmethod
+    def _check_group(group, dev):
+        lr = group["lr"]
+        if isinstance(lr, torch.Tensor):
+            if lr.device != dev or lr.dtype != torch.float32:
+                raise ValueError("AdamW: a tensor lr must be float32 and on the parameters' device")
+            lr = 0.0
+        if not all(0 <= x < math.inf for x in (lr, group["eps"], group["weight_decay"])):
+            raise ValueError("AdamW: lr, eps and weight_decay must be finite and not negative")
+        if not all(0 <= b < 1 for b in group["betas"]):
+            raise ValueError(f"AdamW: betas must be in [0, 1) (got {group['betas']})")
+        if dev.type != "cuda":
+            raise ValueError(f"AdamW: parameters must be on the GPU (got {dev})")
+
     @torch.no_grad()
     def step(self, closure=None, grad_scale: float = 1.0):
         loss = None
@@ -175,6 +191,8 @@ class AdamW(torch.optim.Optimizer):
                 work.setdefault((gi, p.device, p.dtype, g.dtype, "master" in st, t), []).append((p, g, st))
         if not work:
             return loss
+        for gi, dev, *_ in work:  # before the count moves or a part of the parameters
+            self._check_group(self.param_groups[gi], dev)
         mul = step_dev = None
         if self._counts_on_device:
             devices = {k[1] for k in work}
@@ -197,8 +215,6 @@ class AdamW(torch.optim.Optimizer):
             group = self.param_groups[gi]
             lr, (b1, b2) = group["lr"], group["betas"]
             on_dev = isinstance(lr, torch.Tensor)
-            if on_dev and (lr.device != dev or lr.dtype != torch.float32):
-                raise ValueError("AdamW: a tensor lr must be float32 and on the parameters' device")
             col = lambda k: [st[k] for _, _, st in items]  # noqa: E731
             scales = self.state_bits == 8
             # another seed for each call of a step: tensors of two calls have the same places

@@ -114,3 +114,20 @@ def test_refuses_torchs_variants(other):
     with pytest.raises(ValueError, match=next(iter(other))):
         new.load_state_dict(ref.state_dict())
     assert not new.state
+
+
+@pytest.mark.parametrize("bad", [dict(lr=-1.0), dict(lr=float("inf")), dict(betas=(0.9, 1.0)), dict(eps=float("nan")),
+                                 dict(weight_decay=-0.1), dict(lr=torch.ones(1, dtype=torch.float64)), {}])
+def test_refused_step_is_not_counted(bad):
+    """A value that a scheduler or the user has spoiled (or, at last, parameters that are not on the GPU) is refused
+    before the count of steps moves."""
+    ps = [_param(4), _param(5)]
+    opt = AdamW([dict(params=ps[:1]), dict(params=ps[1:])], capturable=True)
+    for p in ps:
+        p.grad = torch.ones_like(p)
+        opt._new_state(p)
+    opt.param_groups[1].update(bad)
+    with pytest.raises(ValueError):
+        opt.step()
+    assert int(opt.state[ps[0]]["step"]) == 0
+    assert all((p == 0).all() for p in ps)
