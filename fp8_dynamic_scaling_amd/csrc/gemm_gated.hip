@@ -12,19 +12,14 @@
 //    16 tokens 25.
 //  - k_gemm_fp8 (gemm_generic.hpp): grouped products of K up to 64 or weights past 32-bit offsets.
 #include <algorithm>
-#include <cmath>
 
+#include "gated_tiles.hpp"
 #include "gemm_gated_pp.hpp"
 #include "gemm_generic.hpp"
 
 namespace fp8dyn {
 
 namespace {
-
-// two stages at least, and 32-bit offsets within a tile of A, in B and in the output
-bool fast_eligible(const GatedMmArgs& g) {
-  return g.K > 64 && 2 * g.F <= (1 << 22) && g.K <= (1 << 22) && 2 * g.F * g.K < ((int64_t)1 << 31);
-}
 
 // ---------------------------------------------------------------------------
 // Few rows (and small products): one pass over the weights, straight from memory to registers.
@@ -241,46 +236,6 @@ hipError_t launch_few(const GatedMmArgs& g) {
   return hipSuccess;
 }
 
-// Rows of a workgroup's tile in the ping-pong kernel, or 0 for k_gated_few: the least of what each would take,
-//   rounds over the CUs x (2 us + K x the time for 1024 of K),
-// with times from measurements of one full round each (us for 1024 of K; the last with full precision):
-//   k_gated_few, 64 rows x 16 features, two a CU         3.6
-//   tiles of 64 x 128 features                           4.2 (8.2): a stage's loads bound it, not its products
-//   tiles of 128 x 128 features                          6.8 (12.9)
-//   tiles of 256 x 128 features, up to half of the CUs   9.6 (15.5); all of them 12.6 (22)
-// Measured, k_gated_few / 64 / 128 / 256 rows, us: 256 x 2048 x 2048 11.9 / 12.6 / 15.0 / 23.1; 1024 x 1040 x 720
-// 18.1 / 11.0 / 12.9 / 30.0; 1024 x 2048 x 2048 38.0 / 14.4 / 16.3 / 24.1; 256 x 14336 x 4096 124 / 53.9 / 43.4 /
-// 51.3; 2048 x 4096 x 4096 269 / 100 / 69.5 / 56.5. An expert's rows are taken as the mean, and half a tile more.
-int tile_rows(const GatedMmArgs& g) {
-  const double cus = device_cus(), k = (double)g.K / 1024.0;
-  if (!g.offsets && g.M <= 32) return 0;
-  const double nt = (double)((g.F + 127) / 128);
-  double best = 1e300;
-  int rows = 256;
-  if (!g.offsets) {
-    const double wgs = (double)((g.F + 15) / 16) * (double)((g.M + 63) / 64);
-    best = std::ceil(wgs / (2.0 * cus)) * (2.0 + 3.6 * k);
-    rows = 0;
-  }
-  if (g.packed || fast_eligible(g)) {
-    for (const int bm : {64, 128, 256}) {
-      double mt = (double)((g.M + bm - 1) / bm);
-      if (g.offsets) {
-        mt = (double)g.M / g.E / bm + 0.5;
-        mt = (mt < 1.0 ? 1.0 : mt) * g.E;
-      }
-      const double tiles = mt * nt;
-      const double c = bm == 64    ? (g.exact ? 8.2 : 4.2)
-                       : bm == 128 ? (g.exact ? 12.9 : 6.8)
-                       : 2.0 * tiles <= cus ? (g.exact ? 15.5 : 9.6)
-                                            : (g.exact ? 22.0 : 12.6);
-      const double t = std::ceil(tiles / cus) * (2.0 + c * k);
-      if (t < best) best = t, rows = bm;
-    }
-  }
-  return rows;
-}
-
 template <int GATE, int SK, bool GR, bool PKB, bool EX, int BM>
 hipError_t launch_pp_rows(const GatedMmArgs& g) {
   GemmParams p{g.a, g.b, g.sa, g.sb, g.offsets, g.E, g.M, 2 * g.F, g.K, g.out, g.gu};
@@ -327,10 +282,10 @@ __global__ void k_gated_zero(const int32_t* end, int64_t M, int64_t F, uint16_t*
 
 template <int GATE, int SK, bool EX>
 hipError_t launch_form(const GatedMmArgs& g) {
-  const int rows = tile_rows(g);
-  if (rows == 0) return launch_few<GATE, SK>(g);
+  const int rows = gated_tile_rows(g.M, g.F, g.K, g.offsets ? g.E : 0, g.packed, g.exact, device_cus());
+  if (rows == kGatedFew) return launch_few<GATE, SK>(g);
   if constexpr (SK == kScaleRow) {
-    if (!g.packed && !fast_eligible(g)) return launch_generic<GATE, EX>(g);
+    if (rows == kGatedGeneric) return launch_generic<GATE, EX>(g);
     if (g.offsets)
       return g.packed ? launch_pp<GATE, SK, true, true, EX>(g, rows) : launch_pp<GATE, SK, true, false, EX>(g, rows);
   }
@@ -345,7 +300,7 @@ hipError_t launch_act(const GatedMmArgs& g) {
 
 }  // namespace
 
-bool gated_mm_packed_ok(const GatedMmArgs& g) { return fast_eligible(g); }
+bool gated_mm_packed_ok(const GatedMmArgs& g) { return gated_fast_eligible(g.F, g.K); }
 
 hipError_t launch_gated_mm(const GatedMmArgs& g) {
   if (g.K == 0) {
