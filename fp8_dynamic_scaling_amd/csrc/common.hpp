@@ -228,4 +228,11 @@ inline int device_cus() {
   return cus;
 }
 
+// Orders a wavefront's LDS reads behind its writes, and its next writes behind those reads, where lanes read what other
+// lanes of the wavefront wrote. LDS serves a wavefront in order, so that this is for the compiler: no instruction.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 }  // namespace fp8dyn

@@ -95,8 +95,6 @@ __global__ __launch_bounds__(64 * WV) void k_gated_few(GemmParams p) {
 #pragma unroll
       for (int j = 0; j < 2 * MT; ++j) b.a[j] &= in;
     }
-    // a wave's LDS instructions take effect in order: the reads below see these stores, and the next unit's
-    // stores come behind them
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int row = PKB ? 16 * (j >> 1) + (lane >> 2) : 8 * j + lr;
@@ -105,6 +103,7 @@ __global__ __launch_bounds__(64 * WV) void k_gated_few(GemmParams p) {
     }
 #pragma unroll
     for (int j = 0; j < 2 * MT; ++j) *reinterpret_cast<u32x4*>(mine + (32 + 8 * j + lr) * STRIDE + 16 * lp) = b.a[j];
+    wave_lds_fence();
     v8bf wb[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -132,6 +131,7 @@ __global__ __launch_bounds__(64 * WV) void k_gated_few(GemmParams p) {
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) asm volatile("" ::"v"(wb[h][0]), "v"(wb[h][1]), "v"(wb[h][2]), "v"(wb[h][3]));
+    wave_lds_fence();  // the next unit's stores come behind these reads
   };
 #pragma unroll
   for (int d = 0; d < D; ++d)

@@ -28,7 +28,10 @@ __device__ __forceinline__ void gated_epilogue(const GemmParams& p, const TileIn
   const int lrow = lane & 31, lg = lane >> 5, grp = wave >> 2, wn = wave & 3;
   const int row0 = grp * 32 * MI, f0 = wn * 32;
   float* s_cs = reinterpret_cast<float*>(lds + kGatedBuf) + wave * 64;
-  if constexpr (ROW) s_cs[lane] = cs;  // read by this wave alone
+  if constexpr (ROW) {
+    s_cs[lane] = cs;  // read by this wave alone
+    wave_lds_fence();
+  }
   const int32_t m_lim = (int32_t)(ti.m_end - ti.m0) - row0, f_lim = (int32_t)(F - ti.n0);
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + (ti.m0 + row0) * F + ti.n0;
   uint16_t* gu = p.gu ? p.gu + (ti.m0 + row0) * 2 * F + ti.n0 : nullptr;

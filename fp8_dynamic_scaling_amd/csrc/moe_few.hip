@@ -111,12 +111,6 @@ __device__ __forceinline__ v8bf decode8(uint32_t d0, uint32_t d1) {
 // The wavefront's number, known to be the same in all of its lanes.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// Orders a wavefront's LDS reads behind its writes (LDS serves a wavefront in order).
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // ---- one unit's operands --------------------------------------------------------
 //
 // A unit is the values [128 u, 128 u + 128) of the contraction, of length K; the
