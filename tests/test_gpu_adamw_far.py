@@ -1,5 +1,5 @@
 """The AdamW step and the norm at the ends of their ranges: roots of subnormal numbers, moments and factors that
-overflow (GPU)."""
+overflow, tables whose workgroups take two pieces (GPU)."""
 import numpy as np
 import pytest
 import torch
@@ -80,6 +80,31 @@ def test_adamw_second_moment_that_overflows(mx8):
         assert (s["ms"][0] != 255).all()
     else:
         assert torch.isinf(s["v"][0][[37, 70]]).all() and torch.isfinite(s["m"][0]).all()
+
+
+@pytest.mark.parametrize("p16,g16,master", [(True, True, False), (True, False, True), (False, False, False)])
+@pytest.mark.parametrize("seed", [0, (5 << 32) + 77])
+def test_adamw_large_table(p16, g16, master, seed):
+    """A table past 2^24 elements, whose workgroups take two pieces: each tensor as when it is stepped alone, at its place
+    among empty ones (whose random bits go by the place), by workgroups of one."""
+    f = lib()
+    sizes = [1, 4096 * 1200 + 2047, 2048, 4096 * 700 + 2049, 33, 4096 * 900 + 1, 4097, 4096 * 1500 + 31, 0, 2047]
+    assert sum(sizes) >= 8192 * 2048 and max(sizes) < 8192 * 2048
+    s, ref = (make(sizes, p16, g16, master, False) for _ in range(2))
+    for t in (s, ref):
+        for k in "mv":
+            t[k] = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in sizes]
+            t[k + "s"] = [torch.zeros(-(-n // 32), dtype=torch.uint8, device="cuda") for n in sizes]
+    mul = torch.tensor([0.37], device="cuda")
+    for t in (1, 2):
+        step(f, s, t, seed, mul)
+        for i in range(len(sizes)):
+            one = {k: v and [x if j == i else x[:0] for j, x in enumerate(v)] for k, v in ref.items()}
+            step(f, one, t, seed, mul)
+        for k, v in s.items():
+            for i, (x, y) in enumerate(zip(v or (), ref[k] or ())):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), (t, k, i)
+    assert (s["v"][7] != 0).any()
 
 
 def test_grad_norm_factor_that_overflows():
