@@ -24,6 +24,13 @@ constexpr int kGatedFew = 0, kGatedGeneric = -1;
 // Measured, k_gated_few / 64 / 128 / 256 rows, us: 256 x 2048 x 2048 11.9 / 12.6 / 15.0 / 23.1; 1024 x 1040 x 720
 // 18.1 / 11.0 / 12.9 / 30.0; 1024 x 2048 x 2048 38.0 / 14.4 / 16.3 / 24.1; 256 x 14336 x 4096 124 / 53.9 / 43.4 /
 // 51.3; 2048 x 4096 x 4096 269 / 100 / 69.5 / 56.5. An expert's rows are taken as the mean, and half a tile more.
+// The times have no term for memory, and are too short where large weights bound a round (18.8 for 64 x 14336 x 4096).
+// What the rule takes is the fastest there too, but for the last (k_gated_few / 64 / 128 rows, packed): 33 x 14336 x 4096
+// 36.0 / 30.9 / 32.7; 64 x 14336 x 4096 39.2 / 35.8 / 37.9; 96 x 14336 x 4096 61.9 / 33.5 / 40.9; 64 x 8192 x 8192
+// 37.2 / 58.9 / 60.1; 64 x 4096 x 4096 15.0 / 28.5 / 30.0; 64 x 14336 x 4096 row-major 39.8 / 43.7 / 46.1.
+// Dense products that the ping-pong kernel does not take are k_gated_few's, which reads the weights once for each 64
+// rows: 1024 x 66000 x 16400 12.9 ms, as a grouped product of one expert, kGatedGeneric, 5.7; 8192 x 14336 x 64 703 and
+// 459 us.
 // experts: 0 for a dense product. Grouped products that the ping-pong kernel does not take are kGatedGeneric.
 inline int gated_tile_rows(int64_t M, int64_t F, int64_t K, int32_t experts, bool packed, bool exact, int cu_count) {
   const double cus = cu_count, k = (double)K / 1024.0;

@@ -6,11 +6,12 @@
 // themselves are written only for a backward: without them F values a row leave the kernel instead of 2F, and no
 // pass reads them again.
 //  - k_gated_pp (gemm_gated_pp.hpp): many rows, bound by the matrix cores. Measured, 8192 x 14336 x 4096: 717 to
-//    727 us (2.65 to 2.68 PFLOP/s; the library's plain FP8 product of the same size reaches 2.75), with both
-//    projections, 0.7 GB of stores in all, 777 to 785; full precision 1261 and 1303 us.
-//  - k_gated_few (below): few rows, bound by reading the weights. One token of 14336 x 4096: 20.5 us (5.7 TB/s),
-//    16 tokens 25.
+//    744 us (2.59 to 2.68 PFLOP/s; the library's plain FP8 product of the same size reaches 2.75), with both
+//    projections, 0.7 GB of stores in all, 758 to 816; full precision 1261 to 1302 and 1303 to 1350 us.
+//  - k_gated_few (below): few rows, bound by reading the weights. One token of 14336 x 4096: 20.5 to 22 us (5.3 to
+//    5.7 TB/s), 16 tokens 25.
 //  - k_gemm_fp8 (gemm_generic.hpp): grouped products of K up to 64 or weights past 32-bit offsets.
+// gated_tiles.hpp has the rule that chooses.
 #include <algorithm>
 
 #include "gated_tiles.hpp"
