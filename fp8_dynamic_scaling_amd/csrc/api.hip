@@ -779,6 +779,8 @@ fp8_status fp8_adamw(const fp8_adamw_tensor* tensors, int32_t count, fp8_out par
   if ((!lr_dev && bad_factor(lr)) || bad_factor(beta1) || bad_factor(beta2) || bad_factor(eps) ||
       bad_factor(weight_decay) || beta1 >= 1.0 || beta2 >= 1.0 || (!step_dev && step < 1))
     return FP8_ERR_INVALID_ARGUMENT;
+  // the reciprocal takes a divisor that is subnormal for zero: elements without gradients would become NaN
+  if (eps > 0.0 && eps < 0x1p-126) return FP8_ERR_INVALID_ARGUMENT;
   if (!aligned(grad_mul, 4) || !aligned(step_dev, 4) || !aligned(lr_dev, 4)) return FP8_ERR_ALIGNMENT;
   const bool mx = state == FP8_STATE_MX8;
   const size_t ps = param_type == FP8_OUT_F32 ? 4 : 2, gs = grad_type == FP8_OUT_F32 ? 4 : 2, ss = mx ? 1 : 4;

@@ -46,6 +46,8 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError(f"betas must be two numbers in [0, 1) (got {betas})")
         if not eps >= 0 or not weight_decay >= 0:
             raise ValueError("eps and weight_decay must not be negative")
+        if 0 < eps < 2.0 ** -126:
+            raise ValueError(f"eps must be 0 or a normal fp32 number (got {eps})")
         if max_norm is not None and not max_norm > 0:
             raise ValueError(f"max_norm must be positive (got {max_norm})")
         if not 0 < seed < 1 << 63:
@@ -157,6 +159,8 @@ class AdamW(torch.optim.Optimizer):
             lr = 0.0
         if not all(0 <= x < math.inf for x in (lr, group["eps"], group["weight_decay"])):
             raise ValueError("AdamW: lr, eps and weight_decay must be finite and not negative")
+        if 0 < group["eps"] < 2.0 ** -126:
+            raise ValueError(f"AdamW: eps must be 0 or a normal fp32 number (got {group['eps']})")
         if not all(0 <= b < 1 for b in group["betas"]):
             raise ValueError(f"AdamW: betas must be in [0, 1) (got {group['betas']})")
         if dev.type != "cuda":

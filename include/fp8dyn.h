@@ -633,9 +633,9 @@ typedef enum {
  * grad_mul: device fp32, or NULL. If it is not finite, the call changes nothing.
  * step_dev, lr_dev: device int32 and fp32, or NULL: t and lr are read there when the kernels
  * run (for graphs); step and lr are then not used.
- * betas in [0, 1), eps, lr and weight_decay finite and >= 0, step >= 1 unless step_dev. Every
- * pointer aligned to its elements (else FP8_ERR_ALIGNMENT); 16-byte aligned ones are faster.
- * One launch for each 48 tensors. Tensors that overlap are not detected. */
+ * betas in [0, 1), eps, lr and weight_decay finite and >= 0, eps 0 or at least 2^-126, step >= 1
+ * unless step_dev. Every pointer aligned to its elements (else FP8_ERR_ALIGNMENT); 16-byte
+ * aligned ones are faster. One launch for each 48 tensors. Tensors that overlap are not detected. */
 FP8DYN_API fp8_status fp8_adamw(const fp8_adamw_tensor* tensors, int32_t count, fp8_out param_type,
                                 fp8_out grad_type, fp8_adamw_state state, double lr, double beta1, double beta2,
                                 double eps, double weight_decay, int64_t step, uint64_t seed, const float* grad_mul,

@@ -62,6 +62,20 @@ def test_adamw_small_gradients_take_a_whole_first_step(mx8):
 
 
 @pytest.mark.parametrize("mx8", [True, False])
+def test_adamw_smallest_epsilon(mx8):
+    """Elements without gradients stay, beside one that has one."""
+    f = lib()
+    p, g = torch.ones(64, device="cuda"), torch.zeros(64, device="cuda")
+    g[40] = 1e-3
+    kind = dict(dtype=torch.uint8 if mx8 else torch.float32, device="cuda")
+    ms, vs = (torch.zeros(2, dtype=torch.uint8, device="cuda") for _ in range(2))
+    scales = dict(exp_avg_scales=[ms], exp_avg_sq_scales=[vs]) if mx8 else {}
+    f.fp8_adamw([p], [g], [torch.zeros(64, **kind)], [torch.zeros(64, **kind)], LR, B1, B2, 2.0 ** -126, 0.0, 1, **scales)
+    still = torch.arange(64, device="cuda") != 40
+    assert (p[still] == 1).all() and abs(float(p[40]) - (1 - LR)) <= 2.0 ** -23
+
+
+@pytest.mark.parametrize("mx8", [True, False])
 def test_adamw_second_moment_that_overflows(mx8):
     """A finite gradient whose square is infinite: the root is infinite and the update 0, beside the decay."""
     f = lib()

@@ -4,7 +4,9 @@ import copy
 import pytest
 import torch
 
+import fp8_dynamic_scaling_amd as f
 from fp8_dynamic_scaling_amd.optim import AdamW
+from tests.test_gated_adamw_host import _adamw, lib  # noqa: F401
 
 
 def _param(*shape, dtype=torch.bfloat16):
@@ -116,7 +118,7 @@ def test_refuses_torchs_variants(other):
     assert not new.state
 
 
-@pytest.mark.parametrize("bad", [dict(lr=-1.0), dict(lr=float("inf")), dict(betas=(0.9, 1.0)), dict(eps=float("nan")),
+@pytest.mark.parametrize("bad", [dict(lr=-1.0), dict(lr=float("inf")), dict(betas=(0.9, 1.0)), dict(eps=float("nan")), dict(eps=1e-40),
                                  dict(weight_decay=-0.1), dict(lr=torch.ones(1, dtype=torch.float64)), {}])
 def test_refused_step_is_not_counted(bad):
     """A value that a scheduler or the user has spoiled (or, at last, parameters that are not on the GPU) is refused
@@ -131,3 +133,13 @@ def test_refused_step_is_not_counted(bad):
         opt.step()
     assert int(opt.state[ps[0]]["step"]) == 0
     assert all((p == 0).all() for p in ps)
+
+
+@pytest.mark.parametrize("eps,want", [(1e-40, f.ERR_INVALID_ARGUMENT), (2.0 ** -127, f.ERR_INVALID_ARGUMENT),
+                                      (1e-50, f.ERR_INVALID_ARGUMENT), (2.0 ** -126, f.OK), (0.0, f.OK)])
+def test_epsilon_below_fp32s_normal_numbers(lib, eps, want):  # noqa: F811
+    """The reciprocal takes it for zero, so that zero gradients would make NaN of their parameters."""
+    assert _adamw(lib, [], eps=eps) == want
+    if want != f.OK:
+        with pytest.raises(ValueError, match="eps"):
+            AdamW([_param(4)], eps=eps)
